@@ -337,6 +337,110 @@ int pa_decode_noalloc(void* out, const void* q, const void* k_cache, const void*
                       int32_t max_blocks_per_seq, const pa_cache_desc* cache, float scale, int32_t partition_size,
                       int32_t* err_flag, void* stream);
 
+/*
+ * pa_rope_frequencies - the angle per position of each rotary pair (host; no CUDA call).
+ *   Pair j < rotary_dim / 2 of a head turns by position * inv_freq[j] radians, inv_freq[j] =
+ *   base^(-2 j / rotary_dim), stretched for contexts longer than the trained one by `scaling`:
+ *     PA_ROPE_PLAIN   as is (scaling NULL is the same)
+ *     PA_ROPE_LINEAR  inv_freq / factor (positions interpolated)
+ *     PA_ROPE_NTK     base * factor^(r / (r - 2)), r = rotary_dim >= 4
+ *     PA_ROPE_YARN    inv_freq / factor * ramp_j + inv_freq * (1 - ramp_j), ramp_j = clamp((j - lo) / (hi - lo), 0, 1),
+ *                     lo = max(0, floor(d(beta_fast))), hi = min(r - 1, ceil(d(beta_slow))),
+ *                     d(n) = r ln(original_max_position / (2 pi n)) / (2 ln base), hi - lo at least 1e-3;
+ *                     *magnitude = attention_factor, or if that is 0: 0.1 ln(factor) + 1 (1 for factor <= 1)
+ *     PA_ROPE_BANDS   by the turns n_j = original_max_position * inv_freq / (2 pi) of the trained length:
+ *                     inv_freq / factor * (1 - keep_j) + inv_freq * keep_j,
+ *                     keep_j = clamp((n_j - low_freq_factor) / (high_freq_factor - low_freq_factor), 0, 1)
+ *   *magnitude is 1 except for PA_ROPE_YARN.  rotary_dim even, 2 .. 128; base, and the fields that the
+ *   method names, finite and > 0 (attention_factor >= 0, high_freq_factor > low_freq_factor).
+ */
+enum { PA_ROPE_PLAIN = 0, PA_ROPE_LINEAR = 1, PA_ROPE_NTK = 2, PA_ROPE_YARN = 3, PA_ROPE_BANDS = 4 };
+typedef struct {
+  int32_t method;               /* PA_ROPE_* */
+  double factor;
+  double original_max_position; /* YARN, BANDS */
+  double beta_fast, beta_slow;  /* YARN (usually 32, 1) */
+  double attention_factor;      /* YARN; 0: from factor */
+  double low_freq_factor, high_freq_factor; /* BANDS (usually 1, 4) */
+} pa_rope_scaling;
+
+int pa_rope_frequencies(double* inv_freq, float* magnitude, int32_t rotary_dim, double base,
+                        const pa_rope_scaling* scaling);
+
+/*
+ * pa_rope_and_cache - rotary positions applied to a step's new tokens, with their cache write, in one pass:
+ *   the first rotary_dim elements of every head of q and key are turned,
+ *     y_a = c x_a - s x_b,  y_b = c x_b + s x_a,  c = magnitude cos(a_j), s = magnitude sin(a_j),
+ *     a_j = positions[t] * inv_freq[j],
+ *   pairs (a, b) = (j, j + rotary_dim / 2), or (2j, 2j + 1) when `interleaved`; the other elements are copied.
+ *   Turned queries go to q_out; turned keys, and values as they are, go to the token's slot of the caches as
+ *   pa_reshape_and_cache / pa_reshape_and_cache_fp8 place them.  The angle is reduced to a fraction of a turn
+ *   exactly (any int32 position), the rest is fp32, and each element is rounded once: to dtype, or over an FP8
+ *   cache to the E4M3 code nearest to y / k_scale (x / v_scale), ties to even, saturating at +-448.
+ *
+ *   q, q_out     [num_tokens][num_q_heads][head_size] of dtype (fp16 for an FP8 cache); num_q_heads 0: no queries
+ *   key, value   [num_tokens][num_kv_heads][head_size] of the same type
+ *   *_stride     elements from one token to the next: at least the row of its heads, a multiple of 16 bytes
+ *                (views of a fused projection); all four pointers 16-byte aligned
+ *   q_out        q itself (same stride: in place), or apart from q, key and value
+ *   positions    int32 [num_tokens];  inv_freq  double [rotary_dim / 2] on the device, finite
+ *   slot_mapping int64 [num_tokens], distinct.  A negative slot marks a padding token: nothing of it is written,
+ *                its row of q_out included.  A slot outside the pool gives PA_DEVERR_SLOT, and that token is
+ *                skipped in the same way.
+ *   k_scale, v_scale  FP8 caches (> 0; 0 means 1).  magnitude finite.
+ *   The inputs may be pinned host memory mapped into the device's address space, as for the other appends.
+ */
+int pa_rope_and_cache(void* q_out, void* k_cache, void* v_cache, const void* q, const void* key, const void* value,
+                      int64_t q_out_stride, int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                      const int32_t* positions, const int64_t* slot_mapping, const double* inv_freq,
+                      int32_t num_tokens, int32_t num_q_heads, int32_t rotary_dim, int32_t interleaved,
+                      float magnitude, const pa_cache_desc* cache, float k_scale, float v_scale, int32_t* err_flag,
+                      void* stream);
+
+/*
+ * pa_decode_window - one decode step with a sliding window and first tokens that stay visible: pa_decode
+ *   where the query of sequence s, at position p = seq_lens[s] - 1, sees only the positions
+ *     i <= p  with  i > p - window  or  i < num_sinks.
+ *   A window no shorter than the sequence sees all of it.  Table entries of blocks that hold no visible
+ *   position are never read and their blocks never touched: they may have been released.  Other positions of
+ *   a block that holds a visible one are loaded and have no effect, whatever they contain.
+ *
+ *   key, value   both NULL, or the step's append as in pa_decode_append (f16, bf16, FP8 caches): each
+ *                sequence's new token is stored at position seq_lens[s] - 1 and attended in the same launch
+ *   seq_lens     0 writes a zero row (and appends nothing).  A length past the table, or a negative one, gives
+ *                PA_DEVERR_QUERY and nothing of that sequence is written.
+ *   window >= 1, num_sinks >= 0.  Types, head sizes, block sizes, alignments and options as for pa_decode_ex
+ *   (ALiBi slopes, FP8 scales, test_flags); caches, tables and lengths of any block size it takes.
+ *   One launch, no workspace: a window bounds an item's keys, which the CTAs of one cluster share.  Two calls
+ *   may overlap.  The kernel is a programmatic dependent of the one before it on `stream`; it reads nothing
+ *   before that one has finished.
+ */
+int pa_decode_window(void* out, const void* q, void* k_cache, void* v_cache, const void* key, const void* value,
+                     const int32_t* block_tables, const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads,
+                     int32_t max_blocks_per_seq, const pa_cache_desc* cache, float scale, int32_t window,
+                     int32_t num_sinks, int32_t* err_flag, void* stream, const pa_decode_options* options);
+
+/*
+ * pa_prefill_window - attention of a chunk of new tokens over the paged cache, with the window and first
+ *   tokens of pa_decode_window: query j of sequence s, at position p = L - n + j, sees the positions i <= p
+ *   with i > p - window or i < num_sinks.  The chunk's own K/V are in the cache already (pa_rope_and_cache,
+ *   pa_reshape_and_cache).  Chunks of one token (a decode step) to whole prompts, and any mixture of them.
+ *
+ *   out, q, query_start, seq_lens, max_query_len  as for pa_prefill; out rows outside every chunk are not
+ *                written.  A sequence whose chunk breaks the rules there is skipped (PA_DEVERR_QUERY).
+ *   Table entries of blocks without a position that some query of the chunk sees are never read (they may
+ *   have been released).  Value rows of positions that some queries of the chunk see and others do not must
+ *   be finite.
+ *   scale        finite and > 0;  window >= 1;  num_sinks >= 0
+ *   k_scale, v_scale  FP8 caches (> 0; 0 means 1): q and out are fp16
+ *   Every cache type, head size and block size of pa_decode.  No workspace.
+ */
+int pa_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                      const int32_t* seq_lens, const int32_t* query_start, int32_t num_seqs,
+                      int32_t num_query_tokens, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                      int32_t max_query_len, const pa_cache_desc* cache, float scale, int32_t window,
+                      int32_t num_sinks, float k_scale, float v_scale, int32_t* err_flag, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* pa_status_string(int status);
 

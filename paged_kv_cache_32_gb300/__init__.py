@@ -24,7 +24,8 @@ PA_DEVERR = {0: "none", 1: "block id out of range", 2: "slot out of range", 3: "
 
 EXPORTED = ("pa_decode", "pa_decode_ex", "pa_decode_append", "pa_decode_partition_size", "pa_decode_workspace_size",
             "pa_reshape_and_cache", "pa_copy_blocks", "pa_status_string", "pa_version", "pa_decode_noalloc", "pa_prefill",
-            "pa_reshape_and_cache_fp8")
+            "pa_reshape_and_cache_fp8", "pa_rope_frequencies", "pa_rope_and_cache", "pa_decode_window",
+            "pa_prefill_window")
 
 
 PA_DECODE_TEST_EXPIRE_FIRST_WAIT = 1
@@ -38,6 +39,15 @@ class pa_decode_options(ctypes.Structure):
 class pa_cache_desc(ctypes.Structure):
     _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_size", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN, PA_ROPE_BANDS = range(5)
+
+
+class pa_rope_scaling(ctypes.Structure):
+    _fields_ = [("method", ctypes.c_int32), ("factor", ctypes.c_double), ("original_max_position", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double), ("attention_factor", ctypes.c_double),
+                ("low_freq_factor", ctypes.c_double), ("high_freq_factor", ctypes.c_double)]
 
 
 class PaError(RuntimeError):
@@ -81,6 +91,18 @@ def lib() -> ctypes.CDLL:
         L.pa_reshape_and_cache_fp8.argtypes = [vp, vp, vp, vp, vp, i32, desc_p, ctypes.c_float, ctypes.c_float, vp, vp]
         L.pa_reshape_and_cache_fp8.restype = ctypes.c_int
         L.pa_copy_blocks.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        L.pa_rope_frequencies.argtypes = [vp, vp, i32, ctypes.c_double, ctypes.POINTER(pa_rope_scaling)]
+        L.pa_rope_frequencies.restype = ctypes.c_int
+        L.pa_rope_and_cache.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, i32, i32, i32, i32, f32,
+                                        desc_p, f32, f32, vp, vp]
+        L.pa_rope_and_cache.restype = ctypes.c_int
+        L.pa_decode_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, desc_p, f32, i32, i32, vp, vp,
+                                       ctypes.POINTER(pa_decode_options)]
+        L.pa_decode_window.restype = ctypes.c_int
+        L.pa_prefill_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, desc_p, f32, i32, i32, f32,
+                                        f32, vp, vp]
+        L.pa_prefill_window.restype = ctypes.c_int
         L.pa_status_string.argtypes = [ctypes.c_int]
         L.pa_status_string.restype = ctypes.c_char_p
         L.pa_version.argtypes = []
@@ -283,3 +305,192 @@ def pa_copy_blocks(k_cache, v_cache, block_pairs, err_flag=None, stream=None, de
     status = lib().pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(block_pairs), int(block_pairs.shape[0]),
                                   ctypes.byref(desc), _ptr(err_flag), _stream(stream))
     _check(status, "pa_copy_blocks")
+
+
+# ---------------------------------------------------------------- rotary positions and windowed attention
+def _call_checks(cache, tensors, where: str):
+    """The checks that the sliding-window calls make of their tensors: each (tensor, name, dtype) has that dtype and
+    lies on the caches' device, or in pinned host memory."""
+    dev = cache.device
+    if not cache.is_cuda:
+        raise ValueError(f"{where}: the caches must be CUDA tensors")
+    for t, name, dtype in tensors:
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+        if t.device != dev and not (t.device.type == "cpu" and t.is_pinned()):
+            raise ValueError(f"{where}: {name} is on {t.device}, the caches on {dev}")
+
+
+def _rows_dtype(cache):
+    """The type of queries, outputs and new rows for a cache: its own, fp16 for an FP8 cache."""
+    import torch
+    return torch.float16 if cache.element_size() == 1 else cache.dtype
+
+
+class _on_device:
+    """The stream to launch on, with the tensors' device current during the call."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _cache_checks(k_cache, v_cache, desc, where: str):
+    _dense(k_cache, "k_cache")
+    _dense(v_cache, "v_cache")
+    if v_cache.dtype != k_cache.dtype or v_cache.numel() != k_cache.numel() or v_cache.device != k_cache.device:
+        raise ValueError(f"{where}: k_cache and v_cache must match in type, size and device")
+    return desc or cache_desc(k_cache)
+
+
+def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, method: int = PA_ROPE_PLAIN, factor: float = 1.0,
+                        original_max_position: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                        attention_factor: float = 0.0, low_freq_factor: float = 1.0, high_freq_factor: float = 4.0,
+                        device=None):
+    """(inv_freq, magnitude): the angle per position of each of the rotary_dim / 2 pairs, as a float64 tensor
+    (on ``device``), and the factor on the turned elements.  ``method``: PA_ROPE_PLAIN, PA_ROPE_LINEAR,
+    PA_ROPE_NTK, PA_ROPE_YARN or PA_ROPE_BANDS, the ways to stretch the frequencies for contexts longer than the
+    trained one."""
+    import torch
+    inv = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64)
+    mag = ctypes.c_float(1.0)
+    s = pa_rope_scaling(int(method), factor, original_max_position, beta_fast, beta_slow, attention_factor,
+                        low_freq_factor, high_freq_factor)
+    if int(rotary_dim) > 128:
+        raise PaError(3, "pa_rope_frequencies")
+    _check(lib().pa_rope_frequencies(_ptr(inv), ctypes.addressof(mag), int(rotary_dim), float(base), ctypes.byref(s)),
+           "pa_rope_frequencies")
+    return (inv if device is None else inv.to(device)), mag.value
+
+
+def _token_stride(t, heads: int, d: int, name: str, where: str) -> int:
+    """Elements between the tokens of [tokens, heads, d]; a token's row is dense."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{where}: {name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
+        raise ValueError(f"{where}: the heads of one token of {name} must be dense")
+    return int(s[0]) if t.shape[0] > 1 else max(heads * d, 1)
+
+
+def pa_rope_and_cache(q_out, k_cache, v_cache, q, key, value, positions, slot_mapping, inv_freq,
+                      interleaved: bool = False, magnitude: float = 1.0, err_flag=None, stream=None,
+                      desc: pa_cache_desc | None = None, k_scale: float | None = None,
+                      v_scale: float | None = None) -> None:
+    """Turn the first 2 * len(inv_freq) elements of each head of q and key by positions * inv_freq, write the queries
+    to q_out and the keys and values to their cache slots.
+
+    q, q_out [num_tokens, num_q_heads, head_size] (both None: no queries), key, value [num_tokens, num_kv_heads,
+    head_size] of the cache's type (fp16 for an FP8 cache): a token's heads are dense, tokens may lie further apart
+    (views of a fused projection).  q_out may be q.  positions int32, slot_mapping int64 [num_tokens] (negative:
+    padding, nothing is written); inv_freq float64 on the device, magnitude: see pa_rope_frequencies.
+    ``interleaved``: pairs (2j, 2j + 1), else (j, j + rotary_dim / 2)."""
+    import torch
+    where = "pa_rope_and_cache"
+    desc = _cache_checks(k_cache, v_cache, desc, where)
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{where}: q and q_out go together")
+    rows = _rows_dtype(k_cache)
+    _call_checks(k_cache, ((q_out, "q_out", rows), (q, "q", rows), (key, "key", rows), (value, "value", rows),
+                           (positions, "positions", torch.int32), (slot_mapping, "slot_mapping", torch.int64),
+                           (inv_freq, "inv_freq", torch.float64), (err_flag, "err_flag", torch.int32)), where)
+    for t, n in ((positions, "positions"), (slot_mapping, "slot_mapping"), (inv_freq, "inv_freq")):
+        _dense(t, n)
+    d, hkv = desc.head_size, desc.num_kv_heads
+    tokens, hq = int(key.shape[0]), 0 if q is None else int(q.shape[1])
+    strides = [_token_stride(t, h, d, n, where) if t is not None else 0
+               for t, h, n in ((q_out, hq, "q_out"), (q, hq, "q"), (key, hkv, "key"), (value, hkv, "value"))]
+    for t, n in ((q_out, "q_out"), (q, "q"), (value, "value"), (positions, "positions"), (slot_mapping, "slot_mapping")):
+        if t is not None and t.shape[0] != tokens:
+            raise ValueError(f"{where}: {n} must hold {tokens} tokens")
+    with _on_device(k_cache.device, stream) as st:
+        status = lib().pa_rope_and_cache(_ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(q), _ptr(key), _ptr(value),
+                                         *strides, _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq), tokens, hq,
+                                         2 * inv_freq.numel(), int(bool(interleaved)), float(magnitude),
+                                         ctypes.byref(desc), float(k_scale or 0.0), float(v_scale or 0.0),
+                                         _ptr(err_flag), st)
+    _check(status, where)
+
+
+def _attention_checks(where, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc, *more):
+    import torch
+    desc = _cache_checks(k_cache, v_cache, desc, where)
+    rows = _rows_dtype(k_cache)
+    _call_checks(k_cache, ((out, "out", rows), (q, "q", rows), (block_tables, "block_tables", torch.int32),
+                           (seq_lens, "seq_lens", torch.int32), (err_flag, "err_flag", torch.int32)) + more, where)
+    for t, n in ((out, "out"), (q, "q"), (block_tables, "block_tables"), (seq_lens, "seq_lens")):
+        _dense(t, n)
+    if q.dim() != 3 or q.shape[2] != desc.head_size or out.shape != q.shape:
+        raise ValueError(f"{where}: q and out must be [queries, heads, {desc.head_size}]")
+    if block_tables.dim() != 2 or seq_lens.dim() != 1 or block_tables.shape[0] != seq_lens.shape[0]:
+        raise ValueError(f"{where}: block_tables must be [num_seqs, max_blocks_per_seq], seq_lens [num_seqs]")
+    return desc
+
+
+def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, window: int, num_sinks: int = 0,
+                     key=None, value=None, err_flag=None, stream=None, desc: pa_cache_desc | None = None,
+                     alibi_slopes=None, k_scale: float | None = None, v_scale: float | None = None,
+                     test_flags: int = 0) -> None:
+    """pa_decode where each sequence's query sees the last ``window`` positions and the first ``num_sinks``.
+
+    Table entries of blocks outside are never read (released blocks).  ``key`` / ``value`` [num_seqs, num_kv_heads,
+    head_size]: each sequence's new token, stored at position seq_lens[s] - 1 and attended in the same launch
+    (16-bit and FP8 caches).  No workspace."""
+    import torch
+    where = "pa_decode_window"
+    rows = _rows_dtype(k_cache)
+    desc = _attention_checks(where, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc,
+                             (key, "key", rows), (value, "value", rows), (alibi_slopes, "alibi_slopes", torch.float32))
+    num_seqs, num_q_heads = int(q.shape[0]), int(q.shape[1])
+    if seq_lens.shape[0] != num_seqs:
+        raise ValueError(f"{where}: one query per sequence")
+    for t, n in ((key, "key"), (value, "value")):
+        if t is not None and tuple(_dense(t, n).shape) != (num_seqs, desc.num_kv_heads, desc.head_size):
+            raise ValueError(f"{where}: {n} must be [{num_seqs}, {desc.num_kv_heads}, {desc.head_size}]")
+    if alibi_slopes is not None and _dense(alibi_slopes, "alibi_slopes").numel() != num_q_heads:
+        raise ValueError(f"{where}: one ALiBi slope per query head")
+    opts = None
+    if alibi_slopes is not None or k_scale is not None or v_scale is not None or test_flags:
+        opts = ctypes.byref(pa_decode_options(_ptr(alibi_slopes), float(k_scale or 0.0), float(v_scale or 0.0),
+                                              int(test_flags)))
+    with _on_device(k_cache.device, stream) as st:
+        status = lib().pa_decode_window(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(key), _ptr(value),
+                                        _ptr(block_tables), _ptr(seq_lens), num_seqs, num_q_heads,
+                                        int(block_tables.shape[1]), ctypes.byref(desc), float(scale), int(window),
+                                        int(num_sinks), _ptr(err_flag), st, opts)
+    _check(status, where)
+
+
+def pa_prefill_window(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_query_len: int, scale: float,
+                      window: int, num_sinks: int = 0, err_flag=None, stream=None, desc: pa_cache_desc | None = None,
+                      k_scale: float | None = None, v_scale: float | None = None) -> None:
+    """Attention of a chunk of new tokens with a sliding window: the queries q[query_start[s]:query_start[s + 1]] are
+    the last n_s of seq_lens[s] cached tokens; the one at position p sees the last ``window`` positions up to p and
+    the first ``num_sinks``.  Every cache type, head size and block size; arguments as for pa_prefill, ``k_scale`` /
+    ``v_scale`` the scales of an FP8 cache (q and out are fp16 then)."""
+    import torch
+    where = "pa_prefill_window"
+    desc = _attention_checks(where, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc,
+                             (query_start, "query_start", torch.int32))
+    num_seqs = int(seq_lens.shape[0])
+    if tuple(_dense(query_start, "query_start").shape) != (num_seqs + 1,):
+        raise ValueError(f"{where}: query_start must be [num_seqs + 1]")
+    with _on_device(k_cache.device, stream) as st:
+        status = lib().pa_prefill_window(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                                         _ptr(seq_lens), _ptr(query_start), num_seqs, int(q.shape[0]), int(q.shape[1]),
+                                         int(block_tables.shape[1]), int(max_query_len), ctypes.byref(desc),
+                                         float(scale), int(window), int(num_sinks), float(k_scale or 0.0),
+                                         float(v_scale or 0.0), _ptr(err_flag), st)
+    _check(status, where)

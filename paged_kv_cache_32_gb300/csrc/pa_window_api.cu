@@ -1,0 +1,178 @@
+// pa_window_api.cu - the C-ABI entry points of windowed attention: argument
+// validation, tensor maps, the choice of kernel and split.  Every host-side
+// check runs before any CUDA call, so an argument error launches nothing.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <math.h>
+
+#include "pa.h"
+#include "pa_window.h"
+
+using namespace pa::host;
+
+namespace {
+
+constexpr int kMaxCluster = 8;    // the portable cluster size
+constexpr int kFillCtas = 912;    // CTAs that fill 152 SMs with three resident CTAs twice
+constexpr int kMinCtaTokens = 128;  // tokens of a CTA below which a split no longer pays
+
+// CTAs that share one item's keys: doubled while the grid would leave SMs idle and each CTA keeps some slabs
+// for its four warps.
+int cluster_size(long long items, long long max_keys) {
+  int c = 1;
+  while (c < kMaxCluster && items * c < kFillCtas && max_keys / (2 * c) >= kMinCtaTokens) c *= 2;
+  return c;
+}
+
+// Checks that both entry points share.
+int check_window(const pa_cache_desc* cache, int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                 float scale, int32_t window, int32_t num_sinks) {
+  const int rc = check_cache(cache);
+  if (rc != PA_OK) return rc;
+  if (num_seqs < 0 || num_q_heads <= 0 || max_blocks_per_seq < 0) return PA_ERR_INVALID_ARG;
+  if (num_q_heads % cache->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (!(scale == scale) || isinf(scale)) return PA_ERR_INVALID_ARG;
+  if (window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+  if ((int64_t)max_blocks_per_seq * cache->block_size > kInt32Max) return PA_ERR_TOO_LARGE;
+  return PA_OK;
+}
+
+int check_scales(const pa_cache_desc* cache, float* k_scale, float* v_scale) {
+  if (*k_scale == 0.f) *k_scale = 1.f;
+  if (*v_scale == 0.f) *v_scale = 1.f;
+  if (cache->dtype != PA_FP8_E4M3) return PA_OK;
+  return *k_scale > 0.f && !isinf(*k_scale) && *v_scale > 0.f && !isinf(*v_scale) ? PA_OK : PA_ERR_INVALID_ARG;
+}
+
+// Launches the rows kernel of the cache's type; p.tiles (row groups) and p.cluster are set here.
+int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t stream) {
+  const long long rows = (long long)p.max_query_len * (p.num_q_heads / p.num_kv_heads);
+  if (rows > kInt32Max - 8) return PA_ERR_TOO_LARGE;
+  p.tiles = (int32_t)((rows + 7) / 8);
+  // keys that an item may see: its rows' windows, the first tokens, all within the table
+  const long long cap = (long long)p.max_blocks * p.block_size;
+  const long long reach = (long long)p.window + p.sinks + 8;
+  const long long items = pa::window_items(p);
+  p.cluster = cluster_size(items, reach < cap ? reach : cap);
+  if (items * p.cluster > kInt32Max) return PA_ERR_TOO_LARGE;
+  cudaError_t e;
+  if (cache->dtype == PA_F32) {
+    e = pa::launch_window_rows_f32(cache->head_size, p, stream);
+  } else if (cache->dtype == PA_FP8_E4M3) {
+    CUtensorMap tk, tk32;
+    if (!encode_fp8_key_map(&tk, p.k_cache, cache, pa::kTcSlabTokens) ||
+        !encode_fp8_key_map(&tk32, p.k_cache, cache, 2 * pa::kTcSlabTokens))
+      return PA_ERR_CUDA;
+    e = pa::launch_window_rows_fp8(tk, tk32, p, stream);
+  } else {
+    CUtensorMap tk, tv;
+    // a slab is one 16-row box, or (8-token blocks) two 8-row boxes from two blocks
+    const int box_rows = cache->block_size < pa::kTcSlabTokens ? cache->block_size : pa::kTcSlabTokens;
+    if (!encode_cache_map(&tk, p.k_cache, cache, box_rows) || !encode_cache_map(&tv, p.v_cache, cache, box_rows))
+      return PA_ERR_CUDA;
+    e = pa::launch_window_rows_tc(cache->dtype, cache->head_size, tk, tv, p, stream);
+  }
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa::WindowParams base_params(const pa_cache_desc* cache, void* out, const void* q, const void* k_cache,
+                             const void* v_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                             int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks, float scale, int32_t window,
+                             int32_t num_sinks, int32_t* err_flag) {
+  pa::WindowParams p = {};
+  p.out = out;
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.err_flag = err_flag;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.max_blocks = max_blocks;
+  p.block_size = cache->block_size;
+  p.num_blocks = cache->num_blocks;
+  p.num_query_tokens = num_seqs;
+  p.max_query_len = 1;
+  p.window = window;
+  p.sinks = num_sinks;
+  p.cluster = 1;
+  p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+  p.k_scale = p.v_scale = 1.f;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_decode_window(void* out, const void* q, void* k_cache, void* v_cache, const void* key, const void* value,
+                     const int32_t* block_tables, const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads,
+                     int32_t max_blocks_per_seq, const pa_cache_desc* cache, float scale, int32_t window,
+                     int32_t num_sinks, int32_t* err_flag, void* stream, const pa_decode_options* options) {
+  int rc = check_window(cache, num_seqs, num_q_heads, max_blocks_per_seq, scale, window, num_sinks);
+  if (rc != PA_OK) return rc;
+  if ((key == nullptr) != (value == nullptr)) return PA_ERR_NULL_POINTER;
+  if (key != nullptr && cache->dtype == PA_F32) return PA_ERR_UNSUPPORTED;  // the 16-bit and FP8 kernels append
+  float k_scale = options != nullptr ? options->k_scale : 0.f, v_scale = options != nullptr ? options->v_scale : 0.f;
+  rc = check_scales(cache, &k_scale, &v_scale);
+  if (rc != PA_OK) return rc;
+  if (num_seqs == 0) return PA_OK;
+  if (out == nullptr || q == nullptr || k_cache == nullptr || v_cache == nullptr || seq_lens == nullptr)
+    return PA_ERR_NULL_POINTER;
+  if (block_tables == nullptr && max_blocks_per_seq > 0) return PA_ERR_NULL_POINTER;
+  const uintptr_t qalign = cache->dtype == PA_F32 ? 4 : 16;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, qalign) || !aligned(out, 4) ||
+      !aligned(key, 16) || !aligned(value, 16) || !aligned(seq_lens, 4) || !aligned(block_tables, 4))
+    return PA_ERR_MISALIGNED;
+  const float* alibi = options != nullptr ? options->alibi_slopes : nullptr;
+  if (!aligned(alibi, 4)) return PA_ERR_MISALIGNED;
+  if ((int64_t)num_seqs * num_q_heads > kInt32Max) return PA_ERR_TOO_LARGE;
+
+  pa::WindowParams p = base_params(cache, out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_q_heads,
+                                   max_blocks_per_seq, scale, window, num_sinks, err_flag);
+  p.alibi = alibi;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.test_expire_first_wait =
+      (options != nullptr && (options->test_flags & PA_DECODE_TEST_EXPIRE_FIRST_WAIT) != 0u) ? 1 : 0;
+  p.new_k = key;
+  p.new_v = value;
+  p.k_cache_out = k_cache;
+  p.v_cache_out = v_cache;
+  return launch_rows(cache, p, static_cast<cudaStream_t>(stream));
+}
+
+int pa_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                      const int32_t* seq_lens, const int32_t* query_start, int32_t num_seqs,
+                      int32_t num_query_tokens, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                      int32_t max_query_len, const pa_cache_desc* cache, float scale, int32_t window,
+                      int32_t num_sinks, float k_scale, float v_scale, int32_t* err_flag, void* stream) {
+  int rc = check_window(cache, num_seqs, num_q_heads, max_blocks_per_seq, scale, window, num_sinks);
+  if (rc != PA_OK) return rc;
+  if (num_query_tokens < 0 || max_query_len < 0 || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+  rc = check_scales(cache, &k_scale, &v_scale);
+  if (rc != PA_OK) return rc;
+  if (num_seqs == 0 || max_query_len == 0 || num_query_tokens == 0) return PA_OK;
+  if (out == nullptr || q == nullptr || k_cache == nullptr || v_cache == nullptr || seq_lens == nullptr ||
+      query_start == nullptr || block_tables == nullptr)
+    return PA_ERR_NULL_POINTER;
+  const uintptr_t qalign = cache->dtype == PA_F32 ? 4 : 16;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, qalign) || !aligned(out, qalign) ||
+      !aligned(seq_lens, 4) || !aligned(query_start, 4) || !aligned(block_tables, 4))
+    return PA_ERR_MISALIGNED;
+  if ((int64_t)num_query_tokens * num_q_heads * 128 > ((int64_t)1 << 40)) return PA_ERR_TOO_LARGE;
+
+  pa::WindowParams p = base_params(cache, out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_q_heads,
+                                   max_blocks_per_seq, scale, window, num_sinks, err_flag);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.query_start = query_start;
+  p.num_query_tokens = num_query_tokens;
+  p.max_query_len = max_query_len;
+  return launch_rows(cache, p, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
