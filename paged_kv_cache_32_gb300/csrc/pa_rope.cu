@@ -11,12 +11,18 @@
 // exactly and leaves the fraction to 2^-64 t turns; sincospif takes it from there.
 // One angle per (token, pair) and CTA, kept in shared memory for all heads.
 //
-// Bound by HBM bandwidth: 4 + (cache / element) bytes moved an element against
-// about 75 instructions per 64 bytes.  Work is cut into units of two vectors of
-// V elements (the two halves' elements V u .. of a pair range, or 2 V neighbouring
-// elements), D / 2 V units a head whatever r is; the units of all tokens and
-// heads are one flat range, of which a CTA takes kIter x 256 side by side, all
-// loads of a thread's units issued before the first is used.
+// Bound by HBM bandwidth: 4 + (cache / element) bytes moved an element.  Work is
+// cut into units of two vectors of V elements (elements V u .. of both halves of
+// the pairs, or 2 V neighbouring elements), D / 2 V units a head whatever r is.
+// A CTA walks groups of tokens (or a part of each, when a token has more units
+// than its threads hold); a thread has the same units of every group, so their
+// heads, elements and offsets are worked out once, and the next group's loads
+// are issued as soon as the present one is stored.  Two more warps, a thread
+// per pair, work out the next group's slots and angles meanwhile (their chain of
+// a load, a 64-bit division and a sine is longer than a group's stores).  (c, s)
+// lie in shared memory so that the units of a head read neighbouring banks: by
+// pairs of elements, then units.  The fixed-point frequencies, which take fp64
+// operations (two a clock and SM here), are made once per CTA.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -28,21 +34,43 @@
 namespace pa {
 namespace {
 
-constexpr int kRopeThreads = 256;
+// Threads with units (two warps more for the angles), CTAs of an SM, units of a thread.  Measured on a prompt of
+// 9001 tokens, 64 / 8 heads of 128, bf16 (halves), and of 24576, 32 / 32 heads, fp16 (neighbours): 60 and 183 us
+// (6.1 and 6.6 TB/s); 256 x 2 x 4: 85 and 318, 256 x 3 x 2: 78 and 248, 256 x 4 x 2: 101 and 329, 384 x 3 x 2: 95
+// and 311, 768 x 1 x 1: 72 and 217 us.  More rows at once than these 304 tokens lose more in DRAM than the
+// loads in flight gain; issuing a unit's next load right after its stores, between its neighbours', made a
+// warp's waits cover loads just issued (71 and 216 us).
+constexpr int kRopeThreads = 384;
+constexpr int kRopeResident = 2;
+constexpr int kBatch = 2;
 
-// Vectors of V elements of T, moved with one access each.
+// Vectors of V elements of T, moved with one access; 16-bit pairs are handled as 32-bit words.
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
   T x[V];
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = x[i];
+    } else if constexpr (V == 1) {
+      f[0] = Mma<T>::lo(reinterpret_cast<const unsigned short&>(x[0]));
+    } else {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) f[2 * i] = Mma<T>::lo(w[i]), f[2 * i + 1] = Mma<T>::hi(w[i]);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+    if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = from_float<T>(f[i]);
+    } else {
+      uint32_t* w = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) w[i] = Mma<T>::pack(f[2 * i], f[2 * i + 1]);
+    }
+  }
 };
-template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // f / 2 pi as a fraction of a turn in units of 2^-64 (whole turns per position drop out)
 __device__ __forceinline__ unsigned long long turn_fraction(double f) {
@@ -58,176 +86,216 @@ __device__ __forceinline__ uint8_t code_of(float x, float scale) {
   return (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(x, scale), __NV_SATFINITE, __NV_E4M3);
 }
 
-struct RopeToken {
-  long long row;  // cache row (block * Hkv * B + offset) of kv head 0; < 0: the token is skipped
-  int pos, off;
-};
-
-// T: queries, keys, values; FP8: the cache holds E4M3 codes (else T); V: elements of a vector; ITER: units of a
-// thread.
-template <typename T, bool FP8, bool INTERLEAVED, int V, int ITER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int tokens_per_cta) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  float2* cs = reinterpret_cast<float2*>(smem);  // [token][r / 2]: (c, s)
-  const int half = p.rotary_dim / 2, D = p.head_size;
-  RopeToken* tok = reinterpret_cast<RopeToken*>(cs + (size_t)tokens_per_cta * half);
-  const int per_head = D / (2 * V);
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
-  const int per_token = heads * per_head;
-  const long long total = (long long)p.num_tokens * per_token;
-  const long long u0 = (long long)blockIdx.x * (kRopeThreads * ITER);
-  const int t0 = (int)(u0 / per_token);
-  const int rem0 = (int)(u0 - (long long)t0 * per_token);  // unit of token t0 that this CTA starts with
-  const long long last = min(total, u0 + kRopeThreads * ITER) - 1;
-  const int nt = (int)(last / per_token) - t0 + 1;
-  griddep_wait();
-  griddep_launch_dependents();
-
-  for (int i = threadIdx.x; i < nt; i += kRopeThreads) {
-    const long long slot = p.slot_mapping[t0 + i];
-    RopeToken x;
-    x.pos = p.positions[t0 + i];
-    x.row = -1;
-    x.off = 0;
-    if (slot >= 0) {
-      const long long block = slot / p.block_size;
-      x.off = (int)(slot - block * p.block_size);
-      if (block < p.num_blocks)
-        x.row = block * p.num_kv_heads * p.block_size + x.off;
-      else
-        report_error(p.err_flag, PA_DEVERR_SLOT);
-    }
-    tok[i] = x;
+// E4M3 codes of V values over `scale`, packed in order
+template <int V>
+__device__ __forceinline__ Vec<uint8_t, V> codes_of(const float (&f)[V], float scale) {
+  Vec<uint8_t, V> y;
+  if constexpr (V == 1) {
+    y.x[0] = code_of(f[0], scale);
+  } else {
+    unsigned short* h = reinterpret_cast<unsigned short*>(y.x);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+      h[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)),
+                                      __NV_SATFINITE, __NV_E4M3);
   }
-  // ---- the loads of this thread's units
-  Vec<T, V> a[ITER], b[ITER];
-  int token[ITER], head[ITER], unit[ITER];
-#pragma unroll
-  for (int k = 0; k < ITER; ++k) {
-    const int i = rem0 + k * kRopeThreads + threadIdx.x;
-    token[k] = i / per_token;
-    const int r = i - token[k] * per_token;
-    head[k] = r / per_head;
-    unit[k] = r - head[k] * per_head;
-    if (token[k] >= nt || t0 + token[k] >= p.num_tokens) {
-      token[k] = -1;
-      continue;
-    }
-    const long long t = t0 + token[k];
-    const T* src;
-    if (head[k] < p.num_q_heads) {
-      src = static_cast<const T*>(p.q) + t * p.q_stride + (size_t)head[k] * D;
-    } else if (head[k] < p.num_q_heads + p.num_kv_heads) {
-      src = static_cast<const T*>(p.key) + t * p.key_stride + (size_t)(head[k] - p.num_q_heads) * D;
-    } else {
-      src = static_cast<const T*>(p.value) + t * p.value_stride +
-            (size_t)(head[k] - p.num_q_heads - p.num_kv_heads) * D;
-    }
-    // the unit's vectors: e0, e1 (a pair range of the halves layout: r / 2 apart, else side by side)
-    const bool apart = !INTERLEAVED && unit[k] * V < half;
-    const int e0 = apart ? unit[k] * V : INTERLEAVED ? unit[k] * 2 * V : p.rotary_dim + (unit[k] * V - half) * 2;
-    const int e1 = apart ? e0 + half : e0 + V;
-    a[k] = *reinterpret_cast<const Vec<T, V>*>(src + e0);
-    b[k] = *reinterpret_cast<const Vec<T, V>*>(src + e1);
-  }
-  // ---- angles of the CTA's tokens
-  for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-    const int t = i / half, j = i - t * half;
-    const unsigned long long f = turn_fraction(p.inv_freq[j]);
-    const long long turns = (long long)(f * (unsigned long long)(long long)p.positions[t0 + t]);
-    float s, c;
-    sincospif(__ll2float_rn(turns) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns in [-1, 1]
-    cs[i] = make_float2(c * p.magnitude, s * p.magnitude);
-  }
-  __syncthreads();
-
-#pragma unroll
-  for (int k = 0; k < ITER; ++k) {
-    if (token[k] < 0) continue;
-    const RopeToken x = tok[token[k]];
-    if (x.row < 0) continue;  // padding, or a slot outside the pool
-    const int h = head[k];
-    const bool is_q = h < p.num_q_heads, is_v = h >= p.num_q_heads + p.num_kv_heads;
-    const bool apart = !INTERLEAVED && unit[k] * V < half;
-    const int e0 = apart ? unit[k] * V : INTERLEAVED ? unit[k] * 2 * V : p.rotary_dim + (unit[k] * V - half) * 2;
-    const int e1 = apart ? e0 + half : e0 + V;
-    float u[V], w[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) u[i] = to_float<T>(a[k].x[i]), w[i] = to_float<T>(b[k].x[i]);
-    if (!is_v) {
-      const float2* ct = cs + (size_t)token[k] * half + unit[k] * V;
-      if constexpr (INTERLEAVED) {
-        // pairs V unit .. V unit + V - 1: neighbours within u, then within w
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (unit[k] * V + i < half) {
-            const float2 c = ct[i];
-            float& x0 = 2 * i < V ? u[(2 * i) % V] : w[(2 * i) % V];
-            float& x1 = 2 * i + 1 < V ? u[(2 * i + 1) % V] : w[(2 * i + 1) % V];
-            const float y0 = c.x * x0 - c.y * x1, y1 = c.x * x1 + c.y * x0;
-            x0 = y0, x1 = y1;
-          }
-        }
-      } else if (apart) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 c = ct[i];
-          const float y0 = c.x * u[i] - c.y * w[i], y1 = c.x * w[i] + c.y * u[i];
-          u[i] = y0, w[i] = y1;
-        }
-      }
-    }
-    if (is_q || !FP8) {
-      T* dst;
-      if (is_q) {
-        dst = static_cast<T*>(p.q_out) + (t0 + token[k]) * p.q_out_stride + (size_t)h * D;
-      } else {
-        const int hk = h - p.num_q_heads - (is_v ? p.num_kv_heads : 0);
-        dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) + (x.row + (long long)hk * p.block_size) * D;
-      }
-      Vec<T, V> y, z;
-#pragma unroll
-      for (int i = 0; i < V; ++i) y.x[i] = from_float<T>(u[i]), z.x[i] = from_float<T>(w[i]);
-      *reinterpret_cast<Vec<T, V>*>(dst + e0) = y;
-      *reinterpret_cast<Vec<T, V>*>(dst + e1) = z;
-    } else if (!is_v) {
-      uint8_t* dst = static_cast<uint8_t*>(p.k_cache) + (x.row + (long long)(h - p.num_q_heads) * p.block_size) * D;
-      Vec<uint8_t, V> y, z;
-#pragma unroll
-      for (int i = 0; i < V; ++i) y.x[i] = code_of(u[i], p.k_scale), z.x[i] = code_of(w[i], p.k_scale);
-      *reinterpret_cast<Vec<uint8_t, V>*>(dst + e0) = y;
-      *reinterpret_cast<Vec<uint8_t, V>*>(dst + e1) = z;
-    } else {
-      // values [block][head][off / 16][d][off % 16]
-      const int hk = h - p.num_q_heads - p.num_kv_heads;
-      uint8_t* dst = static_cast<uint8_t*>(p.v_cache) +
-                     (x.row - x.off + (long long)hk * p.block_size + x.off / 16 * 16) * D + x.off % 16;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        dst[(size_t)(e0 + i) * 16] = code_of(u[i], p.v_scale);
-        dst[(size_t)(e1 + i) * 16] = code_of(w[i], p.v_scale);
-      }
-    }
-  }
+  return y;
 }
 
-template <typename T, bool FP8, bool INTERLEAVED, int V, int ITER>
-cudaError_t launch_iter(const RopeParams& p, cudaStream_t stream) {
-  const int per_token = (p.num_q_heads + 2 * p.num_kv_heads) * (p.head_size / (2 * V));
-  const long long total = (long long)p.num_tokens * per_token;
-  const long long ctas = (total + kRopeThreads * ITER - 1) / (kRopeThreads * ITER);
-  const int tokens = (kRopeThreads * ITER - 1) / per_token + 2;  // that a CTA's units may touch
-  const size_t smem = (size_t)tokens * (p.rotary_dim / 2 * sizeof(float2) + sizeof(RopeToken)) + 16;
-  return launch_dependent(rope_kernel<T, FP8, INTERLEAVED, V, ITER>, dim3((unsigned)ctas), dim3(kRopeThreads), smem,
-                          stream, p, tokens);
+struct RopeToken {
+  long long row;  // cache row (block * Hkv * B + offset) of kv head 0; < 0: the token is skipped
+  int off;        // offset in the block
+};
+
+constexpr int kMaxHalf = 64;  // pairs of the largest head
+constexpr int kMaxGroup = 16; // tokens of a group
+
+// How the units are dealt out: groups of `tokens` tokens, each cut into `parts` parts of `part_units` units (a
+// multiple of the units of a head; parts > 1 only for groups of one token).  The CTAs of a part walk its groups.
+struct RopePlan {
+  int tokens, parts, part_units, groups;
+  int log2_per_head;  // units of a head
+};
+
+// T: queries, keys, values; FP8: the cache holds E4M3 codes (else T); V: elements of a vector
+template <typename T, bool FP8, bool INTERLEAVED, int V>
+__global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_kernel(const RopeParams p, const RopePlan plan) {
+  __shared__ __align__(16) float2 cs_all[2][kMaxGroup * kMaxHalf];  // (c, s) of token, pair; two groups in turn
+  __shared__ RopeToken tok_all[2][kMaxGroup];
+  const int half = p.rotary_dim / 2, D = p.head_size, per_head = 1 << plan.log2_per_head;
+  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
+  const int per_token = heads << plan.log2_per_head;
+  // pair V u + i of a token at [i / 2][u][i % 2] (V = 1: [u])
+  auto cs_at = [&](int u, int i) { return V == 1 ? u : ((i / 2) * per_head + u) * 2 + i % 2; };
+  griddep_wait();
+  griddep_launch_dependents();
+  const int part = blockIdx.x % plan.parts;
+  const int first = blockIdx.x / plan.parts, step = gridDim.x / plan.parts;
+
+  if (threadIdx.x >= kRopeThreads) {
+    // ---- slots and angles, one group ahead of the units
+    const int j = threadIdx.x - kRopeThreads;
+    const unsigned long long f = j < half ? turn_fraction(p.inv_freq[j]) : 0ull;
+    int buf = 0;
+    for (int group = first; group < plan.groups; group += step, buf ^= 1) {
+      const int t0 = group * plan.tokens, nt = min(plan.tokens, p.num_tokens - t0);
+      if (j < nt) {
+        const long long slot = p.slot_mapping[t0 + j];
+        RopeToken x;
+        x.row = -1;
+        x.off = 0;
+        if (slot >= 0) {
+          const long long block = slot / p.block_size;
+          x.off = (int)(slot - block * p.block_size);
+          if (block < p.num_blocks)
+            x.row = block * p.num_kv_heads * p.block_size + x.off;
+          else
+            report_error(p.err_flag, PA_DEVERR_SLOT);
+        }
+        tok_all[buf][j] = x;
+      }
+      if (j < half) {
+        for (int t = 0; t < nt; ++t) {
+          const long long turns = (long long)(f * (unsigned long long)(long long)p.positions[t0 + t]);
+          float s, c;
+          sincospif(__ll2float_rn(turns) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns in [-1, 1]
+          cs_all[buf][t * kMaxHalf + cs_at(j / V, j % V)] = make_float2(c * p.magnitude, s * p.magnitude);
+        }
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  // ---- this thread's units: the same heads and elements of every group
+  enum { kNone = -1, kQ = 0, kK = 1, kV = 2 };
+  int kind[kBatch], tl[kBatch], unit[kBatch], apart[kBatch];
+  const T* src[kBatch];     // in token 0's row of the group's first token's array
+  long long dst[kBatch];    // elements from the row of q_out, or of kv head 0 in the cache
+  const int end = plan.parts > 1 ? min(per_token, (part + 1) * plan.part_units) : plan.tokens * per_token;
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    const int i = part * plan.part_units + k * kRopeThreads + threadIdx.x;
+    kind[k] = kNone;
+    tl[k] = unit[k] = apart[k] = 0;
+    src[k] = nullptr;
+    dst[k] = 0;
+    if (i >= end) continue;
+    tl[k] = i / per_token;
+    const int r = i - tl[k] * per_token, h = r >> plan.log2_per_head;
+    unit[k] = r & (per_head - 1);
+    const bool cut = !INTERLEAVED && unit[k] * V < half;  // a vector of each half, else two side by side
+    const int e0 = cut ? unit[k] * V : unit[k] * 2 * V;
+    apart[k] = cut ? half : V;
+    const int hk = (h - p.num_q_heads) % p.num_kv_heads;
+    kind[k] = h < p.num_q_heads ? kQ : h < p.num_q_heads + p.num_kv_heads ? kK : kV;
+    if (kind[k] == kQ) {
+      src[k] = static_cast<const T*>(p.q) + tl[k] * p.q_stride + (size_t)h * D + e0;
+      dst[k] = tl[k] * p.q_out_stride + (long long)h * D + e0;
+    } else {
+      src[k] = kind[k] == kK ? static_cast<const T*>(p.key) + tl[k] * p.key_stride + (size_t)hk * D + e0
+                             : static_cast<const T*>(p.value) + tl[k] * p.value_stride + (size_t)hk * D + e0;
+      // (values of an FP8 cache: [block][head][off / 16][d][off % 16])
+      dst[k] = (long long)hk * p.block_size * D + (FP8 && kind[k] == kV ? e0 * 16 : e0);
+    }
+  }
+  Vec<T, V> a[kBatch], b[kBatch];
+  auto load = [&](int t0, int k) {
+    if (kind[k] == kNone || t0 + tl[k] >= p.num_tokens) return;
+    const long long stride = kind[k] == kQ ? p.q_stride : kind[k] == kK ? p.key_stride : p.value_stride;
+    const T* x = src[k] + t0 * stride;
+    a[k] = *reinterpret_cast<const Vec<T, V>*>(x);
+    b[k] = *reinterpret_cast<const Vec<T, V>*>(x + apart[k]);
+  };
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) load(first * plan.tokens, k);
+
+  int buf = 0;
+  for (int group = first; group < plan.groups; group += step, buf ^= 1) {
+    const int t0 = group * plan.tokens, nt = min(plan.tokens, p.num_tokens - t0);
+    const float2* cs = cs_all[buf];
+    const RopeToken* tok = tok_all[buf];
+    __syncthreads();  // this group's are written, and the ones before, whose buffers come next, have been read
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const RopeToken x = tok[tl[k]];
+      // (a row < 0: padding, or a slot outside the pool)
+      if (kind[k] != kNone && tl[k] < nt && x.row >= 0) {
+        float u[V], w[V];
+        a[k].get(u);
+        b[k].get(w);
+        if (kind[k] != kV && unit[k] * V < half) {
+          const float2* ct = cs + tl[k] * kMaxHalf;
+          float2 c[V];
+          if constexpr (V == 1) {
+            c[0] = ct[cs_at(unit[k], 0)];
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+              const float4 x4 = *reinterpret_cast<const float4*>(ct + cs_at(unit[k], i));
+              c[i] = make_float2(x4.x, x4.y), c[i + 1] = make_float2(x4.z, x4.w);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            // pair V unit + i: elements i of both vectors, or neighbours (2i, 2i + 1) of the two in a row
+            if (!INTERLEAVED || unit[k] * V + i < half) {
+              float& x0 = !INTERLEAVED ? u[i] : 2 * i < V ? u[(2 * i) % V] : w[(2 * i) % V];
+              float& x1 = !INTERLEAVED ? w[i] : 2 * i + 1 < V ? u[(2 * i + 1) % V] : w[(2 * i + 1) % V];
+              const float y0 = c[i].x * x0 - c[i].y * x1, y1 = c[i].x * x1 + c[i].y * x0;
+              x0 = y0, x1 = y1;
+            }
+          }
+        }
+        if (kind[k] == kQ || !FP8) {
+          T* d = kind[k] == kQ ? static_cast<T*>(p.q_out) + t0 * p.q_out_stride
+                               : static_cast<T*>(kind[k] == kK ? p.k_cache : p.v_cache) + x.row * D;
+          Vec<T, V> y, z;
+          y.set(u);
+          z.set(w);
+          *reinterpret_cast<Vec<T, V>*>(d + dst[k]) = y;
+          *reinterpret_cast<Vec<T, V>*>(d + dst[k] + apart[k]) = z;
+        } else if (kind[k] == kK) {
+          uint8_t* d = static_cast<uint8_t*>(p.k_cache) + x.row * D + dst[k];
+          *reinterpret_cast<Vec<uint8_t, V>*>(d) = codes_of(u, p.k_scale);
+          *reinterpret_cast<Vec<uint8_t, V>*>(d + apart[k]) = codes_of(w, p.k_scale);
+        } else {
+          uint8_t* d = static_cast<uint8_t*>(p.v_cache) + (x.row - x.off + x.off / 16 * 16) * D + x.off % 16 + dst[k];
+          const Vec<uint8_t, V> y = codes_of(u, p.v_scale), z = codes_of(w, p.v_scale);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            d[i * 16] = y.x[i];
+            d[(apart[k] + i) * 16] = z.x[i];
+          }
+        }
+      }
+    }
+    if (group + step < plan.groups) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) load((group + step) * plan.tokens, k);
+    }
+  }
 }
 
 template <typename T, bool FP8, bool INTERLEAVED, int V>
 cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
-  // one unit a thread while that leaves the grid small (a decode step), else four
-  const long long units = (long long)p.num_tokens * (p.num_q_heads + 2 * p.num_kv_heads) * (p.head_size / (2 * V));
-  return units < 4ll * 152 * 2 * kRopeThreads ? launch_iter<T, FP8, INTERLEAVED, V, 1>(p, stream)
-                                              : launch_iter<T, FP8, INTERLEAVED, V, 4>(p, stream);
+  RopePlan plan;
+  const int per_head = p.head_size / (2 * V);
+  plan.log2_per_head = 0;
+  while ((1 << plan.log2_per_head) < per_head) ++plan.log2_per_head;
+  const long long per_token = (long long)(p.num_q_heads + 2 * p.num_kv_heads) * per_head;
+  constexpr int kCtas = 152 * kRopeResident;
+  // units of a CTA and group: as many as its threads hold, or, while that leaves SMs idle (a decode step), fewer
+  long long most = kBatch * kRopeThreads;
+  while (most > kRopeThreads && per_token * p.num_tokens < kCtas * most) most /= 2;
+  plan.tokens = (int)(most / per_token);
+  plan.tokens = plan.tokens < 1 ? 1 : plan.tokens > kMaxGroup ? kMaxGroup : plan.tokens;
+  plan.parts = plan.tokens > 1 ? 1 : (int)((per_token + most - 1) / most);
+  plan.part_units = plan.parts > 1 ? (int)((per_token + plan.parts - 1) / plan.parts + per_head - 1) / per_head * per_head : 0;
+  plan.groups = (int)(((long long)p.num_tokens + plan.tokens - 1) / plan.tokens);
+  const int walkers = kCtas / plan.parts > 0 ? kCtas / plan.parts : 1;  // CTAs of a part
+  const int grid = (plan.groups < walkers ? plan.groups : walkers) * plan.parts;
+  return launch_dependent(rope_kernel<T, FP8, INTERLEAVED, V>, dim3((unsigned)grid), dim3(kRopeThreads + kMaxHalf), 0, stream, p,
+                          plan);
 }
 
 template <typename T, bool FP8, int VMAX>

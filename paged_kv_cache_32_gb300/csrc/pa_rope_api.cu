@@ -121,9 +121,8 @@ int pa_rope_and_cache(void* q_out, void* k_cache, void* v_cache, const void* q, 
   if (num_q_heads > 0 && (((q_out != q || q_out_stride != q_stride) && overlap(q, q_stride, q_row)) ||
                           overlap(key, key_stride, kv_row) || overlap(value, value_stride, kv_row)))
     return PA_ERR_INVALID_ARG;
-  // units of two elements at least, counted per token in int32 and per CTA in the grid
-  const int64_t heads = (int64_t)num_q_heads + 2 * cache->num_kv_heads;
-  if (heads * D > kInt32Max / 4 || (int64_t)num_tokens * heads * (D / 2) / 256 > kInt32Max - 1) return PA_ERR_TOO_LARGE;
+  // a token's elements are counted in int32
+  if (((int64_t)num_q_heads + 2 * (int64_t)cache->num_kv_heads) * D > kInt32Max / 32) return PA_ERR_TOO_LARGE;
 
   pa::RopeParams p = {};
   p.q_out = q_out;
