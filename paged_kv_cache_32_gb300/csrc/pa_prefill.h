@@ -18,13 +18,24 @@ struct PrefillParams {
   int32_t* err_flag;            // nullable
   int32_t num_seqs, num_q_heads, num_kv_heads;
   int32_t max_blocks, block_size, num_blocks;
-  int32_t q_tiles;              // ceil(max_query_len / 128)
+  int32_t q_tiles;              // query tiles of the longest chunk: ceil(max_query_len / 128) in the plain form
   int32_t num_query_tokens;     // rows of q and out
   float scale_log2;
+  // windowed form (pa_prefill_window; window 0: the plain one): a query at position p sees the positions i <= p
+  // with i > p - window or i < sinks; a query tile is 128 >> pack_log2 queries of 2^pack_log2 query heads of one
+  // kv head
+  int32_t window, sinks, pack_log2;
+  int32_t max_query_len;        // windowed form: bound on a chunk's queries
 };
 
+namespace host {
+bool encode_query_map(CUtensorMap* map, const void* base, const pa_cache_desc* c, int32_t num_q_heads,
+                      int32_t num_query_tokens, int heads);
+}
+
 // tk, tv: the caches as rows of D elements (box 64 columns x block_size rows, 128-byte swizzle);
-// tq: q as [tokens][heads][D] (box 64 columns x 1 head x 128 tokens, 128-byte swizzle); to: out, the same
+// tq: q as [tokens][heads][D] (box 64 columns x 1 head x 128 tokens, windowed 2^pack_log2 heads x the tile's
+// tokens, 128-byte swizzle); to: out, the same
 cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                               const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream);
 

@@ -10,6 +10,28 @@
 #include "pa_internal.h"
 #include "pa_prefill.h"
 
+namespace pa {
+namespace host {
+
+// q and out [tokens][heads][D]: a tile of 128 rows is one box of 64 columns x `heads` x 128 / heads tokens per half
+bool encode_query_map(CUtensorMap* map, const void* base, const pa_cache_desc* c, int32_t num_q_heads,
+                      int32_t num_query_tokens, int heads) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)c->head_size, (cuuint64_t)num_q_heads, (cuuint64_t)num_query_tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)c->head_size * 2, (cuuint64_t)num_q_heads * c->head_size * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)(128 / heads)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt =
+      c->dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace host
+}  // namespace pa
+
 using namespace pa::host;
 
 extern "C" {
@@ -38,27 +60,13 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
   if ((long long)max_blocks_per_seq * cache->block_size > kInt32Max) return PA_ERR_TOO_LARGE;
   if ((long long)num_query_tokens * num_q_heads * 128 > ((long long)1 << 40)) return PA_ERR_TOO_LARGE;
 
-  auto enc = tensor_map_encoder();
-  if (enc == nullptr) return PA_ERR_CUDA;
   CUtensorMap tk, tv, tq, to;
   if (!encode_cache_map(&tk, k_cache, cache, cache->block_size) ||
       !encode_cache_map(&tv, v_cache, cache, cache->block_size))
     return PA_ERR_CUDA;
-  {
-    // q and out [tokens][heads][D]: a 128-token tile of one head is one box of 64 columns x 1 x 128 per half
-    cuuint64_t dims[3] = {(cuuint64_t)cache->head_size, (cuuint64_t)num_q_heads, (cuuint64_t)num_query_tokens};
-    cuuint64_t strides[2] = {(cuuint64_t)cache->head_size * 2, (cuuint64_t)num_q_heads * cache->head_size * 2};
-    cuuint32_t box[3] = {64, 1, 128};
-    cuuint32_t estr[3] = {1, 1, 1};
-    const CUtensorMapDataType dt =
-        cache->dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (enc(&tq, dt, 3, const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-        enc(&to, dt, 3, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return PA_ERR_CUDA;
-  }
+  if (!encode_query_map(&tq, q, cache, num_q_heads, num_query_tokens, 1) ||
+      !encode_query_map(&to, out, cache, num_q_heads, num_query_tokens, 1))
+    return PA_ERR_CUDA;
   pa::PrefillParams p;
   p.out = out;
   p.q = q;
@@ -77,6 +85,8 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
   p.q_tiles = (int32_t)q_tiles;
   p.num_query_tokens = num_query_tokens;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.window = p.sinks = p.pack_log2 = 0;  // the plain form
+  p.max_query_len = max_query_len;
   cudaError_t e = pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -62,6 +62,19 @@
 //    swizzled layout; the P V issuer then stores a full tile with two
 //    tensor-map stores, and a ragged tile (rows past the chunk belong to
 //    another sequence) is copied out row by row by its warps.
+//
+// The windowed form (kWindow; pa_prefill_window): the query at position p sees
+// the positions i <= p with i > p - W or i < S.
+//  * A tile's 128 rows are 128 / P queries of P = 2^pack_log2 query heads of one
+//    kv head (row r: query r / P, head r % P), which is one box of the q tensor
+//    map.  The queries of a tile then span 128 / P positions, so that fewer key
+//    tiles are cut by the window's edges, and a chunk of a few queries fills one
+//    tile a kv head instead of one a query head.
+//  * The key tiles of an item are those of [0, S) and of the window of its first
+//    row on, walked as one list (key_tile); rows whose window starts later mask.
+//  * Blocks without a position that some query of the chunk sees are not read
+//    (they may have been released); their value rows read as zeros, as the rows
+//    past the sequence do.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -317,15 +330,36 @@ __device__ __forceinline__ void cp_async16(void* smem_dst, const void* gmem_src)
 // all of this thread's cp.async copies have landed (commits the pending ones first)
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Which keys of a tile take part: all of them, or those at x, counted from key 2c, with see0(x) in row 0 and
+// see1(x) in row 1.
+struct SeeAll {};
+struct SeeCausal {
+  int e0, e1;
+  __device__ __forceinline__ bool see0(int x) const { return x <= e0; }
+  __device__ __forceinline__ bool see1(int x) const { return x <= e1; }
+};
+// x in [f, f + n), or below g (the first tokens), and at most e
+template <bool kSinks>
+struct SeeWindow {
+  int e0, e1, f0, f1, g;
+  unsigned n0, n1;
+  __device__ __forceinline__ bool see0(int x) const {
+    return (unsigned)(x - f0) < n0 || (kSinks && x < g && x <= e0);
+  }
+  __device__ __forceinline__ bool see1(int x) const {
+    return (unsigned)(x - f1) < n1 || (kSinks && x < g && x <= e1);
+  }
+};
+
 // P of 8 of the 16 key pairs this thread holds in each of its two rows, pairs j0 .. j0 + 7 (v in
 // the 16x256b layout over the tile's 128 columns: pair j = keys 8j + 2c, 8j + 2c + 1, c = thread % 4;
 // v[4j], v[4j + 1] row 0, v[4j + 2], v[4j + 3] row 1) from the raw scores, the scale in log2 units
-// and the rows' reference maxima; a pair's keys past e0 (e1) of row 0 (1), counted from key 2c, are
-// masked.  Writes the packed words of those pairs in the 16x128b layout (hi[2i] row 0, hi[2i + 1]
+// and the rows' reference maxima; keys that `mask` excludes weigh nothing.  Writes the packed words of those pairs in the 16x128b layout (hi[2i] row 0, hi[2i + 1]
 // row 1 for pair j0 + i; for bf16 also lo) and adds the rows' sums of the unrounded weights to s0, s1.
-template <typename T, bool kMasked>
-__device__ __forceinline__ void make_p(const float* v, int j0, float sl2, float mr0, float mr1, int e0, int e1,
+template <typename T, typename Mask>
+__device__ __forceinline__ void make_p(const float* v, int j0, float sl2, float mr0, float mr1, const Mask& mask,
                                        uint32_t* hi, uint32_t* lo, float& s0, float& s1) {
+  constexpr bool kMasked = !std::is_same<Mask, SeeAll>::value;
   float2 acc0[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   float2 acc1[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 sc2 = make_float2(sl2, sl2), n0 = make_float2(-mr0, -mr0), n1 = make_float2(-mr1, -mr1);
@@ -334,11 +368,11 @@ __device__ __forceinline__ void make_p(const float* v, int j0, float sl2, float 
     const float2 x = fma2(make_float2(v[4 * j], v[4 * j + 1]), sc2, n0);
     const float2 y = fma2(make_float2(v[4 * j + 2], v[4 * j + 3]), sc2, n1);
     float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y), p2 = fast_exp2(y.x), p3 = fast_exp2(y.y);
-    if (kMasked) {
-      p0 = 8 * j <= e0 ? p0 : 0.f;
-      p1 = 8 * j + 1 <= e0 ? p1 : 0.f;
-      p2 = 8 * j <= e1 ? p2 : 0.f;
-      p3 = 8 * j + 1 <= e1 ? p3 : 0.f;
+    if constexpr (kMasked) {
+      p0 = mask.see0(8 * j) ? p0 : 0.f;
+      p1 = mask.see0(8 * j + 1) ? p1 : 0.f;
+      p2 = mask.see1(8 * j) ? p2 : 0.f;
+      p3 = mask.see1(8 * j + 1) ? p3 : 0.f;
     }
     acc0[j & 1] = add2(acc0[j & 1], make_float2(p0, p1));
     acc1[j & 1] = add2(acc1[j & 1], make_float2(p2, p3));
@@ -403,16 +437,70 @@ __device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfItem&
   return true;
 }
 
+// An item of the windowed form: rows of 2^pack_log2 heads from h on, queries tile0 ..
+struct PfWindowItem : PfItem {
+  int n_sink, t_win;      // key tiles of [0, S), first key tile of the rest of the list
+  int lo_chunk, s_chunk;  // what some query of the chunk sees: [0, s_chunk) and from lo_chunk on
+};
+
+__device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfWindowItem& it, bool report) {
+  const int groups = p.num_q_heads >> p.pack_log2, per_tile = kTile >> p.pack_log2;
+  const int per_seq = p.q_tiles * groups;
+  it.s = idx / per_seq;
+  const int rem = idx % per_seq;
+  const int qt = p.q_tiles - 1 - rem / groups;
+  it.h = (rem % groups) << p.pack_log2;
+  it.q0 = __ldg(p.query_start + it.s);
+  it.n = __ldg(p.query_start + it.s + 1) - it.q0;
+  it.L = __ldg(p.seq_lens + it.s);
+  const int B = p.block_size;
+  if (it.q0 < 0 || it.n < 0 || (long long)it.q0 + it.n > p.num_query_tokens || it.n > p.max_query_len ||
+      it.L < it.n || (long long)it.L > (long long)p.max_blocks * B) {
+    if (report && qt == 0 && it.h == 0) report_error(p.err_flag, PA_DEVERR_QUERY);
+    return false;
+  }
+  it.tile0 = qt * per_tile;
+  if (it.tile0 >= it.n) return false;
+  it.hkv = it.h / (p.num_q_heads / p.num_kv_heads);
+  const int queries = min(per_tile, it.n - it.tile0);
+  it.rows = queries << p.pack_log2;
+  it.pos0 = it.L - it.n + it.tile0;
+  it.nblocks_seq = (it.L + B - 1) / B;
+  it.lo_chunk = max(0, it.L - it.n - p.window + 1);
+  it.s_chunk = min(p.sinks, it.L);
+  const int last = it.pos0 + queries - 1, lo = max(0, it.pos0 - p.window + 1);
+  it.n_sink = (min(p.sinks, last + 1) + kTile - 1) / kTile;
+  it.t_win = max(lo / kTile, it.n_sink);
+  it.key_tiles = it.n_sink + max(0, last / kTile + 1 - it.t_win);
+  return true;
+}
+
+// the t-th key tile of an item's list
+__device__ __forceinline__ int key_tile(const PfItem&, int t) { return t; }
+__device__ __forceinline__ int key_tile(const PfWindowItem& it, int t) {
+  return t < it.n_sink ? t : t - it.n_sink + it.t_win;
+}
+// may block positions pos .. pos + w - 1 hold a row that some query of the chunk sees; do they hold no other?
+__device__ __forceinline__ bool block_seen(const PfItem&, int, int) { return true; }
+__device__ __forceinline__ bool block_seen(const PfWindowItem& it, int pos, int w) {
+  return pos < it.s_chunk || pos + w > it.lo_chunk;
+}
+__device__ __forceinline__ bool block_whole(const PfItem&, int, int) { return true; }
+__device__ __forceinline__ bool block_whole(const PfWindowItem& it, int pos, int w) {
+  return pos >= it.lo_chunk || pos + w <= it.s_chunk;
+}
+
 // Persistent: each CTA takes items blockIdx.x, blockIdx.x + gridDim.x, ...  Every role walks the same
 // items; the K/V rings, the S buffers and their barriers run on across items (tg counts this CTA's
 // key tiles so far), so the next item's Q, K/V copies and first S MMAs overlap this item's last
 // P V and epilogue.
-template <typename T>
+template <typename T, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                       const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_out,
                       const PrefillParams p) {
-  const int n_items = p.num_seqs * p.num_q_heads * p.q_tiles;
+  using Item = typename std::conditional<kWindow, PfWindowItem, PfItem>::type;
+  const int n_items = p.num_seqs * (kWindow ? p.num_q_heads >> p.pack_log2 : p.num_q_heads) * p.q_tiles;
   const int B = p.block_size;
   const int blocks_per_tile = kTile / B;
   const int slots = 2 * blocks_per_tile;  // tensor-map copies per tile: one per block and half
@@ -433,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_staged = bar_q + 17; // the item's output tile written to the stage (or stored) (phase per item)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBarOff + 192);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 200);
-  PfItem* items = reinterpret_cast<PfItem*>(smem + kBarOff + 256);  // [2] published items (s < 0: none left)
+  Item* items = reinterpret_cast<Item*>(smem + kBarOff + 256);  // [2] published items (s < 0: none left)
+  static_assert(2 * sizeof(Item) <= 256, "the published items end the barrier region");
   uint8_t* qbuf = smem + kQOff;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int n_s = 0, n_o = 0;  // S / P V commits (control thread)
@@ -486,13 +575,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int tg = 0;
     for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
-      PfItem it;
+      Item it;
       if (!pf_item(p, idx, it, false)) continue;
       const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
       // the table entry of this lane's block, read one tile ahead
       auto fetch = [&](int kt) -> int {
-        const int bi = kt * blocks_per_tile + blk;
-        return (blk < blocks_per_tile && kt < it.key_tiles && bi < it.nblocks_seq) ? __ldg(table + bi) : kPastEnd;
+        const int bi = key_tile(it, kt) * blocks_per_tile + blk;
+        return (blk < blocks_per_tile && kt < it.key_tiles && bi < it.nblocks_seq && block_seen(it, bi * B, B))
+                   ? __ldg(table + bi)
+                   : kPastEnd;
       };
       int entry_next = fetch(0);
       for (int t = 0; t < it.key_tiles; ++t, ++tg) {
@@ -510,8 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* st = ring + (tg & 1) * 2 * kHalf + half * kHalf;
         const bool in_pool = entry >= 0 && entry < p.num_blocks;
         if (!is_v && half == 0 && entry != kPastEnd && !in_pool) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
-        // V: only blocks entirely inside the sequence go by tensor-map copy
-        const bool whole = in_pool && (!is_v || (t * blocks_per_tile + blk + 1) * B <= it.L);
+        // V: only blocks entirely inside the sequence (and the window) go by tensor-map copy
+        const int first_pos = (key_tile(it, t) * blocks_per_tile + blk) * B;
+        const bool whole = in_pool && (!is_v || (first_pos + B <= it.L && block_whole(it, first_pos, B)));
         if (blk < blocks_per_tile) {
           if (whole) {
             mbar_arrive_expect_tx(bar, (uint32_t)B * 128);
@@ -532,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int e = __shfl_sync(0xffffffffu, entry, b);
               if (!((partial >> b) & 1)) continue;
               const int r = r0 + (lane >> 3), chunk = lane & 7;
-              const int pos = t * kTile + r;
+              const int pos = key_tile(it, t) * kTile + r;
               uint8_t* dst = st + swz128(r, chunk);
-              if (pos < it.L && e >= 0 && e < p.num_blocks)
+              if (pos < it.L && block_seen(it, pos, 1) && e >= 0 && e < p.num_blocks)
                 cp_async16(dst, cache + (((size_t)e * p.num_kv_heads + it.hkv) * B + (pos % B)) * kD + half * 64 +
                                     chunk * 8);
               else
@@ -559,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // phase k of bar_qs.  Item k + 1 is published once every softmax warp has read item k (bar_q
       // phase k), which also means the S MMAs of item k - 1, the last readers of that Q buffer, have
       // finished.  It reports inconsistent chunks: every item of this CTA passes through here once.
-      auto publish = [&](int idx, int k, PfItem& it) {
+      auto publish = [&](int idx, int k, Item& it) {
         for (; idx < n_items; idx += gridDim.x)
           if (pf_item(p, idx, it, true)) break;
         if (idx >= n_items) it.s = -1;
@@ -577,13 +669,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool ok = true;
       int tg = 0, item_no = 0;
-      PfItem it;
+      Item it;
       int idx = publish(blockIdx.x, 0, it);
       while (ok && idx < n_items) {
         // Q of this item in its buffer (this thread publishes the barrier's next phase: exact)
         ok = wait_bar_spin(bar_qs, item_no & 1, abort_flag);
         if (!ok) break;
-        PfItem nx;
+        Item nx;
         int idx_next = n_items;
         bool published = false;
         // publish the next item once every softmax warp has read this one (checked between tiles, and
@@ -643,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
-        PfItem it;
+        Item it;
         if (!pf_item(p, idx, it, false)) continue;
         // the first P V overwrites O: the previous item's epilogue must have read it (the barrier's
         // next phase is this item's epilogue, which needs these MMAs, so the wait is exact)
@@ -701,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int tg = 0, item_no = 0;
     int lim0 = 0, lim1 = 0;                                    // last key position each row sees
+    Item it = {};
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // reference maxima (log2 units), partial sums
     // key tile kt of the current item (this CTA's tile tg)
     auto tile = [&](int kt) {
@@ -712,9 +805,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld16x256_x8(s_addr, v);
       tmem_ld16x256_x8(s_addr + 64, v + 32);
       tmem_wait_ld<64>(v);
-      const int key0 = kt * kTile + 2 * c4;          // key of this thread's pair 0
+      const int tile0 = key_tile(it, kt) * kTile;    // first key
+      const int key0 = tile0 + 2 * c4;               // key of this thread's pair 0
       const int e0 = lim0 - key0, e1 = lim1 - key0;  // pair j's keys 8j, 8j + 1 are visible up to e
-      const bool unmasked = __all_sync(0xffffffffu, min(lim0, lim1) >= kt * kTile + kTile - 1);
+      // window: the first position of each row's window
+      const int low0 = kWindow ? max(0, lim0 - p.window + 1) : 0, low1 = kWindow ? max(0, lim1 - p.window + 1) : 0;
+      const bool unmasked =
+          __all_sync(0xffffffffu, min(lim0, lim1) >= tile0 + kTile - 1 &&
+                                      (!kWindow || max(low0, low1) <= tile0 || tile0 + kTile <= p.sinks));
       // ---- fp16, an unmasked tile after the item's first: P with the current reference maxima, kept
       //      when no weight can exceed 2^threshold (each thread's share of a row's tile sum is at most
       //      kLazyBound).  The exact path below would then move no reference max and compute the same
@@ -726,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j0 = 0; j0 < 16; j0 += 8) {
           uint32_t hi[16], lo[16];
-          make_p<T, false>(v, j0, sl2, m0, m1, e0, e1, hi, lo, n0, n1);
+          make_p<T>(v, j0, sl2, m0, m1, SeeAll{}, hi, lo, n0, n1);
           tmem_st16x128_x8(s_addr + 4 * j0, hi);
           if constexpr (split_p<T>()) tmem_st16x128_x8(s_addr + 64 + 4 * j0, lo);
         }
@@ -738,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();  // the words stored above land before the exact path's stores
         }
       }
-      if (!lazy) {
+      auto exact = [&](const auto& mask) {
         // ---- the rows' tile maxima, and the reference maxima they imply
         float a0 = -INFINITY, b0 = -INFINITY, a1 = -INFINITY, b1 = -INFINITY;  // two chains per row
 #pragma unroll
@@ -761,10 +859,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             a0 = b0 = a1 = b1 = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              a0 = max3(a0, 8 * j <= e0 ? v[4 * j] : -INFINITY, 8 * j + 1 <= e0 ? v[4 * j + 1] : -INFINITY);
-              a1 = max3(a1, 8 * j <= e1 ? v[4 * j + 2] : -INFINITY, 8 * j + 1 <= e1 ? v[4 * j + 3] : -INFINITY);
-              b0 = max3(b0, 8 * j + 8 <= e0 ? v[4 * j + 4] : -INFINITY, 8 * j + 9 <= e0 ? v[4 * j + 5] : -INFINITY);
-              b1 = max3(b1, 8 * j + 8 <= e1 ? v[4 * j + 6] : -INFINITY, 8 * j + 9 <= e1 ? v[4 * j + 7] : -INFINITY);
+              a0 = max3(a0, mask.see0(8 * j) ? v[4 * j] : -INFINITY, mask.see0(8 * j + 1) ? v[4 * j + 1] : -INFINITY);
+              a1 = max3(a1, mask.see1(8 * j) ? v[4 * j + 2] : -INFINITY,
+                        mask.see1(8 * j + 1) ? v[4 * j + 3] : -INFINITY);
+              b0 = max3(b0, mask.see0(8 * j + 8) ? v[4 * j + 4] : -INFINITY,
+                        mask.see0(8 * j + 9) ? v[4 * j + 5] : -INFINITY);
+              b1 = max3(b1, mask.see1(8 * j + 8) ? v[4 * j + 6] : -INFINITY,
+                        mask.see1(8 * j + 9) ? v[4 * j + 7] : -INFINITY);
             }
           }
         }
@@ -807,11 +908,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j0 = 0; j0 < 16; j0 += 8) {
           uint32_t hi[16], lo[16];
           if (unmasked)
-            make_p<T, false>(v, j0, sl2, m0, m1, e0, e1, hi, lo, l0, l1);
+            make_p<T>(v, j0, sl2, m0, m1, SeeAll{}, hi, lo, l0, l1);
           else
-            make_p<T, true>(v, j0, sl2, m0, m1, e0, e1, hi, lo, l0, l1);
+            make_p<T>(v, j0, sl2, m0, m1, mask, hi, lo, l0, l1);
           tmem_st16x128_x8(s_addr + 4 * j0, hi);
           if constexpr (split_p<T>()) tmem_st16x128_x8(s_addr + 64 + 4 * j0, lo);
+        }
+      };
+      if (!lazy) {
+        if constexpr (kWindow) {
+          const unsigned n0 = lim0 - low0 + 1, n1 = lim1 - low1 + 1;
+          if (tile0 < p.sinks)
+            exact(SeeWindow<true>{e0, e1, low0 - key0, low1 - key0, p.sinks - key0, n0, n1});
+          else
+            exact(SeeWindow<false>{e0, e1, low0 - key0, low1 - key0, 0, n0, n1});
+        } else {
+          exact(SeeCausal{e0, e1});
         }
       }
       tmem_wait_st();
@@ -820,17 +932,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bar_p[buf]);
       ++tg;
     };
-    auto start_item = [&](const PfItem& x) {
+    auto start_item = [&](const Item& x) {
       take_item();
-      lim0 = min(x.pos0 + r0, x.L - 1);
-      lim1 = min(x.pos0 + r1, x.L - 1);
+      lim0 = min(x.pos0 + (kWindow ? r0 >> p.pack_log2 : r0), x.L - 1);
+      lim1 = min(x.pos0 + (kWindow ? r1 >> p.pack_log2 : r1), x.L - 1);
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;
       tile(0);
     };
     // the first item and its first tile
     ok = warp_wait(bar_qs, 0);
-    PfItem it = items[0];
+    it = items[0];
     if (ok && it.s >= 0) start_item(it);
     // After a failure (a wait gave up) every warp leaves at the next wait: no warp waits for another
     // softmax warp, and the other roles stop at their next wait too.
@@ -848,7 +960,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       //      this item's last P V.
       // (what the epilogue needs of this item is kept apart, and the next item becomes the current one)
       const int orow0 = it.q0 + it.tile0, oh = it.h;  // the tile's first output row, and its head
-      T* out0 = reinterpret_cast<T*>(p.out) + ((size_t)(orow0 + r0) * p.num_q_heads + oh) * kD;  // row r0
+      auto out_row = [&](int r) {
+        const size_t query = (size_t)orow0 + (kWindow ? r >> p.pack_log2 : r);
+        const int head = kWindow ? oh + (r & ((1 << p.pack_log2) - 1)) : oh;
+        return reinterpret_cast<T*>(p.out) + (query * p.num_q_heads + head) * kD;
+      };
       const int rows = it.rows;
       ok = warp_wait(bar_qs, (item_no + 1) & 1);
       it = items[(item_no + 1) & 1];
@@ -894,8 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = row_base + rl;
             if (r < rows) {
               const uint4 v = *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * kHalf + swz128(r, chunk & 7));
-              T* dst = reinterpret_cast<T*>(p.out) + ((size_t)(orow0 + r) * p.num_q_heads + oh) * kD + 8 * chunk;
-              *reinterpret_cast<uint4*>(dst) = v;
+              *reinterpret_cast<uint4*>(out_row(r) + 8 * chunk) = v;
             }
           }
         }
@@ -906,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // transpose within the quad (two xor-shuffle steps per group of 4 j) gives thread c the 16 bytes
         // of columns 8j .. 8j + 7 for j = 4g + c, so a store writes 16 bytes per thread and 64
         // contiguous bytes per row and quad.
-        T* out1 = out0 + (size_t)8 * p.num_q_heads * kD;  // row r1 = r0 + 8
+        T *out0 = out_row(r0), *out1 = out_row(r1);
         const bool hi2 = (c4 >> 1) != 0, odd = (c4 & 1) != 0;
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
@@ -961,9 +1076,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // one CTA per SM (the kernel holds all of tensor memory and most of shared memory), at most one per item
-cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
-                              const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
-  const long long items = (long long)p.num_seqs * p.num_q_heads * p.q_tiles;
+template <typename T, bool kWindow>
+static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+                                  const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
+  const long long items = (long long)p.num_seqs * (p.num_q_heads >> p.pack_log2) * p.q_tiles;
   if (items == 0) return cudaSuccess;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   int dev = 0, sms = 0;
@@ -971,19 +1087,23 @@ cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMa
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(items < sms ? items : sms);
-  if (dtype == PA_F16) {
-    e = cudaFuncSetAttribute(prefill_tc_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    prefill_tc_kernel<__half><<<grid, kThreads, kSmemBytes, stream>>>(tk, tv, tq, to, p);
-  } else if (dtype == PA_BF16) {
-    e = cudaFuncSetAttribute(prefill_tc_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemBytes);
-    if (e != cudaSuccess) return e;
-    prefill_tc_kernel<__nv_bfloat16><<<grid, kThreads, kSmemBytes, stream>>>(tk, tv, tq, to, p);
-  } else {
-    return cudaErrorInvalidValue;
-  }
+  auto kernel = prefill_tc_kernel<T, kWindow>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(tk, tv, tq, to, p);
   return cudaGetLastError();
+}
+
+cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+                              const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
+  const bool window = p.window > 0;
+  if (dtype == PA_F16)
+    return window ? launch_prefill<__half, true>(tk, tv, tq, to, p, stream)
+                  : launch_prefill<__half, false>(tk, tv, tq, to, p, stream);
+  if (dtype == PA_BF16)
+    return window ? launch_prefill<__nv_bfloat16, true>(tk, tv, tq, to, p, stream)
+                  : launch_prefill<__nv_bfloat16, false>(tk, tv, tq, to, p, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace pa

@@ -42,12 +42,6 @@ cudaError_t launch_window_rows_tc(int dtype, int head_size, const CUtensorMap& t
 cudaError_t launch_window_rows_fp8(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p,
                                    cudaStream_t stream);
 cudaError_t launch_window_rows_f32(int head_size, const WindowParams& p, cudaStream_t stream);
-// tq, to: q and out as [tokens][heads][D] in boxes of one query tile (128 rows: 128 / 2^pack_log2 tokens of
-// 2^pack_log2 heads of one kv head)
-cudaError_t launch_window_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
-                                     const CUtensorMap& to, const WindowParams& p, int pack_log2,
-                                     cudaStream_t stream);
-
 // Launch in clusters of `cluster` CTAs (1: none) as a programmatic dependent of the kernel before it (see
 // launch_dependent).
 template <typename... Params, typename... Args>

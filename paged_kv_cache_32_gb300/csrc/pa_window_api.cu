@@ -7,6 +7,7 @@
 #include <math.h>
 
 #include "pa.h"
+#include "pa_prefill.h"
 #include "pa_window.h"
 
 using namespace pa::host;
@@ -74,6 +75,53 @@ int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t st
     e = pa::launch_window_rows_tc(cache->dtype, cache->head_size, tk, tv, p, stream);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// The tile kernel's query heads of a tile: the largest power of two that divides the group (at most 128).
+int pack_log2(int G) {
+  int k = 0;
+  while (k < 7 && G % (2 << k) == 0) ++k;
+  return k;
+}
+
+// fp16 / bf16 caches of head size 128 whose blocks fit the 128-key tiles run on the tensor-core tile kernel
+bool tile_kernel_takes(const pa_cache_desc* c) {
+  return (c->dtype == PA_F16 || c->dtype == PA_BF16) && c->head_size == 128 && 128 % c->block_size == 0;
+}
+
+int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack, cudaStream_t stream) {
+  const long long q_tiles = ((long long)w.max_query_len + (128 >> pack) - 1) / (128 >> pack);
+  // work items are counted in int32, with room for one grid stride past the end
+  if ((long long)w.num_seqs * (w.num_q_heads >> pack) * q_tiles > kInt32Max - 4096) return PA_ERR_TOO_LARGE;
+  CUtensorMap tk, tv, tq, to;
+  if (!encode_cache_map(&tk, w.k_cache, cache, cache->block_size) ||
+      !encode_cache_map(&tv, w.v_cache, cache, cache->block_size) ||
+      !encode_query_map(&tq, w.q, cache, w.num_q_heads, w.num_query_tokens, 1 << pack) ||
+      !encode_query_map(&to, w.out, cache, w.num_q_heads, w.num_query_tokens, 1 << pack))
+    return PA_ERR_CUDA;
+  pa::PrefillParams p = {};
+  p.out = w.out;
+  p.q = w.q;
+  p.k_cache = w.k_cache;
+  p.v_cache = w.v_cache;
+  p.block_tables = w.block_tables;
+  p.seq_lens = w.seq_lens;
+  p.query_start = w.query_start;
+  p.err_flag = w.err_flag;
+  p.num_seqs = w.num_seqs;
+  p.num_q_heads = w.num_q_heads;
+  p.num_kv_heads = w.num_kv_heads;
+  p.max_blocks = w.max_blocks;
+  p.block_size = w.block_size;
+  p.num_blocks = w.num_blocks;
+  p.q_tiles = (int32_t)q_tiles;
+  p.num_query_tokens = w.num_query_tokens;
+  p.scale_log2 = w.scale_log2;
+  p.window = w.window;
+  p.sinks = w.sinks;
+  p.pack_log2 = pack;
+  p.max_query_len = w.max_query_len;
+  return pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa::WindowParams base_params(const pa_cache_desc* cache, void* out, const void* q, const void* k_cache,
@@ -172,6 +220,13 @@ int pa_prefill_window(void* out, const void* q, const void* k_cache, const void*
   p.query_start = query_start;
   p.num_query_tokens = num_query_tokens;
   p.max_query_len = max_query_len;
+  // The tile kernel takes chunks for which it reads the keys less often than the rows kernel would (once a query
+  // tile and head group, against once for eight rows).
+  const int G = num_q_heads / cache->num_kv_heads, pack = pack_log2(G);
+  const long long row_reads = ((long long)max_query_len * G + 7) / 8;
+  const long long tile_reads = ((long long)max_query_len + (128 >> pack) - 1) / (128 >> pack) * (G >> pack);
+  if (tile_kernel_takes(cache) && tile_reads < row_reads)
+    return launch_tiles(cache, p, pack, static_cast<cudaStream_t>(stream));
   return launch_rows(cache, p, static_cast<cudaStream_t>(stream));
 }
 
