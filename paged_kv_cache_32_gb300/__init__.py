@@ -308,51 +308,57 @@ def pa_copy_blocks(k_cache, v_cache, block_pairs, err_flag=None, stream=None, de
 
 
 # ---------------------------------------------------------------- rotary positions and windowed attention
-def _call_checks(cache, tensors, where: str):
-    """The checks that the sliding-window calls make of their tensors: each (tensor, name, dtype) has that dtype and
-    lies on the caches' device, or in pinned host memory."""
-    dev = cache.device
-    if not cache.is_cuda:
-        raise ValueError(f"{where}: the caches must be CUDA tensors")
-    for t, name, dtype in tensors:
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
-        if t.device != dev and not (t.device.type == "cpu" and t.is_pinned()):
-            raise ValueError(f"{where}: {name} is on {t.device}, the caches on {dev}")
+# A step makes one of these calls per layer, and a small one takes the GPU a few microseconds: the checks below
+# are kept to what finds a wrong argument, in the cheapest form.
+def _refuse(t, name: str, dtype, dev: int, where: str):
+    """Why ``t`` was refused (see _need)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev and not (t.device.type == "cpu" and t.is_pinned()):
+        raise ValueError(f"{where}: {name} is on {t.device}, the caches on cuda:{dev}")
 
 
-def _rows_dtype(cache):
-    """The type of queries, outputs and new rows for a cache: its own, fp16 for an FP8 cache."""
+def _need(t, name: str, dtype, dev: int, where: str) -> int:
+    """The address of a dense tensor of that type on device ``dev`` (or in pinned host memory)."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype, dev, where)
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _caches(k_cache, v_cache, desc, where: str):
+    """(device index, k address, v address, descriptor, dtype of queries and new rows) of a cache pair."""
     import torch
-    return torch.float16 if cache.element_size() == 1 else cache.dtype
-
-
-class _on_device:
-    """The stream to launch on, with the tensors' device current during the call."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _cache_checks(k_cache, v_cache, desc, where: str):
-    _dense(k_cache, "k_cache")
-    _dense(v_cache, "v_cache")
-    if v_cache.dtype != k_cache.dtype or v_cache.numel() != k_cache.numel() or v_cache.device != k_cache.device:
+    dev, dtype = k_cache.get_device(), k_cache.dtype
+    if dev < 0:
+        raise ValueError(f"{where}: the caches must be CUDA tensors")
+    if v_cache.dtype is not dtype or v_cache.numel() != k_cache.numel() or v_cache.get_device() != dev:
         raise ValueError(f"{where}: k_cache and v_cache must match in type, size and device")
-    return desc or cache_desc(k_cache)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError(f"{where}: the caches must be contiguous")
+    if desc is None:
+        desc = cache_desc(k_cache)
+    return dev, k_cache.data_ptr(), v_cache.data_ptr(), desc, torch.float16 if desc.dtype == PA_FP8_E4M3 else dtype
+
+
+def _launch(fn, args, dev: int, stream, where: str) -> None:
+    """fn on the arguments that args(stream) gives, with the tensors' device current."""
+    import torch
+    if torch.cuda.current_device() == dev:
+        status = fn(*args(_stream_of(dev, stream)))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args(_stream_of(dev, stream)))
+    if status != PA_OK:
+        raise PaError(status, where)
+
+
+def _stream_of(dev: int, stream) -> int:
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return int(getattr(stream, "cuda_stream", stream))
 
 
 def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, method: int = PA_ROPE_PLAIN, factor: float = 1.0,
@@ -375,14 +381,16 @@ def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, method: int = PA
     return (inv if device is None else inv.to(device)), mag.value
 
 
-def _token_stride(t, heads: int, d: int, name: str, where: str) -> int:
-    """Elements between the tokens of [tokens, heads, d]; a token's row is dense."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{where}: {name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
+def _token_rows(t, name: str, dtype, tokens: int, heads: int, d: int, dev: int, where: str):
+    """(address, elements between tokens) of [tokens, heads, d], where a token's row is dense."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype, dev, where)
+    if t.shape != (tokens, heads, d):
+        raise ValueError(f"{where}: {name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
         raise ValueError(f"{where}: the heads of one token of {name} must be dense")
-    return int(s[0]) if t.shape[0] > 1 else max(heads * d, 1)
+    return t.data_ptr(), (s0 if tokens > 1 else heads * d)
 
 
 def pa_rope_and_cache(q_out, k_cache, v_cache, q, key, value, positions, slot_mapping, inv_freq,
@@ -399,44 +407,44 @@ def pa_rope_and_cache(q_out, k_cache, v_cache, q, key, value, positions, slot_ma
     ``interleaved``: pairs (2j, 2j + 1), else (j, j + rotary_dim / 2)."""
     import torch
     where = "pa_rope_and_cache"
-    desc = _cache_checks(k_cache, v_cache, desc, where)
+    dev, kc, vc, desc, rows = _caches(k_cache, v_cache, desc, where)
+    d, hkv = desc.head_size, desc.num_kv_heads
+    tokens, hq, qp, op, qs, os_ = key.shape[0], 0, None, None, 0, 0
     if (q is None) != (q_out is None):
         raise ValueError(f"{where}: q and q_out go together")
-    rows = _rows_dtype(k_cache)
-    _call_checks(k_cache, ((q_out, "q_out", rows), (q, "q", rows), (key, "key", rows), (value, "value", rows),
-                           (positions, "positions", torch.int32), (slot_mapping, "slot_mapping", torch.int64),
-                           (inv_freq, "inv_freq", torch.float64), (err_flag, "err_flag", torch.int32)), where)
-    for t, n in ((positions, "positions"), (slot_mapping, "slot_mapping"), (inv_freq, "inv_freq")):
-        _dense(t, n)
-    d, hkv = desc.head_size, desc.num_kv_heads
-    tokens, hq = int(key.shape[0]), 0 if q is None else int(q.shape[1])
-    strides = [_token_stride(t, h, d, n, where) if t is not None else 0
-               for t, h, n in ((q_out, hq, "q_out"), (q, hq, "q"), (key, hkv, "key"), (value, hkv, "value"))]
-    for t, n in ((q_out, "q_out"), (q, "q"), (value, "value"), (positions, "positions"), (slot_mapping, "slot_mapping")):
-        if t is not None and t.shape[0] != tokens:
-            raise ValueError(f"{where}: {n} must hold {tokens} tokens")
-    with _on_device(k_cache.device, stream) as st:
-        status = lib().pa_rope_and_cache(_ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(q), _ptr(key), _ptr(value),
-                                         *strides, _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq), tokens, hq,
-                                         2 * inv_freq.numel(), int(bool(interleaved)), float(magnitude),
-                                         ctypes.byref(desc), float(k_scale or 0.0), float(v_scale or 0.0),
-                                         _ptr(err_flag), st)
-    _check(status, where)
+    if q is not None:
+        hq = q.shape[1]
+        qp, qs = _token_rows(q, "q", rows, tokens, hq, d, dev, where)
+        op, os_ = (qp, qs) if q_out is q else _token_rows(q_out, "q_out", rows, tokens, hq, d, dev, where)
+    kp, ks = _token_rows(key, "key", rows, tokens, hkv, d, dev, where)
+    vp, vs = _token_rows(value, "value", rows, tokens, hkv, d, dev, where)
+    pos = _need(positions, "positions", torch.int32, dev, where)
+    slots = _need(slot_mapping, "slot_mapping", torch.int64, dev, where)
+    inv = _need(inv_freq, "inv_freq", torch.float64, dev, where)
+    if positions.numel() != tokens or slot_mapping.numel() != tokens:
+        raise ValueError(f"{where}: positions and slot_mapping must hold {tokens} tokens")
+    err = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, dev, where)
+    _launch(lib().pa_rope_and_cache, lambda st: (
+        op, kc, vc, qp, kp, vp, os_, qs, ks, vs, pos, slots, inv, tokens, hq, 2 * inv_freq.numel(),
+        1 if interleaved else 0, float(magnitude), desc, float(k_scale or 0.0), float(v_scale or 0.0), err, st), dev,
+        stream, where)
 
 
-def _attention_checks(where, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc, *more):
+def _attention(where, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc):
+    """The checks of both windowed attention calls: (device, rows' dtype, descriptor, addresses, table shape)."""
     import torch
-    desc = _cache_checks(k_cache, v_cache, desc, where)
-    rows = _rows_dtype(k_cache)
-    _call_checks(k_cache, ((out, "out", rows), (q, "q", rows), (block_tables, "block_tables", torch.int32),
-                           (seq_lens, "seq_lens", torch.int32), (err_flag, "err_flag", torch.int32)) + more, where)
-    for t, n in ((out, "out"), (q, "q"), (block_tables, "block_tables"), (seq_lens, "seq_lens")):
-        _dense(t, n)
-    if q.dim() != 3 or q.shape[2] != desc.head_size or out.shape != q.shape:
+    dev, kc, vc, desc, rows = _caches(k_cache, v_cache, desc, where)
+    op, qp = _need(out, "out", rows, dev, where), _need(q, "q", rows, dev, where)
+    bt = _need(block_tables, "block_tables", torch.int32, dev, where)
+    sl = _need(seq_lens, "seq_lens", torch.int32, dev, where)
+    err = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, dev, where)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != desc.head_size or out.shape != shape:
         raise ValueError(f"{where}: q and out must be [queries, heads, {desc.head_size}]")
-    if block_tables.dim() != 2 or seq_lens.dim() != 1 or block_tables.shape[0] != seq_lens.shape[0]:
+    table = block_tables.shape
+    if len(table) != 2 or seq_lens.shape != table[:1]:
         raise ValueError(f"{where}: block_tables must be [num_seqs, max_blocks_per_seq], seq_lens [num_seqs]")
-    return desc
+    return dev, rows, desc, (op, qp, kc, vc), bt, sl, err, shape, table
 
 
 def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, window: int, num_sinks: int = 0,
@@ -450,27 +458,27 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, scale: fl
     (16-bit and FP8 caches).  No workspace."""
     import torch
     where = "pa_decode_window"
-    rows = _rows_dtype(k_cache)
-    desc = _attention_checks(where, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc,
-                             (key, "key", rows), (value, "value", rows), (alibi_slopes, "alibi_slopes", torch.float32))
-    num_seqs, num_q_heads = int(q.shape[0]), int(q.shape[1])
-    if seq_lens.shape[0] != num_seqs:
+    dev, rows, desc, ptrs, bt, sl, err, shape, table = _attention(where, out, q, k_cache, v_cache, block_tables,
+                                                                  seq_lens, err_flag, desc)
+    if table[0] != shape[0]:
         raise ValueError(f"{where}: one query per sequence")
-    for t, n in ((key, "key"), (value, "value")):
-        if t is not None and tuple(_dense(t, n).shape) != (num_seqs, desc.num_kv_heads, desc.head_size):
-            raise ValueError(f"{where}: {n} must be [{num_seqs}, {desc.num_kv_heads}, {desc.head_size}]")
-    if alibi_slopes is not None and _dense(alibi_slopes, "alibi_slopes").numel() != num_q_heads:
-        raise ValueError(f"{where}: one ALiBi slope per query head")
+    new = [None, None]
+    for i, (t, n) in enumerate(((key, "key"), (value, "value"))):
+        if t is not None:
+            new[i] = _need(t, n, rows, dev, where)
+            if t.shape != (shape[0], desc.num_kv_heads, desc.head_size):
+                raise ValueError(f"{where}: {n} must be [{shape[0]}, {desc.num_kv_heads}, {desc.head_size}]")
     opts = None
     if alibi_slopes is not None or k_scale is not None or v_scale is not None or test_flags:
-        opts = ctypes.byref(pa_decode_options(_ptr(alibi_slopes), float(k_scale or 0.0), float(v_scale or 0.0),
-                                              int(test_flags)))
-    with _on_device(k_cache.device, stream) as st:
-        status = lib().pa_decode_window(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(key), _ptr(value),
-                                        _ptr(block_tables), _ptr(seq_lens), num_seqs, num_q_heads,
-                                        int(block_tables.shape[1]), ctypes.byref(desc), float(scale), int(window),
-                                        int(num_sinks), _ptr(err_flag), st, opts)
-    _check(status, where)
+        slopes = None
+        if alibi_slopes is not None:
+            slopes = _need(alibi_slopes, "alibi_slopes", torch.float32, dev, where)
+            if alibi_slopes.numel() != shape[1]:
+                raise ValueError(f"{where}: one ALiBi slope per query head")
+        opts = pa_decode_options(slopes, float(k_scale or 0.0), float(v_scale or 0.0), int(test_flags))
+    _launch(lib().pa_decode_window, lambda st: (
+        *ptrs, *new, bt, sl, shape[0], shape[1], table[1], desc, float(scale), int(window), int(num_sinks), err, st, opts),
+        dev, stream, where)
 
 
 def pa_prefill_window(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_query_len: int, scale: float,
@@ -482,15 +490,11 @@ def pa_prefill_window(out, q, k_cache, v_cache, block_tables, seq_lens, query_st
     ``v_scale`` the scales of an FP8 cache (q and out are fp16 then)."""
     import torch
     where = "pa_prefill_window"
-    desc = _attention_checks(where, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc,
-                             (query_start, "query_start", torch.int32))
-    num_seqs = int(seq_lens.shape[0])
-    if tuple(_dense(query_start, "query_start").shape) != (num_seqs + 1,):
+    dev, rows, desc, ptrs, bt, sl, err, shape, table = _attention(where, out, q, k_cache, v_cache, block_tables,
+                                                                  seq_lens, err_flag, desc)
+    start = _need(query_start, "query_start", torch.int32, dev, where)
+    if query_start.shape != (table[0] + 1,):
         raise ValueError(f"{where}: query_start must be [num_seqs + 1]")
-    with _on_device(k_cache.device, stream) as st:
-        status = lib().pa_prefill_window(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                                         _ptr(seq_lens), _ptr(query_start), num_seqs, int(q.shape[0]), int(q.shape[1]),
-                                         int(block_tables.shape[1]), int(max_query_len), ctypes.byref(desc),
-                                         float(scale), int(window), int(num_sinks), float(k_scale or 0.0),
-                                         float(v_scale or 0.0), _ptr(err_flag), st)
-    _check(status, where)
+    _launch(lib().pa_prefill_window, lambda st: (
+        *ptrs, bt, sl, start, table[0], shape[0], shape[1], table[1], int(max_query_len), desc, float(scale), int(window),
+        int(num_sinks), float(k_scale or 0.0), float(v_scale or 0.0), err, st), dev, stream, where)
