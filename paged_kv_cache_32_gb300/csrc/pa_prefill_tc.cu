@@ -70,8 +70,13 @@
 //    map.  The queries of a tile then span 128 / P positions, so that fewer key
 //    tiles are cut by the window's edges, and a chunk of a few queries fills one
 //    tile a kv head instead of one a query head.
-//  * The key tiles of an item are those of [0, S) and of the window of its first
-//    row on, walked as one list (key_tile); rows whose window starts later mask.
+//  * An item's keys are the blocks of [0, S) and those from the window of its
+//    first row on, gathered side by side into key tiles: key x of the item is
+//    position x of the first part (x < xs), x + shift of the second.  Rows whose
+//    window starts later mask.  Gathering by blocks, not by 128-position tiles,
+//    keeps a few first tokens from taking a tile and the window's start from
+//    cutting one (16 chunks, W = 1024, S = 4, B = 16: 8.9 key tiles an item for
+//    10.3).
 //  * Blocks without a position that some query of the chunk sees are not read
 //    (they may have been released); their value rows read as zeros, as the rows
 //    past the sequence do.
@@ -439,7 +444,7 @@ __device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfItem&
 
 // An item of the windowed form: rows of 2^pack_log2 heads from h on, queries tile0 ..
 struct PfWindowItem : PfItem {
-  int n_sink, t_win;      // key tiles of [0, S), first key tile of the rest of the list
+  int xs, shift;          // keys x >= xs of the item are positions x + shift (a multiple of the block size)
   int lo_chunk, s_chunk;  // what some query of the chunk sees: [0, s_chunk) and from lo_chunk on
 };
 
@@ -469,17 +474,20 @@ __device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfWindo
   it.lo_chunk = max(0, it.L - it.n - p.window + 1);
   it.s_chunk = min(p.sinks, it.L);
   const int last = it.pos0 + queries - 1, lo = max(0, it.pos0 - p.window + 1);
-  it.n_sink = (min(p.sinks, last + 1) + kTile - 1) / kTile;
-  it.t_win = max(lo / kTile, it.n_sink);
-  it.key_tiles = it.n_sink + max(0, last / kTile + 1 - it.t_win);
+  const int sink_blocks = (min(p.sinks, last + 1) + B - 1) / B, win_block = max(lo / B, sink_blocks);
+  it.xs = sink_blocks * B;
+  it.shift = (win_block - sink_blocks) * B;
+  const int blocks = sink_blocks + max(0, last / B + 1 - win_block);
+  it.key_tiles = (blocks * B + kTile - 1) / kTile;
   return true;
 }
 
-// the t-th key tile of an item's list
-__device__ __forceinline__ int key_tile(const PfItem&, int t) { return t; }
-__device__ __forceinline__ int key_tile(const PfWindowItem& it, int t) {
-  return t < it.n_sink ? t : t - it.n_sink + it.t_win;
-}
+// position of the item's key x (of the block that starts there: x a multiple of B)
+__device__ __forceinline__ int key_pos(const PfItem&, int x) { return x; }
+__device__ __forceinline__ int key_pos(const PfWindowItem& it, int x) { return x < it.xs ? x : x + it.shift; }
+// positions are counted `shift` lower among an item's keys
+__device__ __forceinline__ int key_shift(const PfItem&) { return 0; }
+__device__ __forceinline__ int key_shift(const PfWindowItem& it) { return it.shift; }
 // may block positions pos .. pos + w - 1 hold a row that some query of the chunk sees; do they hold no other?
 __device__ __forceinline__ bool block_seen(const PfItem&, int, int) { return true; }
 __device__ __forceinline__ bool block_seen(const PfWindowItem& it, int pos, int w) {
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
       // the table entry of this lane's block, read one tile ahead
       auto fetch = [&](int kt) -> int {
-        const int bi = key_tile(it, kt) * blocks_per_tile + blk;
+        const int bi = kWindow ? key_pos(it, (kt * blocks_per_tile + blk) * B) / B : kt * blocks_per_tile + blk;
         return (blk < blocks_per_tile && kt < it.key_tiles && bi < it.nblocks_seq && block_seen(it, bi * B, B))
                    ? __ldg(table + bi)
                    : kPastEnd;
@@ -602,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool in_pool = entry >= 0 && entry < p.num_blocks;
         if (!is_v && half == 0 && entry != kPastEnd && !in_pool) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
         // V: only blocks entirely inside the sequence (and the window) go by tensor-map copy
-        const int first_pos = (key_tile(it, t) * blocks_per_tile + blk) * B;
+        const int first_pos = key_pos(it, (t * blocks_per_tile + blk) * B);
         const bool whole = in_pool && (!is_v || (first_pos + B <= it.L && block_whole(it, first_pos, B)));
         if (blk < blocks_per_tile) {
           if (whole) {
@@ -624,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int e = __shfl_sync(0xffffffffu, entry, b);
               if (!((partial >> b) & 1)) continue;
               const int r = r0 + (lane >> 3), chunk = lane & 7;
-              const int pos = key_tile(it, t) * kTile + r;
+              const int pos = key_pos(it, t * kTile + r);
               uint8_t* dst = st + swz128(r, chunk);
               if (pos < it.L && block_seen(it, pos, 1) && e >= 0 && e < p.num_blocks)
                 cp_async16(dst, cache + (((size_t)e * p.num_kv_heads + it.hkv) * B + (pos % B)) * kD + half * 64 +
@@ -792,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     int tg = 0, item_no = 0;
-    int lim0 = 0, lim1 = 0;                                    // last key position each row sees
+    int lim0 = 0, lim1 = 0;                                    // last key each row sees
     Item it = {};
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // reference maxima (log2 units), partial sums
     // key tile kt of the current item (this CTA's tile tg)
@@ -805,11 +813,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld16x256_x8(s_addr, v);
       tmem_ld16x256_x8(s_addr + 64, v + 32);
       tmem_wait_ld<64>(v);
-      const int tile0 = key_tile(it, kt) * kTile;    // first key
+      const int tile0 = kt * kTile;                  // first key
       const int key0 = tile0 + 2 * c4;               // key of this thread's pair 0
       const int e0 = lim0 - key0, e1 = lim1 - key0;  // pair j's keys 8j, 8j + 1 are visible up to e
-      // window: the first position of each row's window
-      const int low0 = kWindow ? max(0, lim0 - p.window + 1) : 0, low1 = kWindow ? max(0, lim1 - p.window + 1) : 0;
+      // window: the first key of each row's window
+      const int low0 = kWindow ? max(-key_shift(it), lim0 - p.window + 1) : 0;
+      const int low1 = kWindow ? max(-key_shift(it), lim1 - p.window + 1) : 0;
       const bool unmasked =
           __all_sync(0xffffffffu, min(lim0, lim1) >= tile0 + kTile - 1 &&
                                       (!kWindow || max(low0, low1) <= tile0 || tile0 + kTile <= p.sinks));
@@ -934,8 +943,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto start_item = [&](const Item& x) {
       take_item();
-      lim0 = min(x.pos0 + (kWindow ? r0 >> p.pack_log2 : r0), x.L - 1);
-      lim1 = min(x.pos0 + (kWindow ? r1 >> p.pack_log2 : r1), x.L - 1);
+      lim0 = min(x.pos0 + (kWindow ? r0 >> p.pack_log2 : r0), x.L - 1) - key_shift(x);
+      lim1 = min(x.pos0 + (kWindow ? r1 >> p.pack_log2 : r1), x.L - 1) - key_shift(x);
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.f;
       tile(0);

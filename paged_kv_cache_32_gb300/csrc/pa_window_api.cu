@@ -35,7 +35,8 @@ int check_window(const pa_cache_desc* cache, int32_t num_seqs, int32_t num_q_hea
   if (num_q_heads % cache->num_kv_heads != 0) return PA_ERR_INVALID_ARG;
   if (!(scale == scale) || isinf(scale)) return PA_ERR_INVALID_ARG;
   if (window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
-  if ((int64_t)max_blocks_per_seq * cache->block_size > kInt32Max) return PA_ERR_TOO_LARGE;
+  // positions are int32, with room for a key tile past the last one
+  if ((int64_t)max_blocks_per_seq * cache->block_size > kInt32Max - 4096) return PA_ERR_TOO_LARGE;
   return PA_OK;
 }
 
