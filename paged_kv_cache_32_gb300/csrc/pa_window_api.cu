@@ -47,6 +47,22 @@ int check_scales(const pa_cache_desc* cache, float* k_scale, float* v_scale) {
   return *k_scale > 0.f && !isinf(*k_scale) && *v_scale > 0.f && !isinf(*v_scale) ? PA_OK : PA_ERR_INVALID_ARG;
 }
 
+// A cache as (64 columns, rows, D / 64): a box of `rows` rows brings their 64-column parts one after the other
+bool encode_slab_map(CUtensorMap* map, const void* base, const pa_cache_desc* c, int rows) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint32_t parts = (cuuint32_t)(c->head_size / 64);
+  cuuint64_t dims[3] = {64, (cuuint64_t)c->num_blocks * c->num_kv_heads * c->block_size, parts};
+  cuuint64_t strides[2] = {(cuuint64_t)c->head_size * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)rows, parts};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt =
+      c->dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Launches the rows kernel of the cache's type; p.tiles (row groups) and p.cluster are set here.
 int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t stream) {
   const long long rows = (long long)p.max_query_len * (p.num_q_heads / p.num_kv_heads);
@@ -71,7 +87,7 @@ int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t st
     CUtensorMap tk, tv;
     // a slab is one 16-row box, or (8-token blocks) two 8-row boxes from two blocks
     const int box_rows = cache->block_size < pa::kTcSlabTokens ? cache->block_size : pa::kTcSlabTokens;
-    if (!encode_cache_map(&tk, p.k_cache, cache, box_rows) || !encode_cache_map(&tv, p.v_cache, cache, box_rows))
+    if (!encode_slab_map(&tk, p.k_cache, cache, box_rows) || !encode_slab_map(&tv, p.v_cache, cache, box_rows))
       return PA_ERR_CUDA;
     e = pa::launch_window_rows_tc(cache->dtype, cache->head_size, tk, tv, p, stream);
   }

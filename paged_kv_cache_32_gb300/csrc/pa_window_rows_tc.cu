@@ -11,6 +11,11 @@
 // weights enter the second one as two 16-bit terms (rounded part and residual:
 // a single fp16 term would add an error of the size of the output's own
 // rounding), which costs tensor work that the copies hide.
+//
+// A copy takes its issuing lane some 200 cycles, so a slab is two copies, one of
+// K and one of V: the tensor maps see a cache as (64 columns, rows, D / 64), and
+// a box brings a slab's rows of every 64-column part, one part after the other.
+// Blocks of 8 tokens (SPLIT) make a slab of two such boxes.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,7 +33,8 @@ struct RowsShape {
   static constexpr int KSTEPS = D / 16;                    // k-steps of Q K^T = m-tiles of V^T P^T
   static constexpr int NBOX = D / 64;                      // 128-byte (64-element) boxes per row
   static constexpr int BOX_BYTES = SB * 128;
-  static constexpr int SLAB_BYTES = 2 * NBOX * BOX_BYTES;  // K boxes, then V boxes
+  static constexpr int TILE_BYTES = NBOX * BOX_BYTES;      // the slab's rows of K, or of V
+  static constexpr int SLAB_BYTES = 2 * TILE_BYTES;        // K, then V
   static constexpr int RING_BYTES = NS * SLAB_BYTES;       // per warp
   static constexpr int OROW = D + 4;                       // merge row stride (floats): conflict-free stores
   static constexpr int BAR_OFF = NW * RING_BYTES;
@@ -41,15 +47,22 @@ struct RowsShape {
   static_assert(RING_BYTES >= (8 * OROW + 16) * 4, "a warp's ring holds its partial result at the end");
 };
 
+// Byte offset of 16-byte chunk c (8 columns) of row r in a slab's K or V tile: the 64-column parts one after the
+// other, in SPLIT slabs for rows 0..7 first and then for rows 8..15; 128-byte swizzle.
+template <int D, bool SPLIT>
+__device__ __forceinline__ uint32_t tile_chunk(uint32_t r, uint32_t c) {
+  constexpr uint32_t UP = SPLIT ? D / 64 * 1024 : 1024, PART = SPLIT ? 1024 : 2048;
+  return (r >> 3) * UP + (c >> 3) * PART + swz128(r & 7, c & 7);
+}
+
 // One slab: S^T = K Q^T, online softmax update, O^T += V^T P^T.  bias: slopes of the lane's two rows in log2
 // units; tok0: the slab's first token.
-template <typename T, int D>
+template <typename T, int D, bool SPLIT>
 __device__ __forceinline__ void window_slab(const uint8_t* kst, const uint8_t* vst, int tok0, const RowsItem& it,
                                             const uint32_t (&qf)[D / 16][2], float (&o)[D / 16][4], float& m_a,
                                             float& m_b, float& l_a, float& l_b, int lane, float sl2, float bias_a,
                                             float bias_b, int pos_a, int pos_b, int window) {
   constexpr int KSTEPS = D / 16;
-  constexpr int BOX_BYTES = kTcSlabTokens * 128;
   const int g = lane >> 2, q4 = lane & 3;
   float sc[4] = {0.f, 0.f, 0.f, 0.f};  // two accumulators: shorter dependency chain
   float sd[4] = {0.f, 0.f, 0.f, 0.f};
@@ -57,14 +70,14 @@ __device__ __forceinline__ void window_slab(const uint8_t* kst, const uint8_t* v
     const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
     const int khalf = lane >> 4;
 #pragma unroll
-    for (int jj = 0; jj < KSTEPS; ++jj) {
-      const uint32_t addr = smem_u32(kst + (jj >> 2) * BOX_BYTES) + swz128(row, (jj & 3) * 2 + khalf);
-      uint32_t a0, a1, a2, a3;
-      ldmatrix_x4(addr, a0, a1, a2, a3);
-      if (jj & 1)
-        Mma<T>::run(sd, a0, a1, a2, a3, qf[jj][0], qf[jj][1]);
-      else
-        Mma<T>::run(sc, a0, a1, a2, a3, qf[jj][0], qf[jj][1]);
+    for (int j0 = 0; j0 < KSTEPS; j0 += 4) {  // four loads on their way before the first is used
+      uint32_t f[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        ldmatrix_x4(smem_u32(kst) + tile_chunk<D, SPLIT>(row, (j0 + j) * 2 + khalf), f[j][0], f[j][1], f[j][2], f[j][3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        Mma<T>::run(j & 1 ? sd : sc, f[j][0], f[j][1], f[j][2], f[j][3], qf[j0 + j][0], qf[j0 + j][1]);
     }
   }
   // scores: (token g, row a = 2q4), (token g, row b = 2q4 + 1), (token g + 8, row a), (token g + 8, row b)
@@ -103,22 +116,24 @@ __device__ __forceinline__ void window_slab(const uint8_t* kst, const uint8_t* v
   const int row = (lane & 7) + (lane >> 4) * 8;
   const int dhalf = (lane >> 3) & 1;
 #pragma unroll
-  for (int i = 0; i < KSTEPS; ++i) {
-    const uint32_t addr = smem_u32(vst + (i >> 2) * BOX_BYTES) + swz128(row, (i & 3) * 2 + dhalf);
-    uint32_t a0, a1, a2, a3;
-    ldmatrix_x4_trans(addr, a0, a1, a2, a3);
+  for (int i0 = 0; i0 < KSTEPS; i0 += 4) {
+    uint32_t f[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      ldmatrix_x4_trans(smem_u32(vst) + tile_chunk<D, SPLIT>(row, (i0 + i) * 2 + dhalf), f[i][0], f[i][1], f[i][2],
+                        f[i][3]);
     if (!full) {
-      a0 &= mlo;
-      a1 &= mlo;
-      a2 &= mhi;
-      a3 &= mhi;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i][0] &= mlo, f[i][1] &= mlo, f[i][2] &= mhi, f[i][3] &= mhi;
     }
-    Mma<T>::run(o[i], a0, a1, a2, a3, pb0, pb1);
-    Mma<T>::run(o[i], a0, a1, a2, a3, pc0, pc1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Mma<T>::run(o[i0 + i], f[i][0], f[i][1], f[i][2], f[i][3], pb0, pb1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Mma<T>::run(o[i0 + i], f[i][0], f[i][1], f[i][2], f[i][3], pc0, pc1);
   }
 }
 
-template <typename T, int D, int NW, int NS>
+template <typename T, int D, int NW, int NS, bool SPLIT>
 __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
     window_rows_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                           const WindowParams p) {
@@ -151,7 +166,6 @@ __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
   const int mine = it.v1 - it.v0;
   const int n_my = mine > warp ? (mine - warp + NW - 1) / NW : 0;
   const int B = p.block_size;
-  const bool split = B < S::SB;  // 8-token blocks: a slab is two 8-row halves from two blocks
   const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
   auto slab_tok = [&](int k) { return rows_slab(it, it.v0 + warp + k * NW) * S::SB; };
   // lane l holds the table entries of this warp's slab 32 b + l: its block, or with 8-token blocks those of its
@@ -160,8 +174,8 @@ __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
     e0 = e1 = -1;
     if (k < n_my) {
       const int tok0 = slab_tok(k);
-      if (!split || rows_touch(it, tok0, B)) e0 = __ldg(table + tok0 / B);
-      if (split && rows_touch(it, tok0 + B, B)) e1 = __ldg(table + tok0 / B + 1);
+      if (!SPLIT || rows_touch(it, tok0, B)) e0 = __ldg(table + tok0 / B);
+      if (SPLIT && rows_touch(it, tok0 + B, B)) e1 = __ldg(table + tok0 / B + 1);
     }
   };
   int pb_batch = 0, pb_reg, pb_reg2;
@@ -176,32 +190,25 @@ __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
     const int pb = __shfl_sync(0xffffffffu, pb_reg, k & 31);
     const int pb2 = __shfl_sync(0xffffffffu, pb_reg2, k & 31);
     const int tok0 = slab_tok(k);
-    const bool has1 = !split || rows_touch(it, tok0, B), has2 = split && rows_touch(it, tok0 + B, B);
+    const bool has1 = !SPLIT || rows_touch(it, tok0, B), has2 = SPLIT && rows_touch(it, tok0 + B, B);
     const bool valid = (!has1 || (pb >= 0 && pb < p.num_blocks)) && (!has2 || (pb2 >= 0 && pb2 < p.num_blocks));
     const int stage = k % NS;
     valid_mask = valid ? (valid_mask | (1u << stage)) : (valid_mask & ~(1u << stage));
     if (lane == 0) {
       uint64_t* bar = &bars[stage];
       uint8_t* dst = ring + stage * S::SLAB_BYTES;
-      if (valid && !split) {
+      if (valid && !SPLIT) {
         const int y = (pb * p.num_kv_heads + it.hkv) * B + tok0 % B;  // first row
         mbar_arrive_expect_tx(bar, S::SLAB_BYTES);
-#pragma unroll
-        for (int b = 0; b < S::NBOX; ++b) tma_load_2d(dst + b * S::BOX_BYTES, &tmap_k, b * 64, y, bar);
-#pragma unroll
-        for (int b = 0; b < S::NBOX; ++b) tma_load_2d(dst + (S::NBOX + b) * S::BOX_BYTES, &tmap_v, b * 64, y, bar);
+        tma_load_3d(dst, &tmap_k, 0, y, 0, bar);
+        tma_load_3d(dst + S::TILE_BYTES, &tmap_v, 0, y, 0, bar);
       } else if (valid) {
-        // 8-row boxes: rows 8u .. 8u + 7 of each 16-row region come from block u, 1024 bytes apart, which keeps
-        // the 128-byte swizzle of a 16-row box.  Rows of a half that no row sees keep what they held: masked.
+        // rows 8u .. 8u + 7 come from block u; those of a half that no row sees keep what they held: masked
         mbar_arrive_expect_tx(bar, (has1 ? S::SLAB_BYTES / 2 : 0) + (has2 ? S::SLAB_BYTES / 2 : 0));
         for (int u = has1 ? 0 : 1; u < (has2 ? 2 : 1); ++u) {
           const int y = ((u ? pb2 : pb) * p.num_kv_heads + it.hkv) * B;
-#pragma unroll
-          for (int b = 0; b < S::NBOX; ++b)
-            tma_load_2d(dst + b * S::BOX_BYTES + u * (S::BOX_BYTES / 2), &tmap_k, b * 64, y, bar);
-#pragma unroll
-          for (int b = 0; b < S::NBOX; ++b)
-            tma_load_2d(dst + (S::NBOX + b) * S::BOX_BYTES + u * (S::BOX_BYTES / 2), &tmap_v, b * 64, y, bar);
+          tma_load_3d(dst + u * (S::TILE_BYTES / 2), &tmap_k, 0, y, 0, bar);
+          tma_load_3d(dst + S::TILE_BYTES + u * (S::TILE_BYTES / 2), &tmap_v, 0, y, 0, bar);
         }
       } else {
         report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
@@ -272,8 +279,7 @@ __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
           const int c = lane % CH, r = app_tok - tok0;
           asm volatile("cp.async.wait_all;" ::: "memory");
           const uint4 x = *reinterpret_cast<const uint4*>(stage_rows + 16 * lane);
-          uint8_t* tile = kst + (is_v ? S::NBOX * S::BOX_BYTES : 0);
-          *reinterpret_cast<uint4*>(tile + (c / 8) * S::BOX_BYTES + swz128(r, c % 8)) = x;
+          *reinterpret_cast<uint4*>(kst + (is_v ? S::TILE_BYTES : 0) + tile_chunk<D, SPLIT>(r, c)) = x;
           if (it.row0 == 0) {
             const int pb = __ldg(table + app_tok / B);  // in the pool: the slab is valid
             const size_t dst = (((size_t)pb * p.num_kv_heads + it.hkv) * B + app_tok % B) * CH + c;
@@ -283,8 +289,8 @@ __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
         }
         __syncwarp();
       }
-      window_slab<T, D>(kst, kst + S::NBOX * S::BOX_BYTES, tok0, it, qf, o, m_a, m_b, l_a, l_b, lane, p.scale_log2,
-                        bias_a, bias_b, pos_a, pos_b, p.window);
+      window_slab<T, D, SPLIT>(kst, kst + S::TILE_BYTES, tok0, it, qf, o, m_a, m_b, l_a, l_b, lane, p.scale_log2,
+                               bias_a, bias_b, pos_a, pos_b, p.window);
     }
     __syncwarp();
     if (k + NS < n_my) issue(k + NS);
@@ -325,24 +331,33 @@ __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
                                                     reinterpret_cast<float*>(smem + S::MINE_OFF));
 }
 
-template <typename T, int D, int NW, int NS>
+template <typename T, int D, int NW, int NS, bool SPLIT>
 cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const WindowParams& p, cudaStream_t stream) {
   using S = RowsShape<D, NW, NS>;
-  auto kernel = window_rows_tc_kernel<T, D, NW, NS>;
+  auto kernel = window_rows_tc_kernel<T, D, NW, NS, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
                         p.cluster, stream, tk, tv, p);
 }
 
+template <typename T>
+cudaError_t launch_type(int head_size, const CUtensorMap& tk, const CUtensorMap& tv, const WindowParams& p,
+                        cudaStream_t stream) {
+  const bool split = p.block_size < kTcSlabTokens;
+  if (head_size == 128)
+    return split ? launch_rows<T, 128, 4, 2, true>(tk, tv, p, stream) : launch_rows<T, 128, 4, 2, false>(tk, tv, p, stream);
+  if (head_size == 64)
+    return split ? launch_rows<T, 64, 4, 4, true>(tk, tv, p, stream) : launch_rows<T, 64, 4, 4, false>(tk, tv, p, stream);
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 cudaError_t launch_window_rows_tc(int dtype, int head_size, const CUtensorMap& tk, const CUtensorMap& tv,
                                   const WindowParams& p, cudaStream_t stream) {
-  if (dtype == PA_F16 && head_size == 128) return launch_rows<__half, 128, 4, 2>(tk, tv, p, stream);
-  if (dtype == PA_F16 && head_size == 64) return launch_rows<__half, 64, 4, 4>(tk, tv, p, stream);
-  if (dtype == PA_BF16 && head_size == 128) return launch_rows<__nv_bfloat16, 128, 4, 2>(tk, tv, p, stream);
-  if (dtype == PA_BF16 && head_size == 64) return launch_rows<__nv_bfloat16, 64, 4, 4>(tk, tv, p, stream);
+  if (dtype == PA_F16) return launch_type<__half>(head_size, tk, tv, p, stream);
+  if (dtype == PA_BF16) return launch_type<__nv_bfloat16>(head_size, tk, tv, p, stream);
   return cudaErrorInvalidValue;
 }
 
