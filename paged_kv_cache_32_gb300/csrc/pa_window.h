@@ -22,7 +22,8 @@ struct WindowParams {
   int32_t max_query_len;        // bound on a sequence's queries (1 without query_start)
   int32_t window, sinks;        // >= 1, >= 0
   int32_t tiles;                // row groups (8 rows) or query tiles of a sequence's kv head in the grid
-  int32_t cluster;              // CTAs that share one item's keys (rows kernels)
+  int32_t cluster;              // rows kernels: CTAs that share one item's keys,
+  int32_t warps;                // and warps of a CTA (3, 4 or 6; fp32: 4)
   float scale_log2;             // scale * log2(e)
   const float* alibi;           // nullable [Hq]: score_i += slope_h * (i - p)
   float k_scale, v_scale;       // FP8 caches
@@ -34,7 +35,7 @@ struct WindowParams {
   void* v_cache_out;
 };
 
-// CTAs of a rows launch, and its cluster size (also used by the launchers' callers to bound the grid)
+// items of a rows launch: eight query rows of one kv head each
 inline long long window_items(const WindowParams& p) { return (long long)p.num_seqs * p.num_kv_heads * p.tiles; }
 
 cudaError_t launch_window_rows_tc(int dtype, int head_size, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -14,16 +14,39 @@ using namespace pa::host;
 
 namespace {
 
-constexpr int kMaxCluster = 8;    // the portable cluster size
-constexpr int kFillCtas = 912;    // CTAs that fill 152 SMs with three resident CTAs twice
-constexpr int kMinCtaTokens = 128;  // tokens of a CTA below which a split no longer pays
+constexpr int kSms = 152;
+constexpr int kMaxCluster = 8;     // the portable cluster size
+constexpr int kMinCtaTokens = 64;  // tokens of a CTA below which a split no longer pays
 
-// CTAs that share one item's keys: doubled while the grid would leave SMs idle and each CTA keeps some slabs
-// for its four warps.
-int cluster_size(long long items, long long max_keys) {
-  int c = 1;
-  while (c < kMaxCluster && items * c < kFillCtas && max_keys / (2 * c) >= kMinCtaTokens) c *= 2;
-  return c;
+// How the rows kernels spread over the SMs.  A warp holds 16 KB of slabs, so an SM takes 4 CTAs of 3 warps, 3 of 4
+// or 2 of 6.
+//  * Few items (at most half the SMs): CTAs of 6 warps, an item's keys split over a cluster until the CTAs fill the
+//    SMs twice.  One sequence, 8 kv heads, 4096 keys: 10.8 us (clusters of 4: 15.4; 4 warps: 12.4); 64 items of
+//    4096 keys: 27.1 us (4 warps: 29.4; clusters of 2: 29.2).
+//  * More: no split (a cluster waits for as many free places at once: two of 4 warps cost 94 -> 109 us on 1024
+//    items of 1024 keys), and the CTA size whose last round is fullest, the smallest among equals.  1024 keys:
+//    256 items 26.6 / 27.9 / 28.7 us with 6 / 4 / 3 warps, 384 items 42.8 / 37.4 / 38.7, 512 items 48.6 / 58.0 /
+//    48.3, 768 items 69.9 / 67.8 / 74.5, 1024 items 92.2 / 93.4 / 87.9.
+//    (Splitting long items in two all the same evens out a last round of unequal contexts, 96 FP8 sequences of
+//    2500 to 40000 tokens with a window of 8192: 240 -> 226 us, and costs as much when they are equal, 246 -> 264.)
+void spread(long long items, long long max_keys, pa::WindowParams& p) {
+  p.cluster = 1;
+  if (items <= kSms / 2) {
+    p.warps = 6;
+    while (p.cluster < kMaxCluster && items * p.cluster * 2 <= 2 * kSms &&
+           max_keys / (2 * p.cluster) >= kMinCtaTokens)
+      p.cluster *= 2;
+    return;
+  }
+  double best = 0.0;
+  for (int warps : {3, 4, 6}) {
+    const double rounds = (double)items / (kSms * (12 / warps));
+    const double full = rounds / ceil(rounds);
+    if (full > best + 1e-9) {
+      best = full;
+      p.warps = warps;
+    }
+  }
 }
 
 // Checks that both entry points share.
@@ -63,7 +86,7 @@ bool encode_slab_map(CUtensorMap* map, const void* base, const pa_cache_desc* c,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launches the rows kernel of the cache's type; p.tiles (row groups) and p.cluster are set here.
+// Launches the rows kernel of the cache's type; p.tiles (row groups), p.cluster and p.warps are set here.
 int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t stream) {
   const long long rows = (long long)p.max_query_len * (p.num_q_heads / p.num_kv_heads);
   if (rows > kInt32Max - 8) return PA_ERR_TOO_LARGE;
@@ -72,7 +95,8 @@ int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t st
   const long long cap = (long long)p.max_blocks * p.block_size;
   const long long reach = (long long)p.window + p.sinks + 8;
   const long long items = pa::window_items(p);
-  p.cluster = cluster_size(items, reach < cap ? reach : cap);
+  spread(items, reach < cap ? reach : cap, p);
+  if (cache->dtype == PA_F32) p.warps = 4;
   if (items * p.cluster > kInt32Max) return PA_ERR_TOO_LARGE;
   cudaError_t e;
   if (cache->dtype == PA_F32) {

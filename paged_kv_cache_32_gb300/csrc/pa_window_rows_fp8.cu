@@ -360,14 +360,23 @@ __global__ void __launch_bounds__(RowsFp8Shape<D, NW, NS>::THREADS)
 
 }  // namespace
 
-cudaError_t launch_window_rows_fp8(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p,
-                                   cudaStream_t stream) {
-  using S = RowsFp8Shape<128, 4, 2>;
-  auto kernel = window_rows_fp8_kernel<128, 4, 2>;
+template <int NW>
+static cudaError_t launch_warps(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p,
+                                cudaStream_t stream) {
+  using S = RowsFp8Shape<128, NW, 2>;
+  auto kernel = window_rows_fp8_kernel<128, NW, 2>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
                         p.cluster, stream, tk, tk32, p);
+}
+
+cudaError_t launch_window_rows_fp8(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p,
+                                   cudaStream_t stream) {
+  if (p.warps == 3) return launch_warps<3>(tk, tk32, p, stream);
+  if (p.warps == 4) return launch_warps<4>(tk, tk32, p, stream);
+  if (p.warps == 6) return launch_warps<6>(tk, tk32, p, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace pa

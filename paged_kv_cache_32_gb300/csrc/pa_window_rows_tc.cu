@@ -341,14 +341,23 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Wind
                         p.cluster, stream, tk, tv, p);
 }
 
+template <typename T, int D, int NS, bool SPLIT>
+cudaError_t launch_warps(const CUtensorMap& tk, const CUtensorMap& tv, const WindowParams& p, cudaStream_t stream) {
+  if (p.warps == 3) return launch_rows<T, D, 3, NS, SPLIT>(tk, tv, p, stream);
+  if (p.warps == 4) return launch_rows<T, D, 4, NS, SPLIT>(tk, tv, p, stream);
+  if (p.warps == 6) return launch_rows<T, D, 6, NS, SPLIT>(tk, tv, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+// two slabs a warp (four of head size 64): a deeper ring leaves fewer warps an SM and gained nothing
 template <typename T>
 cudaError_t launch_type(int head_size, const CUtensorMap& tk, const CUtensorMap& tv, const WindowParams& p,
                         cudaStream_t stream) {
   const bool split = p.block_size < kTcSlabTokens;
   if (head_size == 128)
-    return split ? launch_rows<T, 128, 4, 2, true>(tk, tv, p, stream) : launch_rows<T, 128, 4, 2, false>(tk, tv, p, stream);
+    return split ? launch_warps<T, 128, 2, true>(tk, tv, p, stream) : launch_warps<T, 128, 2, false>(tk, tv, p, stream);
   if (head_size == 64)
-    return split ? launch_rows<T, 64, 4, 4, true>(tk, tv, p, stream) : launch_rows<T, 64, 4, 4, false>(tk, tv, p, stream);
+    return split ? launch_warps<T, 64, 4, true>(tk, tv, p, stream) : launch_warps<T, 64, 4, false>(tk, tv, p, stream);
   return cudaErrorInvalidValue;
 }
 
