@@ -26,6 +26,8 @@ struct PrefillParams {
   // kv head
   int32_t window, sinks, pack_log2;
   int32_t max_query_len;        // windowed form: bound on a chunk's queries
+  // windowed form over an FP8 cache: a value code's scale (the key codes' is part of scale_log2)
+  float v_scale;
 };
 
 namespace host {
@@ -36,6 +38,7 @@ bool encode_query_map(CUtensorMap* map, const void* base, const pa_cache_desc* c
 // tk, tv: the caches as rows of D elements (box 64 columns x block_size rows, 128-byte swizzle);
 // tq: q as [tokens][heads][D] (box 64 columns x 1 head x 128 tokens, windowed 2^pack_log2 heads x the tile's
 // tokens, 128-byte swizzle); to: out, the same
+// dtype: the cache's (FP8: windowed form only, tk and tv not used)
 cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                               const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream);
 

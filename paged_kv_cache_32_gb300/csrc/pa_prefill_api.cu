@@ -23,7 +23,7 @@ bool encode_query_map(CUtensorMap* map, const void* base, const pa_cache_desc* c
   cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)(128 / heads)};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType dt =
-      c->dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+      c->dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   return enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -87,6 +87,7 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
   p.scale_log2 = scale * 1.4426950408889634f;
   p.window = p.sinks = p.pack_log2 = 0;  // the plain form
   p.max_query_len = max_query_len;
+  p.v_scale = 1.f;
   cudaError_t e = pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

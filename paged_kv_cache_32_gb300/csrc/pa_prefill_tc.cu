@@ -80,6 +80,11 @@
 //  * Blocks without a position that some query of the chunk sees are not read
 //    (they may have been released); their value rows read as zeros, as the rows
 //    past the sequence do.
+//  * FP8 caches (kFp8, fp16 queries): the producers load the codes into registers
+//    a tile ahead, convert them to fp16 (exact) and store the swizzled tiles
+//    themselves.  Values lie in the cache with a dimension's 16 tokens side by
+//    side, so the value tile is V^T, rows of 64 keys, and P V takes it like S
+//    takes K.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -90,6 +95,7 @@
 
 #include "pa.h"
 #include "pa_device.cuh"
+#include "pa_fp8.cuh"
 #include "pa_internal.h"
 #include "pa_prefill.h"
 
@@ -498,12 +504,138 @@ __device__ __forceinline__ bool block_whole(const PfWindowItem& it, int pos, int
   return pos >= it.lo_chunk || pos + w <= it.s_chunk;
 }
 
+// 16 codes, or zeros; volatile, so that the load stays where it is issued, a tile before its use (as an ordinary
+// load it was moved down to it, and every tile waited for its 16 loads one after the other)
+__device__ __forceinline__ uint4 load_codes(const uint8_t* src, bool take) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(src), "r"((int)take));
+  return v;
+}
+
+// A producer warp over an FP8 cache: of every tile, warps 0..3 take the keys 32 w .. 32 w + 31 of K (a lane 16 of a
+// row's 128 codes), warps 4..7 the same keys of V (a lane the 16 tokens of a group at one dimension).  A warp alone
+// on its scheduler takes some six cycles an instruction, hence eight warps; a group's loads for the next tile are issued when its present codes are stored.
+// `bar` counts the filled stages, `freed` the MMAs that have read a tile (one phase per tile held by an S buffer).
+constexpr int kFp8Producers = 8;
+constexpr int kFp8LoadWarp0 = kSoftmaxWarps + 4;  // (whole warpgroups share a register limit: two warps idle)
+constexpr int kFp8Threads = (kFp8LoadWarp0 + kFp8Producers) * 32;
+// Registers: 20 warps are launched with 96 a thread (five warps a scheduler); the softmax warps, which hold a row's
+// 64 scores, take what the producers give back.  16 chunks of 256-1024 tokens, W = 1024: 329 us with 120 / 72
+// registers for softmax / producers, 397 with 112 / 80, 461 with 128 / 64 (the producers spill), 512 with 96 for
+// all, 804 with four producer warps at 128.
+constexpr int kFp8LaunchRegs = 96, kFp8SoftmaxRegs = 120, kFp8LoadRegs = 72;
+static_assert(8 * 32 * kFp8SoftmaxRegs + 4 * 32 * kFp8LaunchRegs + kFp8Producers * 32 * kFp8LoadRegs <=
+                  kFp8Threads * kFp8LaunchRegs,
+              "a raised limit waits for registers that the launch does not have");
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, int lane, int n_items, uint8_t* ring,
+                                             uint64_t* bar, uint64_t* freed, volatile int* abort_flag) {
+  constexpr int kPastEnd = INT_MIN, kLoads = 8;  // loads of a lane and tile: two groups of 16 keys x 4
+  const bool is_v = role >= kFp8Producers / 2;
+  const int w = role & 3, B = p.block_size, log2_b = __ffs(B) - 1, blocks_per_tile = kTile / B;
+  // this lane's place in a group: K: row 4 i + lane / 8, codes 16 (lane % 8) ..; V: dimension 32 i + lane
+  const uint8_t* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + lane * 16;
+  int tg = 0;
+  bool ok = true;
+  for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+    PfWindowItem it;
+    if (!pf_item(p, idx, it, false)) continue;
+    const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
+    // lane b < blocks_per_tile: the table entry of the tile's block b
+    auto fetch = [&](int kt) -> int {
+      const int bi = key_pos(it, (kt * blocks_per_tile + lane) * B) >> log2_b;
+      return (lane < blocks_per_tile && kt < it.key_tiles && bi < it.nblocks_seq && block_seen(it, bi * B, B))
+                 ? __ldg(table + bi)
+                 : kPastEnd;
+    };
+    uint4 raw[kLoads];
+    // the table entries of a tile, -1 outside the pool
+    auto checked = [&](int entry) {
+      const bool in_pool = entry >= 0 && entry < p.num_blocks;
+      if (role == 0 && entry != kPastEnd && !in_pool) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+      return in_pool ? entry : -1;
+    };
+    auto load = [&](int entry, int g) {
+      const int key0 = 32 * w + 16 * g;  // the group lies in one block
+      const int e = __shfl_sync(0xffffffffu, entry, key0 >> log2_b);
+      // 16 tokens of one head: 2 KB side by side, rows of K or [D][16] of V
+      const uint8_t* src = cache + (((size_t)(e * p.num_kv_heads + it.hkv) << log2_b) + (key0 & (B - 1))) * kD;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[4 * g + i] = load_codes(src + 512 * i, e >= 0);
+    };
+    const int first = checked(fetch(0));
+    load(first, 0);
+    load(first, 1);
+    int entry = fetch(1);
+    for (int t = 0; t < it.key_tiles; ++t, ++tg) {
+      const int ahead = checked(entry);  // of the next tile
+      entry = fetch(t + 2);
+      if (tg >= 2) ok = __all_sync(0xffffffffu, wait_bar(&freed[(tg - 2) % kSBufs], ((tg - 2) / kSBufs) & 1, abort_flag));
+      if (!ok) break;
+      uint8_t* st = ring + (tg & 1) * 2 * kHalf;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+        if (is_v) {
+          // values of tokens that no query of the chunk sees may be NaN codes: zeros
+          const int pos = key_pos(it, t * kTile + 32 * w + 16 * g);
+          if (!(pos + 16 <= it.L && block_whole(it, pos, 16))) {
+            const int mine = pos + (lane & 15);
+            const unsigned some = __ballot_sync(0xffffffffu, mine < it.L && block_seen(it, mine, 1));
+            // a word's four tokens: bit b of the nibble -> byte b
+#pragma unroll
+            for (int i = 0; i < 4; ++i) keep[i] = ((((some >> (4 * i)) & 15u) * 0x00204081u) & 0x01010101u) * 0xffu;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 c = raw[4 * g + i];
+          uint4 a, b;
+          codes_to_half(c.x & keep[0], a.x, a.y);
+          codes_to_half(c.y & keep[1], a.z, a.w);
+          codes_to_half(c.z & keep[2], b.x, b.y);
+          codes_to_half(c.w & keep[3], b.z, b.w);
+          if (is_v) {
+            // V^T: row = dimension, 64 keys a half
+            uint8_t* half = st + (w >> 1) * kHalf;
+            const int chunk = 4 * (w & 1) + 2 * g;
+            *reinterpret_cast<uint4*>(half + swz128(32 * i + lane, chunk)) = a;
+            *reinterpret_cast<uint4*>(half + swz128(32 * i + lane, chunk + 1)) = b;
+          } else {
+            // the upper four lanes of a row, whose chunks fall into the banks of the lower four, swap their stores
+            const int r = 32 * w + 16 * g + 4 * i + (lane >> 3), up = (lane >> 2) & 1, chunk = 2 * (lane & 3);
+            uint8_t* half = st + up * kHalf;
+            *reinterpret_cast<uint4*>(half + swz128(r, chunk + up)) = up ? b : a;
+            *reinterpret_cast<uint4*>(half + swz128(r, chunk + 1 - up)) = up ? a : b;
+          }
+        }
+        if (t + 1 < it.key_tiles) load(ahead, g);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic writes -> tensor-core reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[tg & 1]);
+    }
+  }
+}
+
 // Persistent: each CTA takes items blockIdx.x, blockIdx.x + gridDim.x, ...  Every role walks the same
 // items; the K/V rings, the S buffers and their barriers run on across items (tg counts this CTA's
 // key tiles so far), so the next item's Q, K/V copies and first S MMAs overlap this item's last
 // P V and epilogue.
-template <typename T, bool kWindow>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, bool kWindow, bool kFp8>
+__global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                       const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_out,
                       const PrefillParams p) {
@@ -540,8 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(bar_q, kSoftmaxWarps);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&bar_k[b], slots);      // each copy slot arrives once per tile (with its bytes, or none)
-      mbar_init(&bar_v[b], slots + 2);  // + each V producer's partial-block / zero-fill arrival
+      // each copy slot arrives once per tile (with its bytes, or none); FP8: each producer warp
+      mbar_init(&bar_k[b], kFp8 ? kFp8Producers / 2 : slots);
+      mbar_init(&bar_v[b], kFp8 ? kFp8Producers / 2 : slots + 2);  // + each V producer's partial-block / zero-fill arrival
     }
     for (int b = 0; b < kSBufs; ++b) {
       mbar_init(&bar_s[b], 1);
@@ -570,7 +703,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
   };
 
-  if (warp >= kLoadWarp0) {
+  if (kFp8 && warp >= kSoftmaxWarps + 2) {
+    // =================================================================== producers over an FP8 cache
+    if (warp >= kFp8LoadWarp0) {
+      regs_dec<kFp8LoadRegs>();
+      const bool v = warp >= kFp8LoadWarp0 + kFp8Producers / 2;
+      fp8_producer(p, warp - kFp8LoadWarp0, lane, n_items, smem + (v ? kVOff : kKOff), v ? bar_v : bar_k,
+                   v ? bar_o : bar_s, abort_flag);
+    }
+  } else if (!kFp8 && warp >= kLoadWarp0) {
     // =================================================================== producers: one half of K or V tiles
     const bool is_v = warp >= kLoadWarp0 + 2;
     const int half = (warp - kLoadWarp0) & 1;  // columns 64 half .. 64 half + 63
@@ -725,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kPVWarp) {
     // =================================================================== O += P V issuer
     if (lane == 0) {
-      const uint32_t id_o = idesc<T>(1);
+      const uint32_t id_o = idesc<T>(kFp8 ? 0 : 1);  // FP8 caches: V^T, rows of 64 keys
       bool ok = true;
       int tg = 0, item_no = 0;
       int prev_row0 = 0, prev_h = 0;  // the previous item's output tile
@@ -761,7 +902,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int part = 0; part < (split_p<T>() ? 2 : 1); ++part) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_ts(tmem + kOCol, tmem + buf * 128 + part * 64 + kk * 8, sw128_desc(vb + kk * 2048, kHalf, 1024),
+              mma_ts(tmem + kOCol, tmem + buf * 128 + part * 64 + kk * 8,
+                     kFp8 ? sw128_desc(vb + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024)
+                          : sw128_desc(vb + kk * 2048, kHalf, 1024),
                      id_o, kt > 0 || part > 0 || kk > 0);
           }
           mma_commit(&bar_o[buf]);
@@ -786,6 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // =================================================================== softmax warps
+    if constexpr (kFp8) regs_inc<kFp8SoftmaxRegs>();
     // Warp w owns the 16 query rows (tensor-memory lanes) 32 (w % 4) + 16 (w / 4) .. + 15 of the tile,
     // all 128 key columns: thread t holds rows r0 = base + t / 4 and r1 = r0 + 8, keys 8j + 2 (t % 4)
     // and + 1 (j = 0..15), so a row's maximum and sum take two shuffles among its four threads.
@@ -991,7 +1135,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_ofree);
-      const float inv0 = s0 > 0.f ? 1.f / s0 : 0.f, inv1 = s1 > 0.f ? 1.f / s1 : 0.f;
+      const float unit = kFp8 ? p.v_scale : 1.f;
+      const float inv0 = s0 > 0.f ? unit / s0 : 0.f, inv1 = s1 > 0.f ? unit / s1 : 0.f;
       if constexpr (kStagedOut<T>) {
         // The tile goes to the stage, in the 128-byte-swizzled layout of the output's tensor map (row r's
         // 16-byte chunk k of column half h at h * kHalf + swz128(r, k)).  Thread c of a quad writes bytes
@@ -1066,7 +1211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a wait expired (the flag is stable: every thread has left its loop): record it, and let the
     // copies and MMAs this CTA started finish, each wait bounded, before its memory is released
     if (threadIdx.x == 0) report_error(p.err_flag, PA_DEVERR_TIMEOUT);
-    if (warp >= kLoadWarp0 && lane == 0) {  // copies still landing
+    if (!kFp8 && warp >= kLoadWarp0 && lane == 0) {  // copies still landing
       uint64_t* ring_bar = warp >= kLoadWarp0 + 2 ? bar_v : bar_k;
       for (int t = max(0, n_issued - 2); t < n_issued; ++t) drain_wait(&ring_bar[t & 1], (t >> 1) & 1);
     }
@@ -1085,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // one CTA per SM (the kernel holds all of tensor memory and most of shared memory), at most one per item
-template <typename T, bool kWindow>
+template <typename T, bool kWindow, bool kFp8 = false>
 static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                   const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
   const long long items = (long long)p.num_seqs * (p.num_q_heads >> p.pack_log2) * p.q_tiles;
@@ -1096,10 +1241,10 @@ static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, 
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)(items < sms ? items : sms);
-  auto kernel = prefill_tc_kernel<T, kWindow>;
+  auto kernel = prefill_tc_kernel<T, kWindow, kFp8>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, kSmemBytes, stream>>>(tk, tv, tq, to, p);
+  kernel<<<grid, kFp8 ? kFp8Threads : kThreads, kSmemBytes, stream>>>(tk, tv, tq, to, p);
   return cudaGetLastError();
 }
 
@@ -1112,6 +1257,7 @@ cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMa
   if (dtype == PA_BF16)
     return window ? launch_prefill<__nv_bfloat16, true>(tk, tv, tq, to, p, stream)
                   : launch_prefill<__nv_bfloat16, false>(tk, tv, tq, to, p, stream);
+  if (dtype == PA_FP8_E4M3 && window) return launch_prefill<__half, true, true>(tk, tv, tq, to, p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -125,9 +125,9 @@ int pack_log2(int G) {
   return k;
 }
 
-// fp16 / bf16 caches of head size 128 whose blocks fit the 128-key tiles run on the tensor-core tile kernel
+// 16-bit and FP8 caches of head size 128 whose blocks fit the 128-key tiles run on the tensor-core tile kernel
 bool tile_kernel_takes(const pa_cache_desc* c) {
-  return (c->dtype == PA_F16 || c->dtype == PA_BF16) && c->head_size == 128 && 128 % c->block_size == 0;
+  return c->dtype != PA_F32 && c->head_size == 128 && 128 % c->block_size == 0;
 }
 
 int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack, cudaStream_t stream) {
@@ -135,8 +135,9 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   // work items are counted in int32, with room for one grid stride past the end
   if ((long long)w.num_seqs * (w.num_q_heads >> pack) * q_tiles > kInt32Max - 4096) return PA_ERR_TOO_LARGE;
   CUtensorMap tk, tv, tq, to;
-  if (!encode_cache_map(&tk, w.k_cache, cache, cache->block_size) ||
-      !encode_cache_map(&tv, w.v_cache, cache, cache->block_size) ||
+  const bool fp8 = cache->dtype == PA_FP8_E4M3;  // read by plain loads
+  if ((!fp8 && (!encode_cache_map(&tk, w.k_cache, cache, cache->block_size) ||
+                !encode_cache_map(&tv, w.v_cache, cache, cache->block_size))) ||
       !encode_query_map(&tq, w.q, cache, w.num_q_heads, w.num_query_tokens, 1 << pack) ||
       !encode_query_map(&to, w.out, cache, w.num_q_heads, w.num_query_tokens, 1 << pack))
     return PA_ERR_CUDA;
@@ -157,11 +158,13 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   p.num_blocks = w.num_blocks;
   p.q_tiles = (int32_t)q_tiles;
   p.num_query_tokens = w.num_query_tokens;
-  p.scale_log2 = w.scale_log2;
+  p.scale_log2 = w.scale_log2 * w.k_scale;
+  p.v_scale = w.v_scale;
   p.window = w.window;
   p.sinks = w.sinks;
   p.pack_log2 = pack;
   p.max_query_len = w.max_query_len;
+  if (fp8) tk = tv = tq;
   return pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

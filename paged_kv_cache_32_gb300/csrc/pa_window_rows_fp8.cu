@@ -19,6 +19,7 @@
 #include <math.h>
 
 #include "pa.h"
+#include "pa_fp8.cuh"
 #include "pa_window_rows.cuh"
 
 namespace pa {
@@ -43,16 +44,6 @@ struct RowsFp8Shape {
   static_assert(D == 128, "a key is one 128-byte swizzle row");
   static_assert(RING_BYTES >= (8 * OROW + 16) * 4, "a warp's ring holds its partial result at the end");
 };
-
-// four E4M3 codes (bytes 0..3 of r) -> two f16x2, exact: lo = (byte 0, byte 1), hi = (byte 2, byte 3)
-__device__ __forceinline__ void codes_to_half(uint32_t r, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(r));
-}
 
 // key row of the S MMA's A row r (see the file comment)
 __device__ __forceinline__ int key_row(int r) {
