@@ -26,6 +26,7 @@ struct PrefillParams {
   // kv head
   int32_t window, sinks, pack_log2;
   int32_t max_query_len;        // windowed form: bound on a chunk's queries
+  int32_t split;                // windowed form: CTAs of a cluster that share one item's key tiles
   // windowed form over an FP8 cache: a value code's scale (the key codes' is part of scale_log2)
   float v_scale;
 };

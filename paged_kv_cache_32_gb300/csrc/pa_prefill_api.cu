@@ -86,6 +86,7 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
   p.num_query_tokens = num_query_tokens;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.window = p.sinks = p.pack_log2 = 0;  // the plain form
+  p.split = 1;
   p.max_query_len = max_query_len;
   p.v_scale = 1.f;
   cudaError_t e = pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, static_cast<cudaStream_t>(stream));

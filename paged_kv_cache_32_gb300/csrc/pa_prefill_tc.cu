@@ -94,9 +94,11 @@
 #include <type_traits>
 
 #include "pa.h"
+#include "pa_cluster.cuh"
 #include "pa_device.cuh"
 #include "pa_fp8.cuh"
 #include "pa_internal.h"
+#include "pa_launch.h"
 #include "pa_prefill.h"
 
 namespace pa {
@@ -488,6 +490,23 @@ __device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfWindo
   return true;
 }
 
+// Split items: this CTA's share of the key tiles, from tile `first` of the item on (key_tiles: its number).
+struct PfSplitItem : PfWindowItem {
+  int first;
+};
+
+__device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfSplitItem& it, bool report) {
+  if (!pf_item(p, idx, static_cast<PfWindowItem&>(it), report)) return false;
+  // a CTA without a tile takes one past the end, of which its rows see nothing
+  const int rank = (int)(blockIdx.x % (unsigned)p.split), all = it.key_tiles;
+  it.first = (int)((long long)all * rank / p.split);
+  it.key_tiles = (int)((long long)all * (rank + 1) / p.split) - it.first;
+  if (it.key_tiles == 0) it.first = all, it.key_tiles = 1;
+  return true;
+}
+__device__ __forceinline__ int first_tile(const PfItem&) { return 0; }
+__device__ __forceinline__ int first_tile(const PfSplitItem& it) { return it.first; }
+
 // position of the item's key x (of the block that starts there: x a multiple of B)
 __device__ __forceinline__ int key_pos(const PfItem&, int x) { return x; }
 __device__ __forceinline__ int key_pos(const PfWindowItem& it, int x) { return x < it.xs ? x : x + it.shift; }
@@ -540,8 +559,10 @@ template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-__device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, int lane, int n_items, uint8_t* ring,
-                                             uint64_t* bar, uint64_t* freed, volatile int* abort_flag) {
+template <typename Item>
+__device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, int lane, int idx0, int idx_step,
+                                             int n_items, uint8_t* ring, uint64_t* bar, uint64_t* freed,
+                                             volatile int* abort_flag) {
   constexpr int kPastEnd = INT_MIN, kLoads = 8;  // loads of a lane and tile: two groups of 16 keys x 4
   const bool is_v = role >= kFp8Producers / 2;
   const int w = role & 3, B = p.block_size, log2_b = __ffs(B) - 1, blocks_per_tile = kTile / B;
@@ -549,13 +570,13 @@ __device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, i
   const uint8_t* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + lane * 16;
   int tg = 0;
   bool ok = true;
-  for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
-    PfWindowItem it;
+  for (int idx = idx0; ok && idx < n_items; idx += idx_step) {
+    Item it;
     if (!pf_item(p, idx, it, false)) continue;
     const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
     // lane b < blocks_per_tile: the table entry of the tile's block b
     auto fetch = [&](int kt) -> int {
-      const int bi = key_pos(it, (kt * blocks_per_tile + lane) * B) >> log2_b;
+      const int bi = key_pos(it, ((first_tile(it) + kt) * blocks_per_tile + lane) * B) >> log2_b;
       return (lane < blocks_per_tile && kt < it.key_tiles && bi < it.nblocks_seq && block_seen(it, bi * B, B))
                  ? __ldg(table + bi)
                  : kPastEnd;
@@ -590,7 +611,7 @@ __device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, i
         uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
         if (is_v) {
           // values of tokens that no query of the chunk sees may be NaN codes: zeros
-          const int pos = key_pos(it, t * kTile + 32 * w + 16 * g);
+          const int pos = key_pos(it, (first_tile(it) + t) * kTile + 32 * w + 16 * g);
           if (!(pos + 16 <= it.L && block_whole(it, pos, 16))) {
             const int mine = pos + (lane & 15);
             const unsigned some = __ballot_sync(0xffffffffu, mine < it.L && block_seen(it, mine, 1));
@@ -630,16 +651,63 @@ __device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, i
   }
 }
 
+// Split items (few items, long windows): the CTAs of a cluster each left the unnormalised rows of their share of
+// the keys, then (reference maximum in log2 units, sum), kPartRow floats a row; each now merges its share of the
+// rows through distributed shared memory.  Every thread of the cluster comes here once.
+constexpr int kPartRow = kD + 4;
+static_assert(kTile * kPartRow * 4 <= 8 * kHalf, "the rows fit the K and V stages");
+template <typename T>
+__device__ __forceinline__ void split_merge(const PrefillParams& p, const float* part, int idx) {
+  cluster_sync_all();
+  PfWindowItem it;
+  const bool has_item = pf_item(p, idx, it, false);  // the same for the whole cluster
+  if (has_item) {
+    const int rank = (int)cluster_rank(), C = p.split;
+    const int begin = it.rows * rank / C, count = it.rows * (rank + 1) / C - begin;
+    for (int i = threadIdx.x; i < count * (kD / 4); i += blockDim.x) {
+      const int r = begin + i / (kD / 4), col = i % (kD / 4) * 4;
+      const float* row = part + r * kPartRow;
+      float mx = -INFINITY;
+      for (int c = 0; c < C; ++c) mx = fmaxf(mx, ld_cluster(row + kD, c));
+      float l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < C; ++c) {
+        const float m = ld_cluster(row + kD, c);
+        const float w = m == -INFINITY ? 0.f : fast_exp2(m - mx);
+        const float4 x = ld_cluster4(row + col, c);
+        l = fmaf(w, ld_cluster(row + kD + 1, c), l);
+        acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
+      }
+      const float inv = l > 0.f ? p.v_scale / l : 0.f;
+      const size_t query = (size_t)it.q0 + it.tile0 + (r >> p.pack_log2);
+      const int head = it.h + (r & ((1 << p.pack_log2) - 1));
+      uint2 y;
+      y.x = Mma<T>::pack(acc.x * inv, acc.y * inv);
+      y.y = Mma<T>::pack(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (query * p.num_q_heads + head) * kD + col) = y;
+    }
+  }
+  cluster_sync_all();  // no CTA leaves while another reads its rows
+}
+
+// kWindow: see the file comment; kSplit: windowed, a cluster of p.split CTAs an item
+enum class PfForm { kPlain, kWindow, kSplit };
+
 // Persistent: each CTA takes items blockIdx.x, blockIdx.x + gridDim.x, ...  Every role walks the same
 // items; the K/V rings, the S buffers and their barriers run on across items (tg counts this CTA's
 // key tiles so far), so the next item's Q, K/V copies and first S MMAs overlap this item's last
 // P V and epilogue.
-template <typename T, bool kWindow, bool kFp8>
+template <typename T, PfForm kForm, bool kFp8>
 __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                       const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_out,
                       const PrefillParams p) {
-  using Item = typename std::conditional<kWindow, PfWindowItem, PfItem>::type;
+  constexpr bool kWindow = kForm != PfForm::kPlain, kSplit = kForm == PfForm::kSplit;
+  using Item = typename std::conditional<kSplit, PfSplitItem,
+                                         typename std::conditional<kWindow, PfWindowItem, PfItem>::type>::type;
+  // split: the CTAs of a cluster take the same items
+  const int idx0 = kSplit ? blockIdx.x / (unsigned)p.split : blockIdx.x;
+  const int idx_step = kSplit ? gridDim.x / (unsigned)p.split : gridDim.x;
   const int n_items = p.num_seqs * (kWindow ? p.num_q_heads >> p.pack_log2 : p.num_q_heads) * p.q_tiles;
   const int B = p.block_size;
   const int blocks_per_tile = kTile / B;
@@ -708,8 +776,8 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     if (warp >= kFp8LoadWarp0) {
       regs_dec<kFp8LoadRegs>();
       const bool v = warp >= kFp8LoadWarp0 + kFp8Producers / 2;
-      fp8_producer(p, warp - kFp8LoadWarp0, lane, n_items, smem + (v ? kVOff : kKOff), v ? bar_v : bar_k,
-                   v ? bar_o : bar_s, abort_flag);
+      fp8_producer<Item>(p, warp - kFp8LoadWarp0, lane, idx0, idx_step, n_items, smem + (v ? kVOff : kKOff),
+                         v ? bar_v : bar_k, v ? bar_o : bar_s, abort_flag);
     }
   } else if (!kFp8 && warp >= kLoadWarp0) {
     // =================================================================== producers: one half of K or V tiles
@@ -723,13 +791,14 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     if (lane == 0) tma_prefetch_descriptor(tmap);
     bool ok = true;
     int tg = 0;
-    for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+    for (int idx = idx0; ok && idx < n_items; idx += idx_step) {
       Item it;
       if (!pf_item(p, idx, it, false)) continue;
       const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
       // the table entry of this lane's block, read one tile ahead
       auto fetch = [&](int kt) -> int {
-        const int bi = kWindow ? key_pos(it, (kt * blocks_per_tile + blk) * B) / B : kt * blocks_per_tile + blk;
+        const int vb = (first_tile(it) + kt) * blocks_per_tile + blk;
+        const int bi = kWindow ? key_pos(it, vb * B) / B : vb;
         return (blk < blocks_per_tile && kt < it.key_tiles && bi < it.nblocks_seq && block_seen(it, bi * B, B))
                    ? __ldg(table + bi)
                    : kPastEnd;
@@ -751,7 +820,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         const bool in_pool = entry >= 0 && entry < p.num_blocks;
         if (!is_v && half == 0 && entry != kPastEnd && !in_pool) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
         // V: only blocks entirely inside the sequence (and the window) go by tensor-map copy
-        const int first_pos = key_pos(it, (t * blocks_per_tile + blk) * B);
+        const int first_pos = key_pos(it, ((first_tile(it) + t) * blocks_per_tile + blk) * B);
         const bool whole = in_pool && (!is_v || (first_pos + B <= it.L && block_whole(it, first_pos, B)));
         if (blk < blocks_per_tile) {
           if (whole) {
@@ -773,7 +842,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
               const int e = __shfl_sync(0xffffffffu, entry, b);
               if (!((partial >> b) & 1)) continue;
               const int r = r0 + (lane >> 3), chunk = lane & 7;
-              const int pos = key_pos(it, t * kTile + r);
+              const int pos = key_pos(it, (first_tile(it) + t) * kTile + r);
               uint8_t* dst = st + swz128(r, chunk);
               if (pos < it.L && block_seen(it, pos, 1) && e >= 0 && e < p.num_blocks)
                 cp_async16(dst, cache + (((size_t)e * p.num_kv_heads + it.hkv) * B + (pos % B)) * kD + half * 64 +
@@ -801,7 +870,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       // phase k), which also means the S MMAs of item k - 1, the last readers of that Q buffer, have
       // finished.  It reports inconsistent chunks: every item of this CTA passes through here once.
       auto publish = [&](int idx, int k, Item& it) {
-        for (; idx < n_items; idx += gridDim.x)
+        for (; idx < n_items; idx += idx_step)
           if (pf_item(p, idx, it, true)) break;
         if (idx >= n_items) it.s = -1;
         items[k & 1] = it;
@@ -819,7 +888,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       bool ok = true;
       int tg = 0, item_no = 0;
       Item it;
-      int idx = publish(blockIdx.x, 0, it);
+      int idx = publish(idx0, 0, it);
       while (ok && idx < n_items) {
         // Q of this item in its buffer (this thread publishes the barrier's next phase: exact)
         ok = wait_bar_spin(bar_qs, item_no & 1, abort_flag);
@@ -832,7 +901,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         auto try_publish = [&](bool block) {
           if (published) return;
           if (block ? wait_bar_spin(bar_q, item_no & 1, abort_flag) : mbar_test_wait(bar_q, item_no & 1)) {
-            idx_next = publish(idx + gridDim.x, item_no + 1, nx);
+            idx_next = publish(idx + idx_step, item_no + 1, nx);
             published = true;
           } else if (block) {
             ok = false;
@@ -883,7 +952,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
           bulk_commit_group();
         }
       };
-      for (int idx = blockIdx.x; ok && idx < n_items; idx += gridDim.x) {
+      for (int idx = idx0; ok && idx < n_items; idx += idx_step) {
         Item it;
         if (!pf_item(p, idx, it, false)) continue;
         // the first P V overwrites O: the previous item's epilogue must have read it (the barrier's
@@ -920,7 +989,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         if (ok) mbar_arrive(bar_done);
         prev_row0 = it.q0 + it.tile0;
         prev_h = it.h;
-        prev_full = it.rows == kTile;
+        prev_full = it.rows == kTile && !kSplit;
         ++item_no;
       }
       if (ok && item_no > 0) store_prev();
@@ -957,7 +1026,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       tmem_ld16x256_x8(s_addr, v);
       tmem_ld16x256_x8(s_addr + 64, v + 32);
       tmem_wait_ld<64>(v);
-      const int tile0 = kt * kTile;                  // first key
+      const int tile0 = (first_tile(it) + kt) * kTile;  // first key
       const int key0 = tile0 + 2 * c4;               // key of this thread's pair 0
       const int e0 = lim0 - key0, e1 = lim1 - key0;  // pair j's keys 8j, 8j + 1 are visible up to e
       // window: the first key of each row's window
@@ -1119,6 +1188,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         return reinterpret_cast<T*>(p.out) + (query * p.num_q_heads + head) * kD;
       };
       const int rows = it.rows;
+      [[maybe_unused]] const float pm0 = m0, pm1 = m1;  // split: this item's reference maxima
       ok = warp_wait(bar_qs, (item_no + 1) & 1);
       it = items[(item_no + 1) & 1];
       if (ok && it.s >= 0) start_item(it);
@@ -1135,6 +1205,24 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_ofree);
+      if constexpr (kSplit) {
+        // the unnormalised rows, their reference maxima and sums for the cluster's merge (no copy or MMA of
+        // this CTA touches the K and V stages any more: bar_done)
+        float* part = reinterpret_cast<float*>(smem + kKOff);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          *reinterpret_cast<float2*>(part + r0 * kPartRow + 8 * j + 2 * c4) = make_float2(o[4 * j], o[4 * j + 1]);
+          *reinterpret_cast<float2*>(part + r1 * kPartRow + 8 * j + 2 * c4) = make_float2(o[4 * j + 2], o[4 * j + 3]);
+        }
+        if (c4 == 0) {
+          *reinterpret_cast<float2*>(part + r0 * kPartRow + kD) = make_float2(pm0, s0);
+          *reinterpret_cast<float2*>(part + r1 * kPartRow + kD) = make_float2(pm1, s1);
+        }
+        __syncwarp();
+        if (kStagedOut<T> && lane == 0) mbar_arrive(bar_staged);
+        ++item_no;
+        continue;
+      }
       const float unit = kFp8 ? p.v_scale : 1.f;
       const float inv0 = s0 > 0.f ? unit / s0 : 0.f, inv1 = s1 > 0.f ? unit / s1 : 0.f;
       if constexpr (kStagedOut<T>) {
@@ -1225,12 +1313,13 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       for (int t = max(0, n_o - kSBufs); t < n_o; ++t) drain_wait(&bar_o[t % kSBufs], (t / kSBufs) & 1);
     __syncthreads();
   }
+  if constexpr (kSplit) split_merge<T>(p, reinterpret_cast<const float*>(smem + kKOff), idx0);
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 // one CTA per SM (the kernel holds all of tensor memory and most of shared memory), at most one per item
-template <typename T, bool kWindow, bool kFp8 = false>
+template <typename T, PfForm kForm, bool kFp8 = false>
 static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                   const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
   const long long items = (long long)p.num_seqs * (p.num_q_heads >> p.pack_log2) * p.q_tiles;
@@ -1240,24 +1329,32 @@ static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, 
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)(items < sms ? items : sms);
-  auto kernel = prefill_tc_kernel<T, kWindow, kFp8>;
+  // split: one cluster an item
+  const unsigned grid = (unsigned)(p.split > 1 ? items * p.split : items < sms ? items : sms);
+  auto kernel = prefill_tc_kernel<T, kForm, kFp8>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kFp8 ? kFp8Threads : kThreads, kSmemBytes, stream>>>(tk, tv, tq, to, p);
-  return cudaGetLastError();
+  return launch_cluster(kernel, dim3(grid), dim3(kFp8 ? kFp8Threads : kThreads), kSmemBytes, p.split, false, stream, tk,
+                        tv, tq, to, p);
+}
+
+template <typename T, bool kFp8>
+static cudaError_t launch_window(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
+                                 const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
+  return p.split > 1 ? launch_prefill<T, PfForm::kSplit, kFp8>(tk, tv, tq, to, p, stream)
+                     : launch_prefill<T, PfForm::kWindow, kFp8>(tk, tv, tq, to, p, stream);
 }
 
 cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                               const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
   const bool window = p.window > 0;
   if (dtype == PA_F16)
-    return window ? launch_prefill<__half, true>(tk, tv, tq, to, p, stream)
-                  : launch_prefill<__half, false>(tk, tv, tq, to, p, stream);
+    return window ? launch_window<__half, false>(tk, tv, tq, to, p, stream)
+                  : launch_prefill<__half, PfForm::kPlain>(tk, tv, tq, to, p, stream);
   if (dtype == PA_BF16)
-    return window ? launch_prefill<__nv_bfloat16, true>(tk, tv, tq, to, p, stream)
-                  : launch_prefill<__nv_bfloat16, false>(tk, tv, tq, to, p, stream);
-  if (dtype == PA_FP8_E4M3 && window) return launch_prefill<__half, true, true>(tk, tv, tq, to, p, stream);
+    return window ? launch_window<__nv_bfloat16, false>(tk, tv, tq, to, p, stream)
+                  : launch_prefill<__nv_bfloat16, PfForm::kPlain>(tk, tv, tq, to, p, stream);
+  if (dtype == PA_FP8_E4M3 && window) return launch_window<__half, true>(tk, tv, tq, to, p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -1,7 +1,7 @@
 // pa_window.h - launch parameters of the windowed attention kernels (not part of the public ABI).
 #pragma once
 
-#include "pa_internal.h"
+#include "pa_launch.h"
 
 namespace pa {
 
@@ -43,26 +43,4 @@ cudaError_t launch_window_rows_tc(int dtype, int head_size, const CUtensorMap& t
 cudaError_t launch_window_rows_fp8(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p,
                                    cudaStream_t stream);
 cudaError_t launch_window_rows_f32(int head_size, const WindowParams& p, cudaStream_t stream);
-// Launch in clusters of `cluster` CTAs (1: none) as a programmatic dependent of the kernel before it (see
-// launch_dependent).
-template <typename... Params, typename... Args>
-inline cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, int cluster,
-                                  cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 }  // namespace pa

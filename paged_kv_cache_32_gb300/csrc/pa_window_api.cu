@@ -6,6 +6,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 #include "pa.h"
 #include "pa_prefill.h"
 #include "pa_window.h"
@@ -130,6 +132,35 @@ bool tile_kernel_takes(const pa_cache_desc* c) {
   return c->dtype != PA_F32 && c->head_size == 128 && 128 % c->block_size == 0;
 }
 
+// CTAs that share an item's key tiles: as many as leave each SM at most one, with four tiles or more each
+int tile_split(long long items, long long max_keys) {
+  int c = 1;
+  while (c < kMaxCluster && items * c * 2 <= kSms && max_keys / (128 * 2 * c) >= 4) c *= 2;
+  return c;
+}
+
+// Is a chunk faster on the tile kernel than on the rows kernel?  By what both took over 288 chunks of 1 to 17 queries
+// (1 to 32 sequences, 7 to 64 query heads on 1 to 32 kv heads, 300 and 4096 keys, bf16 and FP8):
+//  * rows: 6 us and the longer of 1 us for 23600 (FP8: 30000) keys of an eight-row group over all, and 0.85 us for
+//    each slab of 16 keys (FP8: 1.3 us for 32) of the warp with most;
+//  * tiles: 8 us and, for each item that an SM gets, 3 us and 1.45 (1.85) us a key tile.
+// E.g. 32 sequences, 64 / 8 heads, 4096 keys, bf16: 2 queries each 95 us on rows and 111 on tiles, 5 queries about 230
+// and 111; 8 sequences of 5 queries: 78 and 39.
+bool tiles_faster(const pa_cache_desc* cache, pa::WindowParams p, int pack) {
+  const bool fp8 = cache->dtype == PA_FP8_E4M3;
+  const int G = p.num_q_heads / p.num_kv_heads, queries = 128 >> pack;
+  const double kv = (double)p.num_seqs * p.num_kv_heads;
+  const double keys = std::min((double)p.max_blocks * p.block_size, (double)p.window + p.sinks + queries);
+  const double groups = kv * ceil((double)p.max_query_len * G / 8);
+  spread((long long)std::min(groups, 1e9), (long long)keys, p);
+  const double slabs = ceil(keys / (fp8 ? 32.0 : 16.0) / (p.warps * p.cluster));
+  const double rows_us = 6.0 + std::max(groups * keys / (fp8 ? 30000.0 : 23600.0), slabs * (fp8 ? 1.3 : 0.85));
+  const double items = kv * ceil((double)p.max_query_len / queries) * (G >> pack), share = items / kSms;
+  const double tiles = ceil(keys / 128.0) / tile_split((long long)std::min(items, 1e9), (long long)keys);
+  const double tile_us = 8.0 + 0.5 * (share + ceil(share)) * (3.0 + (fp8 ? 1.85 : 1.45) * tiles);
+  return tile_us < rows_us;
+}
+
 int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack, cudaStream_t stream) {
   const long long q_tiles = ((long long)w.max_query_len + (128 >> pack) - 1) / (128 >> pack);
   // work items are counted in int32, with room for one grid stride past the end
@@ -164,6 +195,8 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   p.sinks = w.sinks;
   p.pack_log2 = pack;
   p.max_query_len = w.max_query_len;
+  p.split = tile_split((long long)w.num_seqs * (w.num_q_heads >> pack) * q_tiles,
+                       std::min((long long)w.max_blocks * w.block_size, (long long)w.window + w.sinks + 128));
   if (fp8) tk = tv = tq;
   return pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -264,12 +297,8 @@ int pa_prefill_window(void* out, const void* q, const void* k_cache, const void*
   p.query_start = query_start;
   p.num_query_tokens = num_query_tokens;
   p.max_query_len = max_query_len;
-  // The tile kernel takes chunks for which it reads the keys less often than the rows kernel would (once a query
-  // tile and head group, against once for eight rows).
-  const int G = num_q_heads / cache->num_kv_heads, pack = pack_log2(G);
-  const long long row_reads = ((long long)max_query_len * G + 7) / 8;
-  const long long tile_reads = ((long long)max_query_len + (128 >> pack) - 1) / (128 >> pack) * (G >> pack);
-  if (tile_kernel_takes(cache) && tile_reads < row_reads)
+  const int pack = pack_log2(num_q_heads / cache->num_kv_heads);
+  if (tile_kernel_takes(cache) && tiles_faster(cache, p, pack))
     return launch_tiles(cache, p, pack, static_cast<cudaStream_t>(stream));
   return launch_rows(cache, p, static_cast<cudaStream_t>(stream));
 }

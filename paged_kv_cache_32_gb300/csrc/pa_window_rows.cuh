@@ -20,6 +20,7 @@
 
 #include <math.h>
 
+#include "pa_cluster.cuh"
 #include "pa_device.cuh"
 #include "pa_window.h"
 
@@ -49,25 +50,6 @@ struct RowsItem {
   int v0, v1;           // this CTA's slabs of the list
   bool empty;           // a decode row of an empty sequence: zeros
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// float at the address of `p` (this CTA's shared memory) in CTA `rank` of the cluster
-__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-      : "=f"(v)
-      : "r"(smem_u32(p)), "r"(rank)
-      : "memory");
-  return v;
-}
 
 // The item of this CTA's cluster and the CTA's share of its slabs (SB tokens each).  False: nothing to do (the
 // same for every CTA of the cluster).  A chunk outside q / out, longer than the grid covers or than its

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
 template <int D>
 cudaError_t launch_f32(const WindowParams& p, cudaStream_t stream) {
   return launch_cluster(window_rows_f32_kernel<D>, dim3((unsigned)(window_items(p) * p.cluster)), dim3(kF32Warps * 32), 0,
-                        p.cluster, stream, p);
+                        p.cluster, true, stream, p);
 }
 
 }  // namespace

@@ -359,7 +359,7 @@ static cudaError_t launch_warps(const CUtensorMap& tk, const CUtensorMap& tk32, 
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
-                        p.cluster, stream, tk, tk32, p);
+                        p.cluster, true, stream, tk, tk32, p);
 }
 
 cudaError_t launch_window_rows_fp8(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p,

@@ -338,7 +338,7 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Wind
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
-                        p.cluster, stream, tk, tv, p);
+                        p.cluster, true, stream, tk, tv, p);
 }
 
 template <typename T, int D, int NS, bool SPLIT>

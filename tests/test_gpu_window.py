@@ -246,6 +246,25 @@ def test_prefill_window_short_chunks(dtype):
         check(s, w.reference(), f"window {window}")
 
 
+@pytest.mark.parametrize("dtype,block_size", [("bf16", 16), ("f16", 64), ("fp8", 32), ("bf16", 8)])
+@pytest.mark.parametrize("window,sinks", [(2500, 3), (1100, 0), (BIG, 0), (700, 400)])
+def test_prefill_window_few_long_items(dtype, block_size, window, sinks):
+    """Few items over many keys: the CTAs of a cluster share an item's key tiles and merge their rows; the short
+    sequences leave some of them without a tile, a ragged chunk some rows outside it."""
+    lens, chunks = [3100, 2600, 130, 3, 900], [300, 150, 70, 3, 0]
+    w = WindowCase(dtype, lens, chunks, 16, 2, 128, block_size, window, sinks, seed=window % 97)
+    s = Step(w)
+    s.prefill()
+    check(s, w.reference(), "few long items")
+    assert torch_equal(s.out, Step(w).prefill())
+
+
+def torch_equal(a, b):
+    import torch
+    torch.cuda.synchronize()
+    return torch.equal(a, b)
+
+
 def test_prefill_window_is_prefill_and_decode(pa):
     """A window past every length gives pa_prefill's result, a chunk of one token pa_decode_window's."""
     w = WindowCase("bf16", [700, 260], [200, 129], 8, 2, 128, 16, 800, 0, seed=3)
