@@ -351,19 +351,6 @@ struct SeeCausal {
   __device__ __forceinline__ bool see0(int x) const { return x <= e0; }
   __device__ __forceinline__ bool see1(int x) const { return x <= e1; }
 };
-// x in [f, f + n), or below g (the first tokens), and at most e
-template <bool kSinks>
-struct SeeWindow {
-  int e0, e1, f0, f1, g;
-  unsigned n0, n1;
-  __device__ __forceinline__ bool see0(int x) const {
-    return (unsigned)(x - f0) < n0 || (kSinks && x < g && x <= e0);
-  }
-  __device__ __forceinline__ bool see1(int x) const {
-    return (unsigned)(x - f1) < n1 || (kSinks && x < g && x <= e1);
-  }
-};
-
 // P of 8 of the 16 key pairs this thread holds in each of its two rows, pairs j0 .. j0 + 7 (v in
 // the 16x256b layout over the tile's 128 columns: pair j = keys 8j + 2c, 8j + 2c + 1, c = thread % 4;
 // v[4j], v[4j + 1] row 0, v[4j + 2], v[4j + 3] row 1) from the raw scores, the scale in log2 units
@@ -1059,6 +1046,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         }
       }
       auto exact = [&](const auto& mask) {
+        constexpr bool kMask = !std::is_same<std::decay_t<decltype(mask)>, SeeAll>::value;
         // ---- the rows' tile maxima, and the reference maxima they imply
         float a0 = -INFINITY, b0 = -INFINITY, a1 = -INFINITY, b1 = -INFINITY;  // two chains per row
 #pragma unroll
@@ -1068,7 +1056,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
           b0 = max3(b0, v[4 * j + 4], v[4 * j + 5]);
           b1 = max3(b1, v[4 * j + 6], v[4 * j + 7]);
         }
-        if (!unmasked) {
+        if constexpr (kMask) if (!unmasked) {
           // The maxima over all 128 keys bound the visible keys' maxima from above.  A bound that moves
           // no row's reference max decides as the visible maxima would, so those are taken only when
           // the bound would move one (rare after an item's first tiles).
@@ -1129,21 +1117,47 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
 #pragma unroll
         for (int j0 = 0; j0 < 16; j0 += 8) {
           uint32_t hi[16], lo[16];
-          if (unmasked)
-            make_p<T>(v, j0, sl2, m0, m1, SeeAll{}, hi, lo, l0, l1);
+          // (window: a row may have seen no key yet; its scores are all -inf, its weights 0)
+          const float z0 = kWindow && m0 == -INFINITY ? 0.f : m0, z1 = kWindow && m1 == -INFINITY ? 0.f : m1;
+          if (!kMask || unmasked)
+            make_p<T>(v, j0, sl2, z0, z1, SeeAll{}, hi, lo, l0, l1);
           else
-            make_p<T>(v, j0, sl2, m0, m1, mask, hi, lo, l0, l1);
+            make_p<T>(v, j0, sl2, z0, z1, mask, hi, lo, l0, l1);
           tmem_st16x128_x8(s_addr + 4 * j0, hi);
           if constexpr (split_p<T>()) tmem_st16x128_x8(s_addr + 64 + 4 * j0, lo);
         }
       };
       if (!lazy) {
         if constexpr (kWindow) {
-          const unsigned n0 = lim0 - low0 + 1, n1 = lim1 - low1 + 1;
-          if (tile0 < p.sinks)
-            exact(SeeWindow<true>{e0, e1, low0 - key0, low1 - key0, p.sinks - key0, n0, n1});
-          else
-            exact(SeeWindow<false>{e0, e1, low0 - key0, low1 - key0, 0, n0, n1});
+          // The excluded scores become -inf once, and the tile goes on like an unmasked one (masking the maxima and
+          // the weights apart, as below: a 4096-token fp16 chunk, W = 4096, 238 -> 229 us, drafts 38.8 -> 37.6).
+          if (!unmasked) {
+            const int f0 = low0 - key0, f1 = low1 - key0, g = p.sinks - key0;
+            const unsigned n0 = lim0 - low0 + 1, n1 = lim1 - low1 + 1;
+            if (g > 0) {  // some of the first tokens: keys below g, up to e0 (e1)
+              const int g0 = min(g, e0 + 1), g1 = min(g, e1 + 1);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int x = 8 * j + i;
+                  if (!((unsigned)(x - f0) < n0 || x < g0)) v[4 * j + i] = -INFINITY;
+                  if (!((unsigned)(x - f1) < n1 || x < g1)) v[4 * j + 2 + i] = -INFINITY;
+                }
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int x = 8 * j + i;
+                  if ((unsigned)(x - f0) >= n0) v[4 * j + i] = -INFINITY;
+                  if ((unsigned)(x - f1) >= n1) v[4 * j + 2 + i] = -INFINITY;
+                }
+              }
+            }
+          }
+          exact(SeeAll{});
         } else {
           exact(SeeCausal{e0, e1});
         }
