@@ -31,8 +31,15 @@ constexpr int kMinCtaTokens = 64;  // tokens of a CTA below which a split no lon
 //    48.3, 768 items 69.9 / 67.8 / 74.5, 1024 items 92.2 / 93.4 / 87.9.
 //    (Splitting long items in two all the same evens out a last round of unequal contexts, 96 FP8 sequences of
 //    2500 to 40000 tokens with a window of 8192: 240 -> 226 us, and costs as much when they are equal, 246 -> 264.)
-void spread(long long items, long long max_keys, pa::WindowParams& p) {
+//  * fp32 (CUDA cores): four warps a CTA, three CTAs an SM, split while that many are not there.
+void spread(int32_t dtype, long long items, long long max_keys, pa::WindowParams& p) {
   p.cluster = 1;
+  if (dtype == PA_F32) {
+    p.warps = 4;
+    while (p.cluster < kMaxCluster && items * p.cluster * 2 <= 3 * kSms && max_keys / (2 * p.cluster) >= kMinCtaTokens)
+      p.cluster *= 2;
+    return;
+  }
   if (items <= kSms / 2) {
     p.warps = 6;
     while (p.cluster < kMaxCluster && items * p.cluster * 2 <= 2 * kSms &&
@@ -97,8 +104,7 @@ int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t st
   const long long cap = (long long)p.max_blocks * p.block_size;
   const long long reach = (long long)p.window + p.sinks + 8;
   const long long items = pa::window_items(p);
-  spread(items, reach < cap ? reach : cap, p);
-  if (cache->dtype == PA_F32) p.warps = 4;
+  spread(cache->dtype, items, reach < cap ? reach : cap, p);
   if (items * p.cluster > kInt32Max) return PA_ERR_TOO_LARGE;
   cudaError_t e;
   if (cache->dtype == PA_F32) {
@@ -152,7 +158,7 @@ bool tiles_faster(const pa_cache_desc* cache, pa::WindowParams p, int pack) {
   const double kv = (double)p.num_seqs * p.num_kv_heads;
   const double keys = std::min((double)p.max_blocks * p.block_size, (double)p.window + p.sinks + queries);
   const double groups = kv * ceil((double)p.max_query_len * G / 8);
-  spread((long long)std::min(groups, 1e9), (long long)keys, p);
+  spread(cache->dtype, (long long)std::min(groups, 1e9), (long long)keys, p);
   const double slabs = ceil(keys / (fp8 ? 32.0 : 16.0) / (p.warps * p.cluster));
   const double rows_us = 6.0 + std::max(groups * keys / (fp8 ? 30000.0 : 23600.0), slabs * (fp8 ? 1.3 : 0.85));
   const double items = kv * ceil((double)p.max_query_len / queries) * (G >> pack), share = items / kSms;

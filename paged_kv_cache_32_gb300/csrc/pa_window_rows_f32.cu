@@ -3,14 +3,15 @@
 // split).
 //
 // fp32 keeps full products, so it runs on the CUDA cores.  A warp takes slabs of
-// 16 tokens, four tokens at a time: every lane holds D / 32 elements of the four
-// K and V rows (coalesced loads, eight in flight), the 8 rows x 4 tokens = 32
-// partial dot products are reduced together (a halving exchange: 31 shuffles
-// leave score j in lane j, where a sum of each alone would take 160), the online
-// softmax works on one score a lane, and the 32 weights are passed round for
-// O += P V.  About 350 instructions per 4 KB of K/V at D = 128: at four
-// instructions a clock an SM could take in 47 bytes a clock, twice its share of
-// HBM, so the copies bound it.
+// 16 tokens, four tokens (a step) at a time: every lane holds D / 32 elements of
+// the four K and V rows, the 8 rows x 4 tokens = 32 partial dot products are
+// reduced together (a halving exchange: 31 shuffles leave score j in lane j,
+// where a sum of each alone would take 160), the online softmax works on one
+// score a lane, and the 32 weights are passed round for O += P V.  About 420
+// instructions per 4 KB of K/V at D = 128, as many cycles again in waits between
+// them: three warps a scheduler keep up with HBM if no load is waited for.  So
+// each lane copies its own elements kRing - 1 steps ahead into shared memory
+// (cp.async: no registers, and no barrier, since it alone reads them back).
 #include <cuda.h>
 #include <math.h>
 
@@ -23,23 +24,27 @@ namespace {
 constexpr int kF32Slab = 16;
 constexpr int kF32Warps = 4;
 
+constexpr int kRing = 4;  // steps in flight per warp, the one in use included
+
+// this lane's elements of a row into its slot, zeros unless `take`
 template <int VEC>
-__device__ __forceinline__ void load_row(const float* src, float (&x)[VEC]) {
-  if constexpr (VEC == 4) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(src));
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-  } else {
-    const float2 v = __ldg(reinterpret_cast<const float2*>(src));
-    x[0] = v.x, x[1] = v.y;
-  }
+__device__ __forceinline__ void copy_row(float* slot, const float* src, bool take) {
+  const uint32_t bytes = take ? VEC * 4 : 0;
+  if constexpr (VEC == 4)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot)), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(slot)), "l"(src), "r"(bytes) : "memory");
 }
 
 template <int D>
 __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const WindowParams p) {
   constexpr int VEC = D / 32, OROW = D, STRIDE = 8 * D + 16;
-  __shared__ float parts[kF32Warps * STRIDE];
+  constexpr int STEP = 8 * D;  // floats of a step: four rows of K, then of V
+  // [warp][step of the ring][K: token 0..3, V: token 0..3][D]; at the end a warp's partial result
+  extern __shared__ __align__(16) float ring_all[];
   __shared__ float wt[8 * kF32Warps + 16];
   __shared__ float mine[8 * D + 16];
+  static_assert(kRing * STEP >= STRIDE, "a warp's ring holds its partial result");
   griddep_begin();
   RowsItem it;
   if (!rows_item<kF32Slab>(p, it)) return;
@@ -70,34 +75,66 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
       p.alibi != nullptr ? __ldg(p.alibi + it.hkv * it.G + (it.row0 + my_row) % it.G) * 1.4426950408889634f : 0.f;
   float m = -INFINITY, l = 0.f;  // of the lane's row (l: of its token of each four)
 
-  for (int v = it.v0 + warp; v < it.v1; v += kF32Warps) {
-    const int tok0 = rows_slab(it, v) * kF32Slab;
-    // lane t < 16: the block of the slab's token t (-1: seen by no row, or not in the pool)
-    int entry = -1;
-    if (lane < kF32Slab && rows_any(it, tok0 + lane)) {
-      entry = __ldg(table + (tok0 + lane) / B);
-      if (entry < 0 || entry >= p.num_blocks) {
-        report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
-        entry = -1;
+  float* ring = ring_all + warp * (kRing * STEP) + lane * VEC;
+  const int mine_n = it.v1 - it.v0, n_my = mine_n > warp ? (mine_n - warp + kF32Warps - 1) / kF32Warps : 0;
+  auto slab_tok = [&](int k) { return rows_slab(it, it.v0 + warp + k * kF32Warps) * kF32Slab; };
+  // lane t < 16: the block of token t of slab k (-1: seen by no row, or not in the pool)
+  auto fetch = [&](int k) {
+    int e = -1;
+    if (k < n_my && lane < kF32Slab) {
+      const int t = slab_tok(k) + lane;
+      if (rows_any(it, t)) {
+        e = __ldg(table + t / B);
+        if (e < 0 || e >= p.num_blocks) {
+          report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+          e = -1;
+        }
       }
     }
-#pragma unroll 1
-    for (int t0 = 0; t0 < kF32Slab; t0 += 4) {
-      float k[4][VEC], x[4][VEC];
-      bool mine_in = false;  // the lane's token takes part
+    return e;
+  };
+  int entry = fetch(0), entry_next = fetch(1);   // of the slab being copied and the one after it
+  unsigned live = 0, live_prev = 0;              // its tokens that take part, and those of the slab before
+  const int steps = 4 * n_my;
+  auto issue = [&](int i) {  // the copies of step i: tokens 4 (i % 4) .. of slab i / 4
+    if (i < steps) {
+      if (i % 4 == 0) {
+        if (i > 0) {
+          entry = entry_next;
+          entry_next = fetch(i / 4 + 1);
+        }
+        live_prev = live;
+        live = __ballot_sync(0xffffffffu, entry >= 0);
+      }
+      const int t0 = 4 * (i % 4), tok0 = slab_tok(i / 4) + t0;
+      float* st = ring + (i % kRing) * STEP;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int e = __shfl_sync(0xffffffffu, entry, t0 + t);
-        if (t == my_tok) mine_in = e >= 0;
-        if (e >= 0) {
-          const size_t row = (((size_t)e * p.num_kv_heads + it.hkv) * B + (tok0 + t0 + t) % B) * D;
-          load_row<VEC>(kc + row, k[t]);
-          load_row<VEC>(vc + row, x[t]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) k[t][i] = x[t][i] = 0.f;
-        }
+        const size_t row = e >= 0 ? (((size_t)e * p.num_kv_heads + it.hkv) * B + (tok0 + t) % B) * D : 0;
+        copy_row<VEC>(st + t * D, kc + row, e >= 0);
+        copy_row<VEC>(st + (4 + t) * D, vc + row, e >= 0);
       }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");  // (empty past the end: the count of groups stays that of steps)
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue(i);
+
+  for (int i = 0; i < steps; ++i) {
+    issue(i + kRing - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");  // step i has landed
+    {
+      // the slab being copied is this step's, or the one after it
+      const unsigned in = (i + kRing - 1 < steps ? (i + kRing - 1) / 4 : n_my - 1) == i / 4 ? live : live_prev;
+      const int t0 = 4 * (i % 4), tok0 = slab_tok(i / 4);
+      const bool mine_in = (in >> (t0 + my_tok)) & 1u;  // the lane's token takes part
+      const float* st = ring + (i % kRing) * STEP;
+      float k[4][VEC], x[4][VEC];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) k[t][e] = st[t * D + e];
       float dot[32];  // value 8 * token + row
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -140,6 +177,10 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
+        for (int e = 0; e < VEC; ++e) x[t][e] = st[(4 + t) * D + e];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
         for (int r = 0; r < 8; ++r) {
           const float w = __shfl_sync(0xffffffffu, pe, 8 * t + r);
 #pragma unroll
@@ -149,7 +190,8 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
   }
   l += __shfl_xor_sync(0xffffffffu, l, 8);
   l += __shfl_xor_sync(0xffffffffu, l, 16);
-  float* wo = parts + warp * STRIDE;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  float* wo = ring_all + warp * (kRing * STEP);
 #pragma unroll
   for (int r = 0; r < 8; ++r)
 #pragma unroll
@@ -159,13 +201,17 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
     wo[8 * OROW + 2 * lane + 1] = l;
   }
   __syncthreads();
-  rows_finish<float, D, kF32Warps, OROW, STRIDE>(p, it, parts, wt, mine);
+  rows_finish<float, D, kF32Warps, OROW, kRing * STEP>(p, it, ring_all, wt, mine);
 }
 
 template <int D>
 cudaError_t launch_f32(const WindowParams& p, cudaStream_t stream) {
-  return launch_cluster(window_rows_f32_kernel<D>, dim3((unsigned)(window_items(p) * p.cluster)), dim3(kF32Warps * 32), 0,
-                        p.cluster, true, stream, p);
+  auto kernel = window_rows_f32_kernel<D>;
+  constexpr size_t kSmem = (size_t)kF32Warps * kRing * 8 * D * sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(kF32Warps * 32), kSmem, p.cluster,
+                        true, stream, p);
 }
 
 }  // namespace
