@@ -23,6 +23,12 @@
 // lie in shared memory so that the units of a head read neighbouring banks: by
 // pairs of elements, then units.  The fixed-point frequencies, which take fp64
 // operations (two a clock and SM here), are made once per CTA.
+//
+// Values of an FP8 cache lie with a dimension's 16 tokens side by side: warps of
+// their own (the grid's first CTAs) take up to 16 tokens of one head, quantise
+// them into shared memory and write each run of slots that follow one another
+// inside a 16-token group with as few stores as its length allows, 16 bytes for
+// a whole group (9001 tokens: single bytes from the units 118 us, these 81).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -42,7 +48,10 @@ namespace {
 // warp's waits cover loads just issued (71 and 216 us).
 constexpr int kRopeThreads = 384;
 constexpr int kRopeResident = 2;
-constexpr int kBatch = 2;
+// narrow vectors, for halves that no 16 bytes divide: more units a thread (the 9001 tokens with 36 and 34 turned
+// elements: 95 and 167 us; with two units 136 and 208, with eight, which spill, 145 and 332)
+template <typename T, int V>
+constexpr int kUnits = sizeof(T) * V >= 16 ? 2 : 4;
 
 // Vectors of V elements of T, moved with one access; 16-bit pairs are handled as 32-bit words.
 template <typename T, int V>
@@ -102,12 +111,8 @@ __device__ __forceinline__ Vec<uint8_t, V> codes_of(const float (&f)[V], float s
   return y;
 }
 
-struct RopeToken {
-  long long row;  // cache row (block * Hkv * B + offset) of kv head 0; < 0: the token is skipped
-  int off;        // offset in the block
-};
-
 constexpr int kMaxHalf = 64;  // pairs of the largest head
+constexpr int kRopeWarps = (kRopeThreads + kMaxHalf) / 32;
 constexpr int kMaxGroup = 16; // tokens of a group
 
 // How the units are dealt out: groups of `tokens` tokens, each cut into `parts` parts of `part_units` units (a
@@ -115,22 +120,114 @@ constexpr int kMaxGroup = 16; // tokens of a group
 struct RopePlan {
   int tokens, parts, part_units, groups;
   int log2_per_head;  // units of a head
+  int value_ctas;     // FP8: the grid's first CTAs, whose warps take the values of value_tokens tokens of one kv head
+  int value_tokens;
 };
+
+// One warp: values of kv head `head` of the tokens t0 .. t0 + n - 1 (n <= 16) into an FP8 cache, through `codes`
+// (n rows of kCodeRow bytes).
+constexpr int kValueTokens = 16;
+constexpr int kCodeRow = 128 + 8;  // a token's codes, padded
+__device__ __forceinline__ void fp8_values(const RopeParams& p, int t0, int n, int head, uint8_t* codes) {
+  constexpr int D = 128;  // of every FP8 cache
+  const int lane = threadIdx.x & 31;
+  const __half* src = static_cast<const __half*>(p.value) + (long long)t0 * p.value_stride + (size_t)head * D;
+  long long slot = lane < n ? p.slot_mapping[t0 + lane] : -1;
+  if (slot >= (long long)p.num_blocks * p.block_size) {
+    if (head == 0) report_error(p.err_flag, PA_DEVERR_SLOT);
+    slot = -1;
+  }
+  Vec<__half, 8> x[kValueTokens / 2];  // lane: dimensions 8 (lane % 16) .. of the tokens lane / 16 + 2 i
+#pragma unroll
+  for (int i = 0; i < kValueTokens / 2; ++i) {
+    const int t = (lane >> 4) + 2 * i;
+    if (t < n) x[i] = *reinterpret_cast<const Vec<__half, 8>*>(src + (long long)t * p.value_stride + 8 * (lane & 15));
+  }
+  // where a lane's token goes, and whether it starts a run
+  long long at = 0;
+  int off = 0;
+  if (slot >= 0) {
+    const long long block = slot / p.block_size;
+    off = (int)(slot - block * p.block_size);
+    at = ((block * p.num_kv_heads + head) * p.block_size + off / 16 * 16) * D + off % 16;
+  }
+  const long long before = __shfl_up_sync(0xffffffffu, slot, 1);
+  const bool start = lane == 0 || slot < 0 || slot != before + 1 || off % 16 == 0;
+  unsigned starts = __ballot_sync(0xffffffffu, start || lane >= n);
+  const unsigned live = __ballot_sync(0xffffffffu, slot >= 0);
+#pragma unroll
+  for (int i = 0; i < kValueTokens / 2; ++i) {
+    const int t = (lane >> 4) + 2 * i;
+    if (t < n) {
+      float f[8];
+      x[i].get(f);
+      *reinterpret_cast<Vec<uint8_t, 8>*>(codes + t * kCodeRow + 8 * (lane & 15)) = codes_of(f, p.v_scale);
+    }
+  }
+  __syncwarp();
+  for (int a = 0; a < n;) {
+    starts &= starts - 1;  // (bit a, the lowest left, is this run's start)
+    const int next = starts ? min(n, __ffs(starts) - 1) : n, len = next - a;
+    const long long to = __shfl_sync(0xffffffffu, at, a);
+    const int o = __shfl_sync(0xffffffffu, off, a) % 16;
+    if ((live >> a) & 1u) {
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const int d = 32 * j + lane;
+        const uint8_t* from = codes + a * kCodeRow + d;
+        uint8_t* dst = static_cast<uint8_t*>(p.v_cache) + to + d * 16;
+        auto word = [&](int i) {
+          return from[i * kCodeRow] | from[(i + 1) * kCodeRow] << 8 | from[(i + 2) * kCodeRow] << 16 |
+                 (uint32_t)from[(i + 3) * kCodeRow] << 24;
+        };
+        if (len == 16) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(word(0), word(4), word(8), word(12));
+        } else {
+          for (int i = 0; i < len;) {
+            if ((o + i) % 4 == 0 && len - i >= 4) {
+              *reinterpret_cast<uint32_t*>(dst + i) = word(i);
+              i += 4;
+            } else {
+              dst[i] = from[i * kCodeRow];
+              ++i;
+            }
+          }
+        }
+      }
+    }
+    a = next;
+  }
+}
 
 // T: queries, keys, values; FP8: the cache holds E4M3 codes (else T); V: elements of a vector
 template <typename T, bool FP8, bool INTERLEAVED, int V>
 __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_kernel(const RopeParams p, const RopePlan plan) {
-  __shared__ __align__(16) float2 cs_all[2][kMaxGroup * kMaxHalf];  // (c, s) of token, pair; two groups in turn
-  __shared__ RopeToken tok_all[2][kMaxGroup];
+  // (c, s) of token, pair; two groups in turn (FP8: or the values' codes)
+  constexpr int kBatch = kUnits<T, V>;
+  constexpr int kCs = kMaxGroup * kMaxHalf, kCodes = FP8 ? kRopeWarps * kValueTokens * kCodeRow / 16 : 0;
+  __shared__ __align__(16) float2 cs_all[2][kCs > kCodes ? kCs : kCodes];
+  // cache row (block * Hkv * B + offset) of the token's kv head 0; < 0: the token is skipped
+  __shared__ long long tok_all[2][kMaxGroup];
   const int half = p.rotary_dim / 2, D = p.head_size, per_head = 1 << plan.log2_per_head;
-  const int heads = p.num_q_heads + 2 * p.num_kv_heads;
+  const int heads = p.num_q_heads + (FP8 ? 1 : 2) * p.num_kv_heads;  // (FP8: values apart)
   const int per_token = heads << plan.log2_per_head;
   // pair V u + i of a token at [i / 2][u][i % 2] (V = 1: [u])
   auto cs_at = [&](int u, int i) { return V == 1 ? u : ((i / 2) * per_head + u) * 2 + i % 2; };
   griddep_wait();
   griddep_launch_dependents();
-  const int part = blockIdx.x % plan.parts;
-  const int first = blockIdx.x / plan.parts, step = gridDim.x / plan.parts;
+  int cta = blockIdx.x;
+  if constexpr (FP8) {
+    if (cta < plan.value_ctas) {
+      const int w = threadIdx.x >> 5, unit = cta * kRopeWarps + w, t0 = unit / p.num_kv_heads * plan.value_tokens;
+      if (t0 < p.num_tokens)
+        fp8_values(p, t0, min(plan.value_tokens, p.num_tokens - t0), unit % p.num_kv_heads,
+                   reinterpret_cast<uint8_t*>(cs_all) + w * (kValueTokens * kCodeRow));
+      return;
+    }
+    cta -= plan.value_ctas;
+  }
+  const int part = cta % plan.parts;
+  const int first = cta / plan.parts, step = (gridDim.x - plan.value_ctas) / plan.parts;
 
   if (threadIdx.x >= kRopeThreads) {
     // ---- slots and angles, one group ahead of the units
@@ -141,18 +238,15 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
       const int t0 = group * plan.tokens, nt = min(plan.tokens, p.num_tokens - t0);
       if (j < nt) {
         const long long slot = p.slot_mapping[t0 + j];
-        RopeToken x;
-        x.row = -1;
-        x.off = 0;
+        long long row = -1;
         if (slot >= 0) {
           const long long block = slot / p.block_size;
-          x.off = (int)(slot - block * p.block_size);
           if (block < p.num_blocks)
-            x.row = block * p.num_kv_heads * p.block_size + x.off;
+            row = block * p.num_kv_heads * p.block_size + (slot - block * p.block_size);
           else
             report_error(p.err_flag, PA_DEVERR_SLOT);
         }
-        tok_all[buf][j] = x;
+        tok_all[buf][j] = row;
       }
       if (j < half) {
         for (int t = 0; t < nt; ++t) {
@@ -194,8 +288,7 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
     } else {
       src[k] = kind[k] == kK ? static_cast<const T*>(p.key) + tl[k] * p.key_stride + (size_t)hk * D + e0
                              : static_cast<const T*>(p.value) + tl[k] * p.value_stride + (size_t)hk * D + e0;
-      // (values of an FP8 cache: [block][head][off / 16][d][off % 16])
-      dst[k] = (long long)hk * p.block_size * D + (FP8 && kind[k] == kV ? e0 * 16 : e0);
+      dst[k] = (long long)hk * p.block_size * D + e0;
     }
   }
   Vec<T, V> a[kBatch], b[kBatch];
@@ -213,13 +306,13 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
   for (int group = first; group < plan.groups; group += step, buf ^= 1) {
     const int t0 = group * plan.tokens, nt = min(plan.tokens, p.num_tokens - t0);
     const float2* cs = cs_all[buf];
-    const RopeToken* tok = tok_all[buf];
+    const long long* tok = tok_all[buf];
     __syncthreads();  // this group's are written, and the ones before, whose buffers come next, have been read
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const RopeToken x = tok[tl[k]];
+      const long long row = tok[tl[k]];
       // (a row < 0: padding, or a slot outside the pool)
-      if (kind[k] != kNone && tl[k] < nt && x.row >= 0) {
+      if (kind[k] != kNone && tl[k] < nt && row >= 0) {
         float u[V], w[V];
         a[k].get(u);
         b[k].get(w);
@@ -248,24 +341,16 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
         }
         if (kind[k] == kQ || !FP8) {
           T* d = kind[k] == kQ ? static_cast<T*>(p.q_out) + t0 * p.q_out_stride
-                               : static_cast<T*>(kind[k] == kK ? p.k_cache : p.v_cache) + x.row * D;
+                               : static_cast<T*>(kind[k] == kK ? p.k_cache : p.v_cache) + row * D;
           Vec<T, V> y, z;
           y.set(u);
           z.set(w);
           *reinterpret_cast<Vec<T, V>*>(d + dst[k]) = y;
           *reinterpret_cast<Vec<T, V>*>(d + dst[k] + apart[k]) = z;
-        } else if (kind[k] == kK) {
-          uint8_t* d = static_cast<uint8_t*>(p.k_cache) + x.row * D + dst[k];
+        } else {
+          uint8_t* d = static_cast<uint8_t*>(p.k_cache) + row * D + dst[k];
           *reinterpret_cast<Vec<uint8_t, V>*>(d) = codes_of(u, p.k_scale);
           *reinterpret_cast<Vec<uint8_t, V>*>(d + apart[k]) = codes_of(w, p.k_scale);
-        } else {
-          uint8_t* d = static_cast<uint8_t*>(p.v_cache) + (x.row - x.off + x.off / 16 * 16) * D + x.off % 16 + dst[k];
-          const Vec<uint8_t, V> y = codes_of(u, p.v_scale), z = codes_of(w, p.v_scale);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            d[i * 16] = y.x[i];
-            d[(apart[k] + i) * 16] = z.x[i];
-          }
         }
       }
     }
@@ -282,10 +367,10 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   const int per_head = p.head_size / (2 * V);
   plan.log2_per_head = 0;
   while ((1 << plan.log2_per_head) < per_head) ++plan.log2_per_head;
-  const long long per_token = (long long)(p.num_q_heads + 2 * p.num_kv_heads) * per_head;
+  const long long per_token = (long long)(p.num_q_heads + (FP8 ? 1 : 2) * p.num_kv_heads) * per_head;
   constexpr int kCtas = 152 * kRopeResident;
   // units of a CTA and group: as many as its threads hold, or, while that leaves SMs idle (a decode step), fewer
-  long long most = kBatch * kRopeThreads;
+  long long most = (long long)kUnits<T, V> * kRopeThreads;
   while (most > kRopeThreads && per_token * p.num_tokens < kCtas * most) most /= 2;
   plan.tokens = (int)(most / per_token);
   plan.tokens = plan.tokens < 1 ? 1 : plan.tokens > kMaxGroup ? kMaxGroup : plan.tokens;
@@ -293,7 +378,12 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   plan.part_units = plan.parts > 1 ? (int)((per_token + plan.parts - 1) / plan.parts + per_head - 1) / per_head * per_head : 0;
   plan.groups = (int)(((long long)p.num_tokens + plan.tokens - 1) / plan.tokens);
   const int walkers = kCtas / plan.parts > 0 ? kCtas / plan.parts : 1;  // CTAs of a part
-  const int grid = (plan.groups < walkers ? plan.groups : walkers) * plan.parts;
+  // (a step's tokens lie in groups of their own: fewer a warp, more warps)
+  plan.value_tokens = p.num_tokens <= 256 ? 1 : p.num_tokens <= 2048 ? 4 : kValueTokens;
+  const long long value_warps =
+      ((long long)p.num_tokens + plan.value_tokens - 1) / plan.value_tokens * p.num_kv_heads;
+  plan.value_ctas = FP8 ? (int)((value_warps + kRopeWarps - 1) / kRopeWarps) : 0;
+  const int grid = plan.value_ctas + (plan.groups < walkers ? plan.groups : walkers) * plan.parts;
   return launch_dependent(rope_kernel<T, FP8, INTERLEAVED, V>, dim3((unsigned)grid), dim3(kRopeThreads + kMaxHalf), 0, stream, p,
                           plan);
 }
@@ -304,6 +394,7 @@ cudaError_t launch_type(bool interleaved, const RopeParams& p, cudaStream_t stre
   // halves: vectors that neither half of the pairs cuts
   const int half = p.rotary_dim / 2;
   if (half % VMAX == 0) return launch_vec<T, FP8, false, VMAX>(p, stream);
+  if (VMAX > 4 && half % 4 == 0) return launch_vec<T, FP8, false, 4>(p, stream);
   if (half % 2 == 0) return launch_vec<T, FP8, false, 2>(p, stream);
   return launch_vec<T, FP8, false, 1>(p, stream);
 }

@@ -131,7 +131,7 @@ class Rope:
 @pytest.mark.parametrize("dtype,d,block_size", [("f32", 64, 5), ("f32", 128, 16), ("f16", 128, 8), ("f16", 64, 16),
                                                 ("bf16", 128, 32), ("bf16", 64, 8), ("fp8", 128, 16), ("fp8", 128, 48)])
 @pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("rotary", [2, 6, 18, 20, 32, 48, 64, 128])
+@pytest.mark.parametrize("rotary", [2, 6, 18, 20, 24, 32, 48, 64, 128])
 def test_rope(pa, dtype, d, block_size, interleaved, rotary):
     if rotary > d:
         rotary = d - 2
