@@ -308,50 +308,49 @@ def pa_copy_blocks(k_cache, v_cache, block_pairs, err_flag=None, stream=None, de
 
 
 # ---------------------------------------------------------------- rotary positions and windowed attention
-# A step makes one of these calls per layer, and a small one takes the GPU a few microseconds: the checks below
-# are kept to what finds a wrong argument, in the cheapest form.
-def _refuse(t, name: str, dtype, dev: int, where: str):
-    """Why ``t`` was refused (see _need)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev and not (t.device.type == "cpu" and t.is_pinned()):
-        raise ValueError(f"{where}: {name} is on {t.device}, the caches on cuda:{dev}")
+# A step makes one of these calls per layer, and a small one takes the GPU a few microseconds, so the checks are
+# written out: each call tests types and devices in one expression, and looks for the reason only when that fails.
+_ROWS: dict = {}  # cache dtype -> (dtype code, dtype of queries and new rows)
 
 
-def _need(t, name: str, dtype, dev: int, where: str) -> int:
-    """The address of a dense tensor of that type on device ``dev`` (or in pinned host memory)."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, name, dtype, dev, where)
-    if not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be contiguous")
-    return t.data_ptr()
+def _rows_of(dtype, where: str):
+    """(dtype code, dtype of queries and new rows) of a cache dtype."""
+    if not _ROWS:
+        import torch
+        _ROWS.update({torch.float32: (PA_F32, torch.float32), torch.float16: (PA_F16, torch.float16),
+                      torch.bfloat16: (PA_BF16, torch.bfloat16), torch.uint8: (PA_FP8_E4M3, torch.float16),
+                      torch.float8_e4m3fn: (PA_FP8_E4M3, torch.float16)})
+    if dtype not in _ROWS:
+        raise TypeError(f"{where}: unsupported cache dtype {dtype}")
+    return _ROWS[dtype]
+
+
+def _refuse(where: str, dev: int, host: bool, *tensors) -> None:
+    """Raises for the first (tensor, name, dtype) that has another dtype or is not on device ``dev`` (``host``: nor in
+    pinned host memory)."""
+    for t, name, dtype in tensors:
+        if t.dtype is not dtype:
+            raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != dev and not (host and t.device.type == "cpu" and t.is_pinned()):
+            raise ValueError(f"{where}: {name} is on {t.device}, the caches on cuda:{dev}")
 
 
 def _caches(k_cache, v_cache, desc, where: str):
-    """(device index, k address, v address, descriptor, dtype of queries and new rows) of a cache pair."""
-    import torch
+    """(device index, descriptor, dtype of queries and new rows) of a cache pair."""
     dev, dtype = k_cache.get_device(), k_cache.dtype
     if dev < 0:
         raise ValueError(f"{where}: the caches must be CUDA tensors")
-    if v_cache.dtype is not dtype or v_cache.numel() != k_cache.numel() or v_cache.get_device() != dev:
+    if v_cache.dtype is not dtype or v_cache.get_device() != dev or v_cache.numel() != k_cache.numel():
         raise ValueError(f"{where}: k_cache and v_cache must match in type, size and device")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError(f"{where}: the caches must be contiguous")
+    code, rows = _ROWS.get(dtype) or _rows_of(dtype, where)
     if desc is None:
-        desc = cache_desc(k_cache)
-    return dev, k_cache.data_ptr(), v_cache.data_ptr(), desc, torch.float16 if desc.dtype == PA_FP8_E4M3 else dtype
-
-
-def _launch(fn, args, dev: int, stream, where: str) -> None:
-    """fn on the arguments that args(stream) gives, with the tensors' device current."""
-    import torch
-    if torch.cuda.current_device() == dev:
-        status = fn(*args(_stream_of(dev, stream)))
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args(_stream_of(dev, stream)))
-    if status != PA_OK:
-        raise PaError(status, where)
+        shape = k_cache.shape
+        if len(shape) != 4:
+            raise ValueError("cache must be [num_blocks, num_kv_heads, block_size, head_size]")
+        desc = pa_cache_desc(shape[0], shape[2], shape[1], shape[3], code)
+    return dev, desc, rows
 
 
 def _stream_of(dev: int, stream) -> int:
@@ -359,6 +358,18 @@ def _stream_of(dev: int, stream) -> int:
         import torch
         return torch._C._cuda_getCurrentRawStream(dev)
     return int(getattr(stream, "cuda_stream", stream))
+
+
+def _launch(fn, dev: int, args, where: str) -> None:
+    """fn(*args) with the tensors' device current."""
+    import torch
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != PA_OK:
+        raise PaError(status, where)
 
 
 def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, method: int = PA_ROPE_PLAIN, factor: float = 1.0,
@@ -381,16 +392,15 @@ def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, method: int = PA
     return (inv if device is None else inv.to(device)), mag.value
 
 
-def _token_rows(t, name: str, dtype, tokens: int, heads: int, d: int, dev: int, where: str):
-    """(address, elements between tokens) of [tokens, heads, d], where a token's row is dense."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, name, dtype, dev, where)
-    if t.shape != (tokens, heads, d):
-        raise ValueError(f"{where}: {name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
+def _token_rows(t, name: str, shape, where: str) -> int:
+    """Elements between the tokens of [tokens, heads, head_size] = shape, where a token's row is dense."""
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} must be {list(shape)}, got {list(t.shape)}")
+    tokens, heads, d = shape
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+    if s2 != 1 or (s1 != d and heads > 1):
         raise ValueError(f"{where}: the heads of one token of {name} must be dense")
-    return t.data_ptr(), (s0 if tokens > 1 else heads * d)
+    return s0 if tokens > 1 else heads * d
 
 
 def pa_rope_and_cache(q_out, k_cache, v_cache, q, key, value, positions, slot_mapping, inv_freq,
@@ -407,44 +417,63 @@ def pa_rope_and_cache(q_out, k_cache, v_cache, q, key, value, positions, slot_ma
     ``interleaved``: pairs (2j, 2j + 1), else (j, j + rotary_dim / 2)."""
     import torch
     where = "pa_rope_and_cache"
-    dev, kc, vc, desc, rows = _caches(k_cache, v_cache, desc, where)
-    d, hkv = desc.head_size, desc.num_kv_heads
-    tokens, hq, qp, op, qs, os_ = key.shape[0], 0, None, None, 0, 0
-    if (q is None) != (q_out is None):
-        raise ValueError(f"{where}: q and q_out go together")
-    if q is not None:
-        hq = q.shape[1]
-        qp, qs = _token_rows(q, "q", rows, tokens, hq, d, dev, where)
-        op, os_ = (qp, qs) if q_out is q else _token_rows(q_out, "q_out", rows, tokens, hq, d, dev, where)
-    kp, ks = _token_rows(key, "key", rows, tokens, hkv, d, dev, where)
-    vp, vs = _token_rows(value, "value", rows, tokens, hkv, d, dev, where)
-    pos = _need(positions, "positions", torch.int32, dev, where)
-    slots = _need(slot_mapping, "slot_mapping", torch.int64, dev, where)
-    inv = _need(inv_freq, "inv_freq", torch.float64, dev, where)
+    dev, desc, rows = _caches(k_cache, v_cache, desc, where)
+    if not (key.dtype is rows and value.dtype is rows and positions.dtype is torch.int32 and
+            slot_mapping.dtype is torch.int64 and inv_freq.dtype is torch.float64 and key.get_device() == dev and
+            value.get_device() == dev and positions.get_device() == dev and slot_mapping.get_device() == dev and
+            inv_freq.get_device() == dev):
+        _refuse(where, dev, True, (key, "key", rows), (value, "value", rows), (positions, "positions", torch.int32),
+                (slot_mapping, "slot_mapping", torch.int64), (inv_freq, "inv_freq", torch.float64))
+    if not (positions.is_contiguous() and slot_mapping.is_contiguous() and inv_freq.is_contiguous()):
+        raise ValueError(f"{where}: positions, slot_mapping and inv_freq must be contiguous")
+    tokens, d, hkv = key.shape[0], desc.head_size, desc.num_kv_heads
     if positions.numel() != tokens or slot_mapping.numel() != tokens:
         raise ValueError(f"{where}: positions and slot_mapping must hold {tokens} tokens")
-    err = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, dev, where)
-    _launch(lib().pa_rope_and_cache, lambda st: (
-        op, kc, vc, qp, kp, vp, os_, qs, ks, vs, pos, slots, inv, tokens, hq, 2 * inv_freq.numel(),
-        1 if interleaved else 0, float(magnitude), desc, float(k_scale or 0.0), float(v_scale or 0.0), err, st), dev,
-        stream, where)
+    kv_shape = (tokens, hkv, d)
+    ks, vs = _token_rows(key, "key", kv_shape, where), _token_rows(value, "value", kv_shape, where)
+    hq = qs = os_ = 0
+    qp = op = err = None
+    if q is not None and q_out is not None:
+        if not (q.dtype is rows and q_out.dtype is rows and q.get_device() == dev and q_out.get_device() == dev):
+            _refuse(where, dev, True, (q, "q", rows), (q_out, "q_out", rows))
+        hq = q.shape[1]
+        q_shape = (tokens, hq, d)
+        qs, os_ = _token_rows(q, "q", q_shape, where), _token_rows(q_out, "q_out", q_shape, where)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q is not q_out:
+        raise ValueError(f"{where}: q and q_out go together")
+    if err_flag is not None:
+        _refuse(where, dev, False, (err_flag, "err_flag", torch.int32))
+        err = err_flag.data_ptr()
+    _launch(lib().pa_rope_and_cache, dev, (
+        op, k_cache.data_ptr(), v_cache.data_ptr(), qp, key.data_ptr(), value.data_ptr(), os_, qs, ks, vs,
+        positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), tokens, hq, 2 * inv_freq.numel(),
+        1 if interleaved else 0, float(magnitude), desc, float(k_scale or 0.0), float(v_scale or 0.0), err,
+        _stream_of(dev, stream)), where)
 
 
-def _attention(where, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc):
-    """The checks of both windowed attention calls: (device, rows' dtype, descriptor, addresses, table shape)."""
+def _attention(where, host, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc):
+    """The checks of both windowed attention calls: (device, rows' dtype, descriptor, address of err_flag, q's shape,
+    the table's shape)."""
     import torch
-    dev, kc, vc, desc, rows = _caches(k_cache, v_cache, desc, where)
-    op, qp = _need(out, "out", rows, dev, where), _need(q, "q", rows, dev, where)
-    bt = _need(block_tables, "block_tables", torch.int32, dev, where)
-    sl = _need(seq_lens, "seq_lens", torch.int32, dev, where)
-    err = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, dev, where)
-    shape = q.shape
+    dev, desc, rows = _caches(k_cache, v_cache, desc, where)
+    if not (out.dtype is rows and q.dtype is rows and block_tables.dtype is torch.int32 and
+            seq_lens.dtype is torch.int32 and out.get_device() == dev and q.get_device() == dev and
+            block_tables.get_device() == dev and seq_lens.get_device() == dev):
+        _refuse(where, dev, host, (out, "out", rows), (q, "q", rows), (block_tables, "block_tables", torch.int32),
+                (seq_lens, "seq_lens", torch.int32))
+    if not (out.is_contiguous() and q.is_contiguous() and block_tables.is_contiguous() and seq_lens.is_contiguous()):
+        raise ValueError(f"{where}: out, q, block_tables and seq_lens must be contiguous")
+    err = None
+    if err_flag is not None:
+        _refuse(where, dev, False, (err_flag, "err_flag", torch.int32))
+        err = err_flag.data_ptr()
+    shape, table = q.shape, block_tables.shape
     if len(shape) != 3 or shape[2] != desc.head_size or out.shape != shape:
         raise ValueError(f"{where}: q and out must be [queries, heads, {desc.head_size}]")
-    table = block_tables.shape
-    if len(table) != 2 or seq_lens.shape != table[:1]:
+    if len(table) != 2 or seq_lens.dim() != 1 or seq_lens.shape[0] != table[0]:
         raise ValueError(f"{where}: block_tables must be [num_seqs, max_blocks_per_seq], seq_lens [num_seqs]")
-    return dev, rows, desc, (op, qp, kc, vc), bt, sl, err, shape, table
+    return dev, rows, desc, err, shape, table
 
 
 def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, window: int, num_sinks: int = 0,
@@ -456,29 +485,34 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, scale: fl
     Table entries of blocks outside are never read (released blocks).  ``key`` / ``value`` [num_seqs, num_kv_heads,
     head_size]: each sequence's new token, stored at position seq_lens[s] - 1 and attended in the same launch
     (16-bit and FP8 caches).  No workspace."""
-    import torch
     where = "pa_decode_window"
-    dev, rows, desc, ptrs, bt, sl, err, shape, table = _attention(where, out, q, k_cache, v_cache, block_tables,
-                                                                  seq_lens, err_flag, desc)
+    dev, rows, desc, err, shape, table = _attention(where, True, out, q, k_cache, v_cache, block_tables, seq_lens,
+                                                    err_flag, desc)
     if table[0] != shape[0]:
         raise ValueError(f"{where}: one query per sequence")
-    new = [None, None]
-    for i, (t, n) in enumerate(((key, "key"), (value, "value"))):
-        if t is not None:
-            new[i] = _need(t, n, rows, dev, where)
-            if t.shape != (shape[0], desc.num_kv_heads, desc.head_size):
-                raise ValueError(f"{where}: {n} must be [{shape[0]}, {desc.num_kv_heads}, {desc.head_size}]")
-    opts = None
+    kp = vp = opts = None
+    if key is not None or value is not None:
+        if key is None or value is None:
+            raise ValueError(f"{where}: key and value go together")
+        if not (key.dtype is rows and value.dtype is rows and key.get_device() == dev and value.get_device() == dev):
+            _refuse(where, dev, True, (key, "key", rows), (value, "value", rows))
+        new = (shape[0], desc.num_kv_heads, desc.head_size)
+        if key.shape != new or value.shape != new or not (key.is_contiguous() and value.is_contiguous()):
+            raise ValueError(f"{where}: key and value must be {list(new)}, contiguous")
+        kp, vp = key.data_ptr(), value.data_ptr()
     if alibi_slopes is not None or k_scale is not None or v_scale is not None or test_flags:
         slopes = None
         if alibi_slopes is not None:
-            slopes = _need(alibi_slopes, "alibi_slopes", torch.float32, dev, where)
-            if alibi_slopes.numel() != shape[1]:
+            import torch
+            _refuse(where, dev, True, (alibi_slopes, "alibi_slopes", torch.float32))
+            if alibi_slopes.numel() != shape[1] or not alibi_slopes.is_contiguous():
                 raise ValueError(f"{where}: one ALiBi slope per query head")
+            slopes = alibi_slopes.data_ptr()
         opts = pa_decode_options(slopes, float(k_scale or 0.0), float(v_scale or 0.0), int(test_flags))
-    _launch(lib().pa_decode_window, lambda st: (
-        *ptrs, *new, bt, sl, shape[0], shape[1], table[1], desc, float(scale), int(window), int(num_sinks), err, st, opts),
-        dev, stream, where)
+    _launch(lib().pa_decode_window, dev, (
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, block_tables.data_ptr(),
+        seq_lens.data_ptr(), shape[0], shape[1], table[1], desc, float(scale), int(window), int(num_sinks), err,
+        _stream_of(dev, stream), opts), where)
 
 
 def pa_prefill_window(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_query_len: int, scale: float,
@@ -490,11 +524,14 @@ def pa_prefill_window(out, q, k_cache, v_cache, block_tables, seq_lens, query_st
     ``v_scale`` the scales of an FP8 cache (q and out are fp16 then)."""
     import torch
     where = "pa_prefill_window"
-    dev, rows, desc, ptrs, bt, sl, err, shape, table = _attention(where, out, q, k_cache, v_cache, block_tables,
-                                                                  seq_lens, err_flag, desc)
-    start = _need(query_start, "query_start", torch.int32, dev, where)
-    if query_start.shape != (table[0] + 1,):
+    dev, rows, desc, err, shape, table = _attention(where, False, out, q, k_cache, v_cache, block_tables, seq_lens,
+                                                    err_flag, desc)
+    if query_start.dtype is not torch.int32 or query_start.get_device() != dev:
+        _refuse(where, dev, False, (query_start, "query_start", torch.int32))
+    if query_start.dim() != 1 or query_start.shape[0] != table[0] + 1 or not query_start.is_contiguous():
         raise ValueError(f"{where}: query_start must be [num_seqs + 1]")
-    _launch(lib().pa_prefill_window, lambda st: (
-        *ptrs, bt, sl, start, table[0], shape[0], shape[1], table[1], int(max_query_len), desc, float(scale), int(window),
-        int(num_sinks), float(k_scale or 0.0), float(v_scale or 0.0), err, st), dev, stream, where)
+    _launch(lib().pa_prefill_window, dev, (
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), query_start.data_ptr(), table[0], shape[0], shape[1], table[1], int(max_query_len), desc,
+        float(scale), int(window), int(num_sinks), float(k_scale or 0.0), float(v_scale or 0.0), err,
+        _stream_of(dev, stream)), where)

@@ -291,3 +291,34 @@ def test_rope_graph_replay(pa):
     g.replay()
     torch.cuda.synchronize()
     r.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_rope_pinned_host_arrays(pa, dtype):
+    """The step's rows, positions and slots in pinned host memory."""
+    import torch
+    r = Rope(pa, dtype, 21, 8, 2, 128, 16, 64, False, seed=6, fused=False)
+    r.q, r.key, r.value, r.q_out = (t.cpu().pin_memory() for t in (r.q, r.key, r.value, r.q_out))
+    r.run()
+    torch.cuda.synchronize()
+    r.check()
+
+
+def test_rope_refuses_wrong_tensors(pa):
+    import torch
+    r = Rope(pa, "bf16", 5, 8, 2, 128, 16, 128, False, seed=6)
+    good = dict(q_out=r.q_out, k_cache=r.k, v_cache=r.v, q=r.q, key=r.key, value=r.value,
+                positions=torch.from_numpy(r.pos).cuda(), slot_mapping=torch.from_numpy(r.slots).cuda(),
+                inv_freq=r.inv.cuda())
+    for kw, error in ((dict(q=r.q.half()), TypeError), (dict(positions=good["positions"].long()), TypeError),
+                      (dict(slot_mapping=good["slot_mapping"].int()), TypeError),
+                      (dict(inv_freq=good["inv_freq"].float()), TypeError), (dict(inv_freq=r.inv), ValueError),
+                      (dict(q=None), ValueError), (dict(key=r.key.cpu()), ValueError), (dict(value=r.value[:4]), ValueError),
+                      (dict(key=r.key.transpose(0, 1)), ValueError), (dict(key=r.key[..., ::2]), ValueError),
+                      (dict(q=r.q[:, ::2], q_out=r.q_out[:, ::2]), ValueError),
+                      (dict(positions=good["positions"][:3]), ValueError),
+                      (dict(k_cache=r.k[0]), ValueError),
+                      (dict(q_out=r.key.expand(-1, -1, -1), q=r.q[:, :2]), pa.PaError)):  # q_out on the keys
+        with pytest.raises(error):
+            pa.pa_rope_and_cache(**{**good, **kw})
+    torch.cuda.synchronize()

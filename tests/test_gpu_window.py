@@ -392,3 +392,81 @@ def test_window_reads_lengths_written_just_before():
             s.decode()
     side.synchronize()
     check(s, ref, "right after the writes")
+
+
+# ---------------------------------------------------------------- arguments
+def pinned(t):
+    return t.cpu().pin_memory()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+def test_decode_window_pinned_host_arrays(dtype):
+    """The step's small arrays in pinned host memory, read and written in place: the same bits."""
+    import torch
+    w = WindowCase(dtype, [300, 0, 41], [1] * 3, 8, 2, 128, 16, 100, 4, seed=3, append=dtype != "f32")
+    s, t = Step(w), Step(w)
+    s.decode()
+    for name in ("q", "out", "table", "lens"):
+        setattr(t, name, pinned(getattr(t, name)))
+    if t.nk is not None:
+        t.nk, t.nv = pinned(t.nk), pinned(t.nv)
+    t.decode()
+    torch.cuda.synchronize()
+    assert int(t.err.item()) == 0
+    assert torch.equal(t.out, s.out.cpu())
+    assert torch.equal(t.k.view(torch.uint8), s.k.view(torch.uint8))
+
+
+def test_window_calls_refuse_wrong_tensors(pa):
+    import torch
+    w = WindowCase("bf16", [30, 20], [1, 1], 8, 2, 128, 16, 10, 2, seed=3)
+    s = Step(w)
+    good = dict(out=s.out, q=s.q, k_cache=s.k, v_cache=s.v, block_tables=s.table, seq_lens=s.lens)
+
+    def decode(**kw):
+        pa.pa_decode_window(**{**good, **kw}, scale=0.1, window=10)
+
+    def prefill(start=s.start, **kw):
+        pa.pa_prefill_window(**{**good, **kw}, query_start=start, max_query_len=1, scale=0.1, window=10)
+
+    for call in (decode, prefill):
+        for kw, error in ((dict(q=s.q.half()), TypeError), (dict(out=s.out.float()), TypeError),
+                          (dict(block_tables=s.table.long()), TypeError), (dict(seq_lens=s.lens.long()), TypeError),
+                          (dict(q=s.q.cpu()), ValueError), (dict(seq_lens=s.lens[:1]), ValueError),
+                          (dict(q=s.q[:, :, :64]), ValueError), (dict(q=s.q[:, :4]), ValueError),
+                          (dict(v_cache=s.v.half()), ValueError), (dict(v_cache=s.v[:1]), ValueError),
+                          (dict(block_tables=s.table[:, ::2]), ValueError), (dict(err_flag=torch.zeros(1)), TypeError),
+                          (dict(err_flag=pinned(s.err)), ValueError)):
+            with pytest.raises(error):
+                call(**kw)
+    with pytest.raises(ValueError):  # tensor-map copies move q and out
+        prefill(q=pinned(s.q))
+    with pytest.raises(ValueError):
+        prefill(start=s.start[:2])
+    with pytest.raises(ValueError):
+        decode(key=s.q[:, :2].contiguous())
+    with pytest.raises(ValueError):
+        decode(key=s.q, value=s.q)
+    with pytest.raises(ValueError):
+        decode(alibi_slopes=torch.zeros(3, device="cuda"))
+    with pytest.raises(pa.PaError):
+        pa.pa_decode_window(**good, scale=0.1, window=0)
+    torch.cuda.synchronize()
+
+
+def test_windowless_empty_batches(pa):
+    """No sequences, no queries, no table: nothing to do."""
+    import torch
+    w = WindowCase("bf16", [30, 20], [1, 1], 8, 2, 128, 16, 10, 2, seed=3)
+    s = Step(w)
+    before = s.out.clone()
+    pa.pa_decode_window(s.out[:0], s.q[:0], s.k, s.v, s.table[:0], s.lens[:0], 0.1, 10)
+    pa.pa_prefill_window(s.out, s.q, s.k, s.v, s.table, s.lens, torch.zeros_like(s.start), 0, 0.1, 10)
+    pa.pa_prefill_window(s.out, s.q, s.k, s.v, s.table, s.lens, torch.zeros_like(s.start), 3, 0.1, 10, err_flag=s.err)
+    torch.cuda.synchronize()
+    assert int(s.err.item()) == 0 and torch.equal(s.out, before)
+    # a table without columns: only empty sequences fit
+    zero = torch.zeros_like(s.lens)
+    pa.pa_decode_window(s.out, s.q, s.k, s.v, s.table[:, :0].contiguous(), zero, 0.1, 10, err_flag=s.err)
+    torch.cuda.synchronize()
+    assert int(s.err.item()) == 0 and torch.count_nonzero(s.out) == 0
