@@ -75,7 +75,8 @@ KERNEL_SOURCES = ("pa_api.cu", "pa_decode_tc.cu", "pa_decode_slab.cuh", "pa_deco
 
 
 # sources that define the prefill call's kernel
-PREFILL_SOURCES = ("pa_prefill_api.cu", "pa_prefill_tc.cu", "pa_prefill.h", "pa_device.cuh", "pa_internal.h")
+PREFILL_SOURCES = ("pa_prefill_api.cu", "pa_prefill_tc.cu", "pa_prefill.h", "pa_cluster.cuh", "pa_fp8.cuh", "pa_launch.h",
+                   "pa_device.cuh", "pa_internal.h")
 # sources that define the decode call on an FP8 cache
 FP8_SOURCES = ("pa_api.cu", "pa_decode_fp8.cu", "pa_decode_epilogue.cuh", "pa_device.cuh", "pa_internal.h",
                "pa_merge.cu")

@@ -818,25 +818,25 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
           }
         }
         if (is_v) {
-          // this half of the blocks not copied above: rows inside the sequence of an in-pool block by
-          // cp.async, the rest zeros.  Four rows of eight 16-byte chunks per step; the four rows lie in
-          // one block (B is a multiple of 16), so every branch below is uniform across the warp.
-          const unsigned partial = __ballot_sync(0xffffffffu, blk < blocks_per_tile && !whole);
+          // this half of the blocks not copied above, block by block: rows that count, of an in-pool block, by
+          // cp.async, the rest zeros; four rows of eight 16-byte chunks per step
+          unsigned partial = __ballot_sync(0xffffffffu, blk < blocks_per_tile && !whole);
           if (partial) {
-            const int first = (__ffs(partial) - 1) * B;  // rows before the first such block are all copied
-            for (int r0 = first; r0 < kTile; r0 += 4) {
-              const int b = r0 / B;
-              const int e = __shfl_sync(0xffffffffu, entry, b);
-              if (!((partial >> b) & 1)) continue;
-              const int r = r0 + (lane >> 3), chunk = lane & 7;
-              const int pos = key_pos(it, (first_tile(it) + t) * kTile + r);
-              uint8_t* dst = st + swz128(r, chunk);
-              if (pos < it.L && block_seen(it, pos, 1) && e >= 0 && e < p.num_blocks)
-                cp_async16(dst, cache + (((size_t)e * p.num_kv_heads + it.hkv) * B + (pos % B)) * kD + half * 64 +
-                                    chunk * 8);
-              else
-                *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
-            }
+            do {
+              const int b = __ffs(partial) - 1;
+              partial &= partial - 1;
+              const int e = __shfl_sync(0xffffffffu, entry, b), pos0 = __shfl_sync(0xffffffffu, first_pos, b);
+              const bool in = e >= 0 && e < p.num_blocks;
+              const int chunk = lane & 7;
+              const T* src = cache + ((size_t)(in ? e : 0) * p.num_kv_heads + it.hkv) * B * kD + half * 64 + chunk * 8;
+              for (int r = lane >> 3; r < B; r += 4) {
+                uint8_t* dst = st + swz128(b * B + r, chunk);
+                if (in && pos0 + r < it.L && block_seen(it, pos0 + r, 1))
+                  cp_async16(dst, src + (size_t)r * kD);
+                else
+                  *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+              }
+            } while (partial);
             cp_async_wait_all();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic writes -> tensor-core reads
           }

@@ -322,3 +322,24 @@ def test_rope_refuses_wrong_tensors(pa):
         with pytest.raises(error):
             pa.pa_rope_and_cache(**{**good, **kw})
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype,num_blocks", [("bf16", 140000), ("fp8", 270000)])
+def test_rope_large_pool(pa, dtype, num_blocks):
+    """Slots past 2^31 elements (2^32 bytes) of the caches: the last blocks take what a small pool takes."""
+    import torch
+    r = Rope(pa, dtype, 100, 8, 8, 128, 16, 128, False, seed=2)
+    t = Rope(pa, dtype, 100, 8, 8, 128, 16, 128, False, seed=2)
+    r.run()
+    small, shift = t.num_blocks, num_blocks - t.num_blocks
+    first = t.k[:1], t.v[:1]
+    t.k = torch.zeros((num_blocks, *t.k.shape[1:]), dtype=t.k.dtype, device="cuda")
+    t.v = torch.zeros((num_blocks, *t.v.shape[1:]), dtype=t.v.dtype, device="cuda")
+    t.k[shift:], t.v[shift:] = first[0], first[1]
+    t.slots = t.slots + shift * 16
+    t.run()
+    assert int(t.err.item()) == 0
+    assert torch.equal(t.k[shift:], r.k) and torch.equal(t.v[shift:], r.v) and torch.equal(t.q_out, r.q_out)
+    assert torch.count_nonzero(t.k[:small]) == 0 and torch.count_nonzero(t.v[:small]) == 0
+    del t
+    torch.cuda.empty_cache()

@@ -247,12 +247,18 @@ def test_prefill_window_short_chunks(dtype):
 
 
 @pytest.mark.parametrize("dtype,block_size", [("bf16", 16), ("f16", 64), ("fp8", 32), ("bf16", 8)])
-@pytest.mark.parametrize("window,sinks", [(2500, 3), (1100, 0), (BIG, 0), (700, 400)])
-def test_prefill_window_few_long_items(dtype, block_size, window, sinks):
+@pytest.mark.parametrize("window,sinks,lens,chunks", [
+    (2500, 3, [3100, 2600, 130, 3, 900], [64, 33, 50, 3, 0]),   # four CTAs an item
+    (1100, 0, [3100, 2600, 130, 3, 900], [64, 33, 50, 3, 0]),   # two
+    (BIG, 0, [3100, 2600, 130, 3, 900], [64, 33, 50, 3, 0]),    # four
+    (700, 400, [3100, 2600, 130, 3, 900], [64, 33, 50, 3, 0]),  # two
+    (4300, 5, [4700, 40], [40, 40]),                            # eight
+    (900, 0, [3000, 1500], [300, 150]),                         # two, more query tiles
+])
+def test_prefill_window_few_long_items(dtype, block_size, window, sinks, lens, chunks):
     """Few items over many keys: the CTAs of a cluster share an item's key tiles and merge their rows; the short
     sequences leave some of them without a tile, a ragged chunk some rows outside it."""
-    lens, chunks = [3100, 2600, 130, 3, 900], [300, 150, 70, 3, 0]
-    w = WindowCase(dtype, lens, chunks, 16, 2, 128, block_size, window, sinks, seed=window % 97)
+    w = WindowCase(dtype, lens, chunks, 8, 1, 128, block_size, window, sinks, seed=window % 97)
     s = Step(w)
     s.prefill()
     check(s, w.reference(), "few long items")
@@ -470,3 +476,47 @@ def test_windowless_empty_batches(pa):
     pa.pa_decode_window(s.out, s.q, s.k, s.v, s.table[:, :0].contiguous(), zero, 0.1, 10, err_flag=s.err)
     torch.cuda.synchronize()
     assert int(s.err.item()) == 0 and torch.count_nonzero(s.out) == 0
+
+
+def in_large_pool(s, num_blocks):
+    """The step's blocks as the last ones of a pool of num_blocks (offsets past 32 bits)."""
+    import torch
+    w, shift = s.w, num_blocks - s.w.num_blocks
+    for name in ("k", "v"):
+        small = getattr(s, name)
+        big = torch.zeros((num_blocks, *small.shape[1:]), dtype=small.dtype, device="cuda")
+        big[shift:] = small
+        setattr(s, name, big)
+    inside = (s.table >= 0) & (s.table < w.num_blocks)
+    s.table = torch.where(inside, s.table + shift, torch.full_like(s.table, -1))
+    return s
+
+
+@pytest.mark.parametrize("dtype,num_blocks", [("f32", 70000), ("bf16", 140000), ("fp8", 270000)])
+def test_window_large_pool(dtype, num_blocks):
+    """Caches of more than 2^31 elements (2^32 bytes): the step, its append, and a chunk, in their last blocks."""
+    import torch
+    hkv = 16 if dtype == "f32" else 8
+    w = WindowCase(dtype, [500, 90, 17], [1] * 3, 2 * hkv, hkv, 128, 16, 60, 4, seed=1, append=dtype != "f32")
+    s = in_large_pool(Step(w), num_blocks)
+    s.decode()
+    check(s, w.reference(), "decode")
+    assert torch.count_nonzero(s.k[:1000].view(torch.uint8)) == 0
+    del s
+    torch.cuda.empty_cache()
+    w = WindowCase(dtype, [500, 90], [70, 90], 2 * hkv, hkv, 128, 16, 60, 4, seed=2)
+    s = in_large_pool(Step(w), num_blocks)
+    s.prefill()
+    check(s, w.reference(), "chunk")
+    del s
+    torch.cuda.empty_cache()
+
+
+def test_decode_window_longer_than_int32():
+    """A window past int32 sees everything, as one of 2^31 - 1 does."""
+    w = WindowCase("bf16", [50, 300], [1, 1], 8, 2, 128, 16, BIG, 0, seed=3)
+    s = Step(w)
+    ref = w.reference()
+    w.window = 2 ** 32 + 5
+    s.decode()
+    check(s, ref, "long window")
