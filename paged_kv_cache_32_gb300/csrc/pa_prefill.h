@@ -18,6 +18,7 @@ struct PrefillParams {
   int32_t* err_flag;            // nullable
   int32_t num_seqs, num_q_heads, num_kv_heads;
   int32_t max_blocks, block_size, num_blocks;
+  int32_t head_size;            // 128; windowed form over 16-bit caches: 64 too
   int32_t q_tiles;              // query tiles of the longest chunk: ceil(max_query_len / 128) in the plain form
   int32_t num_query_tokens;     // rows of q and out
   float scale_log2;

@@ -82,6 +82,7 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
   p.max_blocks = max_blocks_per_seq;
   p.block_size = cache->block_size;
   p.num_blocks = cache->num_blocks;
+  p.head_size = cache->head_size;
   p.q_tiles = (int32_t)q_tiles;
   p.num_query_tokens = num_query_tokens;
   p.scale_log2 = scale * 1.4426950408889634f;

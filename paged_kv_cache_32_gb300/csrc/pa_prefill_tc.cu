@@ -80,6 +80,7 @@
 //  * Blocks without a position that some query of the chunk sees are not read
 //    (they may have been released); their value rows read as zeros, as the rows
 //    past the sequence do.
+//  * Head size 64: one 64-column half of each tile, N = 64 for P V, two producers.
 //  * FP8 caches (kFp8, fp16 queries): the producers load the codes into registers
 //    a tile ahead, convert them to fp16 (exact) and store the swizzled tiles
 //    themselves.  Values lie in the cache with a dimension's 16 tokens side by
@@ -105,7 +106,7 @@ namespace pa {
 namespace {
 
 constexpr int kTile = 128;            // queries per CTA = keys per key tile
-constexpr int kD = 128;               // head size of this kernel
+constexpr int kFp8D = 128;            // head size of every FP8 cache
 constexpr int kHalf = kTile * 128;    // one 128-row x 128-byte swizzled region (16 KB)
 constexpr int kKOff = 0;              // K stages: 2 x 2 regions (dims 0-63, 64-127)
 constexpr int kVOff = 4 * kHalf;      // V stages: 2 x 2 regions
@@ -197,11 +198,11 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uin
 }
 
 // instruction descriptor, kind::f16: fp32 accumulate, A/B element type (0 f16, 1 bf16), B major (0 K, 1 MN),
-// M = N = 128
+// M = 128
 template <typename T>
-__device__ __forceinline__ constexpr uint32_t idesc(uint32_t b_mn) {
+__device__ __forceinline__ constexpr uint32_t idesc(uint32_t b_mn, int n) {
   constexpr uint32_t ab = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-  return (1u << 4) | (ab << 7) | (ab << 10) | (b_mn << 16) | ((uint32_t)(kTile >> 3) << 17) |
+  return (1u << 4) | (ab << 7) | (ab << 10) | (b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kTile >> 4) << 24);
 }
 
@@ -579,7 +580,7 @@ __device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, i
       const int key0 = 32 * w + 16 * g;  // the group lies in one block
       const int e = __shfl_sync(0xffffffffu, entry, key0 >> log2_b);
       // 16 tokens of one head: 2 KB side by side, rows of K or [D][16] of V
-      const uint8_t* src = cache + (((size_t)(e * p.num_kv_heads + it.hkv) << log2_b) + (key0 & (B - 1))) * kD;
+      const uint8_t* src = cache + (((size_t)(e * p.num_kv_heads + it.hkv) << log2_b) + (key0 & (B - 1))) * kFp8D;
 #pragma unroll
       for (int i = 0; i < 4; ++i) raw[4 * g + i] = load_codes(src + 512 * i, e >= 0);
     };
@@ -641,9 +642,10 @@ __device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, i
 // Split items (few items, long windows): the CTAs of a cluster each left the unnormalised rows of their share of
 // the keys, then (reference maximum in log2 units, sum), kPartRow floats a row; each now merges its share of the
 // rows through distributed shared memory.  Every thread of the cluster comes here once.
-constexpr int kPartRow = kD + 4;
-static_assert(kTile * kPartRow * 4 <= 8 * kHalf, "the rows fit the K and V stages");
-template <typename T>
+template <int D>
+constexpr int kPartRow = D + 4;
+static_assert(kTile * kPartRow<128> * 4 <= 8 * kHalf, "the rows fit the K and V stages");
+template <typename T, int D>
 __device__ __forceinline__ void split_merge(const PrefillParams& p, const float* part, int idx) {
   cluster_sync_all();
   PfWindowItem it;
@@ -651,18 +653,18 @@ __device__ __forceinline__ void split_merge(const PrefillParams& p, const float*
   if (has_item) {
     const int rank = (int)cluster_rank(), C = p.split;
     const int begin = it.rows * rank / C, count = it.rows * (rank + 1) / C - begin;
-    for (int i = threadIdx.x; i < count * (kD / 4); i += blockDim.x) {
-      const int r = begin + i / (kD / 4), col = i % (kD / 4) * 4;
-      const float* row = part + r * kPartRow;
+    for (int i = threadIdx.x; i < count * (D / 4); i += blockDim.x) {
+      const int r = begin + i / (D / 4), col = i % (D / 4) * 4;
+      const float* row = part + r * kPartRow<D>;
       float mx = -INFINITY;
-      for (int c = 0; c < C; ++c) mx = fmaxf(mx, ld_cluster(row + kD, c));
+      for (int c = 0; c < C; ++c) mx = fmaxf(mx, ld_cluster(row + D, c));
       float l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int c = 0; c < C; ++c) {
-        const float m = ld_cluster(row + kD, c);
+        const float m = ld_cluster(row + D, c);
         const float w = m == -INFINITY ? 0.f : fast_exp2(m - mx);
         const float4 x = ld_cluster4(row + col, c);
-        l = fmaf(w, ld_cluster(row + kD + 1, c), l);
+        l = fmaf(w, ld_cluster(row + D + 1, c), l);
         acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
       }
       const float inv = l > 0.f ? p.v_scale / l : 0.f;
@@ -671,7 +673,7 @@ __device__ __forceinline__ void split_merge(const PrefillParams& p, const float*
       uint2 y;
       y.x = Mma<T>::pack(acc.x * inv, acc.y * inv);
       y.y = Mma<T>::pack(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (query * p.num_q_heads + head) * kD + col) = y;
+      *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (query * p.num_q_heads + head) * D + col) = y;
     }
   }
   cluster_sync_all();  // no CTA leaves while another reads its rows
@@ -684,12 +686,15 @@ enum class PfForm { kPlain, kWindow, kSplit };
 // items; the K/V rings, the S buffers and their barriers run on across items (tg counts this CTA's
 // key tiles so far), so the next item's Q, K/V copies and first S MMAs overlap this item's last
 // P V and epilogue.
-template <typename T, PfForm kForm, bool kFp8>
+// D: head size (64: windowed forms)
+template <typename T, PfForm kForm, bool kFp8, int D>
 __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                       const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_out,
                       const PrefillParams p) {
   constexpr bool kWindow = kForm != PfForm::kPlain, kSplit = kForm == PfForm::kSplit;
+  constexpr int kHalves = D / 64;  // 64-column halves of a row
+  static_assert(D == 128 || (D == 64 && kWindow && !kFp8), "head size");
   using Item = typename std::conditional<kSplit, PfSplitItem,
                                          typename std::conditional<kWindow, PfWindowItem, PfItem>::type>::type;
   // split: the CTAs of a cluster take the same items
@@ -698,7 +703,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
   const int n_items = p.num_seqs * (kWindow ? p.num_q_heads >> p.pack_log2 : p.num_q_heads) * p.q_tiles;
   const int B = p.block_size;
   const int blocks_per_tile = kTile / B;
-  const int slots = 2 * blocks_per_tile;  // tensor-map copies per tile: one per block and half
+  const int slots = kHalves * blocks_per_tile;  // tensor-map copies per tile: one per block and half
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -729,7 +734,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       // each copy slot arrives once per tile (with its bytes, or none); FP8: each producer warp
       mbar_init(&bar_k[b], kFp8 ? kFp8Producers / 2 : slots);
-      mbar_init(&bar_v[b], kFp8 ? kFp8Producers / 2 : slots + 2);  // + each V producer's partial-block / zero-fill arrival
+      mbar_init(&bar_v[b], kFp8 ? kFp8Producers / 2 : slots + kHalves);  // + each V producer's partial-block / zero-fill arrival
     }
     for (int b = 0; b < kSBufs; ++b) {
       mbar_init(&bar_s[b], 1);
@@ -776,7 +781,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     constexpr int kPastEnd = INT_MIN;
     const int blk = lane;  // lane b < blocks_per_tile copies this half of block b of every tile
     if (lane == 0) tma_prefetch_descriptor(tmap);
-    bool ok = true;
+    bool ok = half < kHalves;  // (head size 64: two producers)
     int tg = 0;
     for (int idx = idx0; ok && idx < n_items; idx += idx_step) {
       Item it;
@@ -828,11 +833,11 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
               const int e = __shfl_sync(0xffffffffu, entry, b), pos0 = __shfl_sync(0xffffffffu, first_pos, b);
               const bool in = e >= 0 && e < p.num_blocks;
               const int chunk = lane & 7;
-              const T* src = cache + ((size_t)(in ? e : 0) * p.num_kv_heads + it.hkv) * B * kD + half * 64 + chunk * 8;
+              const T* src = cache + ((size_t)(in ? e : 0) * p.num_kv_heads + it.hkv) * B * D + half * 64 + chunk * 8;
               for (int r = lane >> 3; r < B; r += 4) {
                 uint8_t* dst = st + swz128(b * B + r, chunk);
                 if (in && pos0 + r < it.L && block_seen(it, pos0 + r, 1))
-                  cp_async16(dst, src + (size_t)r * kD);
+                  cp_async16(dst, src + (size_t)r * D);
                 else
                   *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
               }
@@ -849,7 +854,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
   } else if (warp == kSWarp) {
     // =================================================================== S = Q K^T issuer
     if (lane == 0) {
-      const uint32_t id_s = idesc<T>(0);
+      const uint32_t id_s = idesc<T>(0, kTile);
       tma_prefetch_descriptor(&tmap_q);
       // This thread also schedules: it publishes item k (the first one with queries at or after index
       // idx) in items[k % 2] and starts the copy of its Q tile into Q buffer k % 2, both completing
@@ -864,9 +869,9 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         ++n_pub;
         if (idx < n_items) {
           uint8_t* qb = qbuf + (k & 1) * 2 * kHalf;
-          mbar_arrive_expect_tx(bar_qs, 2 * kHalf);
+          mbar_arrive_expect_tx(bar_qs, kHalves * kHalf);
           tma_load_3d(qb, &tmap_q, 0, it.h, it.q0 + it.tile0, bar_qs);
-          tma_load_3d(qb + kHalf, &tmap_q, 64, it.h, it.q0 + it.tile0, bar_qs);
+          if (kHalves > 1) tma_load_3d(qb + kHalf, &tmap_q, 64, it.h, it.q0 + it.tile0, bar_qs);
         } else {
           mbar_arrive(bar_qs);
         }
@@ -906,7 +911,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
           tc_fence_after();
           const uint32_t kb = smem_u32(smem + kKOff + (tg & 1) * 2 * kHalf);
 #pragma unroll
-          for (int kk = 0; kk < kD / 16; ++kk)
+          for (int kk = 0; kk < D / 16; ++kk)
             mma_ss(tmem + buf * 128, sw128_desc(qa + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024),
                    sw128_desc(kb + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024), id_s, kk > 0);
           mma_commit(&bar_s[buf]);
@@ -922,7 +927,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
   } else if (warp == kPVWarp) {
     // =================================================================== O += P V issuer
     if (lane == 0) {
-      const uint32_t id_o = idesc<T>(kFp8 ? 0 : 1);  // FP8 caches: V^T, rows of 64 keys
+      const uint32_t id_o = idesc<T>(kFp8 ? 0 : 1, D);  // FP8 caches: V^T, rows of 64 keys
       bool ok = true;
       int tg = 0, item_no = 0;
       int prev_row0 = 0, prev_h = 0;  // the previous item's output tile
@@ -935,7 +940,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         ok = wait_bar_spin(bar_staged, (item_no - 1) & 1, abort_flag);
         if (ok && prev_full) {
           tma_store_3d(&tmap_out, 0, prev_h, prev_row0, smem + kOutOff);
-          tma_store_3d(&tmap_out, 64, prev_h, prev_row0, smem + kOutOff + kHalf);
+          if (kHalves > 1) tma_store_3d(&tmap_out, 64, prev_h, prev_row0, smem + kOutOff + kHalf);
           bulk_commit_group();
         }
       };
@@ -1095,7 +1100,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
           ok = warp_wait(&bar_o[(tg - 1) % kSBufs], ((tg - 1) / kSBufs) & 1);
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < kHalves; ++c) {
             float o[32];
             tmem_ld16x256_x8(tmem + half_base + kOCol + 64 * c, o);
             tmem_wait_ld<32>(o);
@@ -1199,7 +1204,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       auto out_row = [&](int r) {
         const size_t query = (size_t)orow0 + (kWindow ? r >> p.pack_log2 : r);
         const int head = kWindow ? oh + (r & ((1 << p.pack_log2) - 1)) : oh;
-        return reinterpret_cast<T*>(p.out) + (query * p.num_q_heads + head) * kD;
+        return reinterpret_cast<T*>(p.out) + (query * p.num_q_heads + head) * D;
       };
       const int rows = it.rows;
       [[maybe_unused]] const float pm0 = m0, pm1 = m1;  // split: this item's reference maxima
@@ -1211,10 +1216,10 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       if (ok) ok = warp_wait(bar_done, item_no & 1);
       if (!ok) break;
       tc_fence_after();
-      float o[64];
+      float o[D / 2];
       tmem_ld16x256_x8(tmem + half_base + kOCol, o);
-      tmem_ld16x256_x8(tmem + half_base + kOCol + 64, o + 32);
-      tmem_wait_ld<64>(o);
+      if constexpr (kHalves > 1) tmem_ld16x256_x8(tmem + half_base + kOCol + 64, o + 32);
+      tmem_wait_ld<D / 2>(o);
       // O may take the next item's first P V
       tc_fence_before();
       __syncwarp();
@@ -1224,13 +1229,13 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         // this CTA touches the K and V stages any more: bar_done)
         float* part = reinterpret_cast<float*>(smem + kKOff);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          *reinterpret_cast<float2*>(part + r0 * kPartRow + 8 * j + 2 * c4) = make_float2(o[4 * j], o[4 * j + 1]);
-          *reinterpret_cast<float2*>(part + r1 * kPartRow + 8 * j + 2 * c4) = make_float2(o[4 * j + 2], o[4 * j + 3]);
+        for (int j = 0; j < D / 8; ++j) {
+          *reinterpret_cast<float2*>(part + r0 * kPartRow<D> + 8 * j + 2 * c4) = make_float2(o[4 * j], o[4 * j + 1]);
+          *reinterpret_cast<float2*>(part + r1 * kPartRow<D> + 8 * j + 2 * c4) = make_float2(o[4 * j + 2], o[4 * j + 3]);
         }
         if (c4 == 0) {
-          *reinterpret_cast<float2*>(part + r0 * kPartRow + kD) = make_float2(pm0, s0);
-          *reinterpret_cast<float2*>(part + r1 * kPartRow + kD) = make_float2(pm1, s1);
+          *reinterpret_cast<float2*>(part + r0 * kPartRow<D> + D) = make_float2(pm0, s0);
+          *reinterpret_cast<float2*>(part + r1 * kPartRow<D> + D) = make_float2(pm1, s1);
         }
         __syncwarp();
         if (kStagedOut<T> && lane == 0) mbar_arrive(bar_staged);
@@ -1245,7 +1250,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         // 4c .. 4c + 3 of each chunk, so the eight rows and four threads of a store fall in 32 banks.
         uint8_t* stage = smem + kOutOff;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < D / 8; ++j) {
           uint8_t* col = stage + (j >> 3) * kHalf + 4 * c4;
           *reinterpret_cast<uint32_t*>(col + swz128(r0, j & 7)) =
               Mma<T>::pack(o[4 * j] * inv0, o[4 * j + 1] * inv0);
@@ -1257,12 +1262,13 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic writes -> the tensor-map store
         } else {
           // a ragged tile (the last of a chunk): its rows past the chunk belong to another sequence, so this
-          // warp copies its own rows inside the chunk out, 16 lanes per 256-byte row
+          // warp copies its own rows inside the chunk out, 16 bytes a lane
           __syncwarp();
           const int row_base = r0 - (lane >> 2);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rl = 2 * i + (lane >> 4), chunk = lane & 15;  // row row_base + rl, bytes 16 chunk ..
+          for (int i = 0; i < D / 16; ++i) {
+            constexpr int kLanes = D / 8;  // of a row
+            const int rl = 32 / kLanes * i + lane / kLanes, chunk = lane % kLanes;  // row row_base + rl, bytes 16 chunk ..
             const int r = row_base + rl;
             if (r < rows) {
               const uint4 v = *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * kHalf + swz128(r, chunk & 7));
@@ -1283,7 +1289,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         for (int rr = 0; rr < 2; ++rr) {
           const float inv = rr ? inv1 : inv0;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < D / 32; ++g) {
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -1327,13 +1333,13 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       for (int t = max(0, n_o - kSBufs); t < n_o; ++t) drain_wait(&bar_o[t % kSBufs], (t / kSBufs) & 1);
     __syncthreads();
   }
-  if constexpr (kSplit) split_merge<T>(p, reinterpret_cast<const float*>(smem + kKOff), idx0);
+  if constexpr (kSplit) split_merge<T, D>(p, reinterpret_cast<const float*>(smem + kKOff), idx0);
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 // one CTA per SM (the kernel holds all of tensor memory and most of shared memory), at most one per item
-template <typename T, PfForm kForm, bool kFp8 = false>
+template <typename T, PfForm kForm, bool kFp8 = false, int D = 128>
 static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                   const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
   const long long items = (long long)p.num_seqs * (p.num_q_heads >> p.pack_log2) * p.q_tiles;
@@ -1345,30 +1351,35 @@ static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, 
   if (e != cudaSuccess) return e;
   // split: one cluster an item
   const unsigned grid = (unsigned)(p.split > 1 ? items * p.split : items < sms ? items : sms);
-  auto kernel = prefill_tc_kernel<T, kForm, kFp8>;
+  auto kernel = prefill_tc_kernel<T, kForm, kFp8, D>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, dim3(grid), dim3(kFp8 ? kFp8Threads : kThreads), kSmemBytes, p.split, false, stream, tk,
                         tv, tq, to, p);
 }
 
-template <typename T, bool kFp8>
+template <typename T, bool kFp8, int D>
 static cudaError_t launch_window(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                  const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
-  return p.split > 1 ? launch_prefill<T, PfForm::kSplit, kFp8>(tk, tv, tq, to, p, stream)
-                     : launch_prefill<T, PfForm::kWindow, kFp8>(tk, tv, tq, to, p, stream);
+  return p.split > 1 ? launch_prefill<T, PfForm::kSplit, kFp8, D>(tk, tv, tq, to, p, stream)
+                     : launch_prefill<T, PfForm::kWindow, kFp8, D>(tk, tv, tq, to, p, stream);
 }
 
 cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                               const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
   const bool window = p.window > 0;
+  if (p.head_size == 64) {
+    if (dtype == PA_F16 && window) return launch_window<__half, false, 64>(tk, tv, tq, to, p, stream);
+    if (dtype == PA_BF16 && window) return launch_window<__nv_bfloat16, false, 64>(tk, tv, tq, to, p, stream);
+    return cudaErrorInvalidValue;
+  }
   if (dtype == PA_F16)
-    return window ? launch_window<__half, false>(tk, tv, tq, to, p, stream)
+    return window ? launch_window<__half, false, 128>(tk, tv, tq, to, p, stream)
                   : launch_prefill<__half, PfForm::kPlain>(tk, tv, tq, to, p, stream);
   if (dtype == PA_BF16)
-    return window ? launch_window<__nv_bfloat16, false>(tk, tv, tq, to, p, stream)
+    return window ? launch_window<__nv_bfloat16, false, 128>(tk, tv, tq, to, p, stream)
                   : launch_prefill<__nv_bfloat16, PfForm::kPlain>(tk, tv, tq, to, p, stream);
-  if (dtype == PA_FP8_E4M3 && window) return launch_window<__half, true>(tk, tv, tq, to, p, stream);
+  if (dtype == PA_FP8_E4M3 && window) return launch_window<__half, true, 128>(tk, tv, tq, to, p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -133,10 +133,8 @@ int pack_log2(int G) {
   return k;
 }
 
-// 16-bit and FP8 caches of head size 128 whose blocks fit the 128-key tiles run on the tensor-core tile kernel
-bool tile_kernel_takes(const pa_cache_desc* c) {
-  return c->dtype != PA_F32 && c->head_size == 128 && 128 % c->block_size == 0;
-}
+// 16-bit and FP8 caches whose blocks fit the 128-key tiles run on the tensor-core tile kernel
+bool tile_kernel_takes(const pa_cache_desc* c) { return c->dtype != PA_F32 && 128 % c->block_size == 0; }
 
 // CTAs that share an item's key tiles: as many as leave each SM at most one, with four tiles or more each
 int tile_split(long long items, long long max_keys) {
@@ -147,8 +145,8 @@ int tile_split(long long items, long long max_keys) {
 
 // Is a chunk faster on the tile kernel than on the rows kernel?  By what both took over 288 chunks of 1 to 17 queries
 // (1 to 32 sequences, 7 to 64 query heads on 1 to 32 kv heads, 300 and 4096 keys, bf16 and FP8):
-//  * rows: 6 us and the longer of 1 us for 23600 (FP8: 30000) keys of an eight-row group over all, and 0.85 us for
-//    each slab of 16 keys (FP8: 1.3 us for 32) of the warp with most;
+//  * rows: 6 us and the longer of 1 us for 23600 (FP8: 30000, head size 64: 35000) keys of an eight-row group over
+//    all, and 0.85 us for each slab of 16 keys (FP8: 1.3 us for 32) of the warp with most;
 //  * tiles: 8 us and, for each item that an SM gets, 3 us and 1.45 (1.85) us a key tile.
 // E.g. 32 sequences, 64 / 8 heads, 4096 keys, bf16: 2 queries each 95 us on rows and 111 on tiles, 5 queries about 230
 // and 111; 8 sequences of 5 queries: 78 and 39.
@@ -160,7 +158,8 @@ bool tiles_faster(const pa_cache_desc* cache, pa::WindowParams p, int pack) {
   const double groups = kv * ceil((double)p.max_query_len * G / 8);
   spread(cache->dtype, (long long)std::min(groups, 1e9), (long long)keys, p);
   const double slabs = ceil(keys / (fp8 ? 32.0 : 16.0) / (p.warps * p.cluster));
-  const double rows_us = 6.0 + std::max(groups * keys / (fp8 ? 30000.0 : 23600.0), slabs * (fp8 ? 1.3 : 0.85));
+  const double rate = fp8 ? 30000.0 : cache->head_size == 64 ? 35000.0 : 23600.0;
+  const double rows_us = 6.0 + std::max(groups * keys / rate, slabs * (fp8 ? 1.3 : 0.85));
   const double items = kv * ceil((double)p.max_query_len / queries) * (G >> pack), share = items / kSms;
   const double tiles = ceil(keys / 128.0) / tile_split((long long)std::min(items, 1e9), (long long)keys);
   const double tile_us = 8.0 + 0.5 * (share + ceil(share)) * (3.0 + (fp8 ? 1.85 : 1.45) * tiles);
@@ -193,6 +192,7 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   p.max_blocks = w.max_blocks;
   p.block_size = w.block_size;
   p.num_blocks = w.num_blocks;
+  p.head_size = cache->head_size;
   p.q_tiles = (int32_t)q_tiles;
   p.num_query_tokens = w.num_query_tokens;
   p.scale_log2 = w.scale_log2 * w.k_scale;

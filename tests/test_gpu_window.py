@@ -246,7 +246,8 @@ def test_prefill_window_short_chunks(dtype):
         check(s, w.reference(), f"window {window}")
 
 
-@pytest.mark.parametrize("dtype,block_size", [("bf16", 16), ("f16", 64), ("fp8", 32), ("bf16", 8)])
+@pytest.mark.parametrize("dtype,block_size,d", [("bf16", 16, 128), ("f16", 64, 128), ("fp8", 32, 128), ("bf16", 8, 128),
+                                                ("bf16", 32, 64), ("f16", 16, 64)])
 @pytest.mark.parametrize("window,sinks,lens,chunks", [
     (2500, 3, [3100, 2600, 130, 3, 900], [64, 33, 50, 3, 0]),   # four CTAs an item
     (1100, 0, [3100, 2600, 130, 3, 900], [64, 33, 50, 3, 0]),   # two
@@ -255,10 +256,10 @@ def test_prefill_window_short_chunks(dtype):
     (4300, 5, [4700, 40], [40, 40]),                            # eight
     (900, 0, [3000, 1500], [300, 150]),                         # two, more query tiles
 ])
-def test_prefill_window_few_long_items(dtype, block_size, window, sinks, lens, chunks):
+def test_prefill_window_few_long_items(dtype, block_size, d, window, sinks, lens, chunks):
     """Few items over many keys: the CTAs of a cluster share an item's key tiles and merge their rows; the short
     sequences leave some of them without a tile, a ragged chunk some rows outside it."""
-    w = WindowCase(dtype, lens, chunks, 8, 1, 128, block_size, window, sinks, seed=window % 97)
+    w = WindowCase(dtype, lens, chunks, 8, 1, d, block_size, window, sinks, seed=window % 97)
     s = Step(w)
     s.prefill()
     check(s, w.reference(), "few long items")
@@ -334,8 +335,9 @@ def test_prefill_window_many_items():
     rng = np.random.default_rng(1)
     chunks = [int(x) for x in rng.integers(1, 200, 14)]
     lens = [c + int(x) for c, x in zip(chunks, rng.integers(0, 400, 14))]
-    for dtype, hq, hkv, bs in (("bf16", 32, 8, 16), ("f16", 16, 16, 64)):
-        w = WindowCase(dtype, lens, chunks, hq, hkv, 128, bs, 150, 10, seed=2)
+    for dtype, hq, hkv, bs, d in (("bf16", 32, 8, 16, 128), ("f16", 16, 16, 64, 128), ("fp8", 32, 8, 16, 128),
+                                  ("bf16", 32, 8, 16, 64), ("f16", 16, 16, 8, 64)):
+        w = WindowCase(dtype, lens, chunks, hq, hkv, d, bs, 150, 10, seed=2)
         s = Step(w)
         s.prefill()
         check(s, w.reference(), dtype)
