@@ -143,13 +143,14 @@ int tile_split(long long items, long long max_keys) {
   return c;
 }
 
-// Is a chunk faster on the tile kernel than on the rows kernel?  By what both took over 288 chunks of 1 to 17 queries
-// (1 to 32 sequences, 7 to 64 query heads on 1 to 32 kv heads, 300 and 4096 keys, bf16 and FP8):
-//  * rows: 6 us and the longer of 1 us for 23600 (FP8: 30000, head size 64: 35000) keys of an eight-row group over
-//    all, and 0.85 us for each slab of 16 keys (FP8: 1.3 us for 32) of the warp with most;
-//  * tiles: 8 us and, for each item that an SM gets, 3 us and 1.45 (1.85) us a key tile.
-// E.g. 32 sequences, 64 / 8 heads, 4096 keys, bf16: 2 queries each 95 us on rows and 111 on tiles, 5 queries about 230
-// and 111; 8 sequences of 5 queries: 78 and 39.
+// Is a chunk faster on the tile kernel than on the rows kernel?  By an estimate of both whose constants were fitted to
+// 432 chunks of 1 to 17 queries (1 to 32 sequences, 7 to 64 query heads on 1 to 32 kv heads, 300 and 4096 keys, bf16 of
+// head size 128 and 64, FP8), on which it loses at most 12% to the faster one:
+//  * rows: 6 us and the longer of 1 us for `rate` keys of an eight-row group over all, and 0.85 us for each slab of 16
+//    keys (FP8: 1.3 us for 32) of the warp with most;
+//  * tiles: 5 us and, for each item that an SM gets, 1 us and `per_tile` a key tile.
+// E.g. 32 sequences, 64 / 8 heads, 4096 keys, bf16: 2 queries each 95 us on rows and 104 on tiles, 5 queries 204 and
+// 104; 8 sequences of 5 queries: 70 and 35; one of 3 with 300 keys: 7 and 10.5.
 bool tiles_faster(const pa_cache_desc* cache, pa::WindowParams p, int pack) {
   const bool fp8 = cache->dtype == PA_FP8_E4M3;
   const int G = p.num_q_heads / p.num_kv_heads, queries = 128 >> pack;
@@ -158,11 +159,12 @@ bool tiles_faster(const pa_cache_desc* cache, pa::WindowParams p, int pack) {
   const double groups = kv * ceil((double)p.max_query_len * G / 8);
   spread(cache->dtype, (long long)std::min(groups, 1e9), (long long)keys, p);
   const double slabs = ceil(keys / (fp8 ? 32.0 : 16.0) / (p.warps * p.cluster));
-  const double rate = fp8 ? 30000.0 : cache->head_size == 64 ? 35000.0 : 23600.0;
+  const bool narrow = cache->head_size == 64;
+  const double rate = fp8 ? 35000.0 : narrow ? 26000.0 : 30000.0, per_tile = fp8 || narrow ? 1.6 : 1.3;
   const double rows_us = 6.0 + std::max(groups * keys / rate, slabs * (fp8 ? 1.3 : 0.85));
   const double items = kv * ceil((double)p.max_query_len / queries) * (G >> pack), share = items / kSms;
   const double tiles = ceil(keys / 128.0) / tile_split((long long)std::min(items, 1e9), (long long)keys);
-  const double tile_us = 8.0 + 0.5 * (share + ceil(share)) * (3.0 + (fp8 ? 1.85 : 1.45) * tiles);
+  const double tile_us = 5.0 + std::max(1.0, 0.5 * (share + ceil(share))) * (1.0 + per_tile * tiles);
   return tile_us < rows_us;
 }
 
