@@ -353,6 +353,9 @@ def _caches(k_cache, v_cache, desc, where: str):
         if len(shape) != 4:
             raise ValueError("cache must be [num_blocks, num_kv_heads, block_size, head_size]")
         desc = pa_cache_desc(shape[0], shape[2], shape[1], shape[3], code)
+    elif (desc.dtype != code or
+          desc.num_blocks * desc.block_size * desc.num_kv_heads * desc.head_size != k_cache.numel()):
+        raise ValueError(f"{where}: desc does not describe the caches")
     return dev, desc, rows
 
 

@@ -318,6 +318,21 @@ def test_prefill_window_rows_and_bad_chunks(dtype):
         assert ok, err
 
 
+def test_prefill_window_c_call_with_a_loose_bound(pa):
+    """max_query_len may be any bound: the C call takes the largest int32."""
+    import ctypes
+    import torch
+    w = WindowCase("bf16", [300, 200, 90], [140, 60, 7], 24, 2, 128, 16, 100, 4, seed=9)
+    s = Step(w)
+    desc = pa.cache_desc(s.k)
+    status = pa.lib().pa_prefill_window(
+        s.out.data_ptr(), s.q.data_ptr(), s.k.data_ptr(), s.v.data_ptr(), s.table.data_ptr(), s.lens.data_ptr(),
+        s.start.data_ptr(), 3, s.q.shape[0], 24, s.table.shape[1], 2 ** 31 - 1, ctypes.byref(desc), w.scale, w.window,
+        w.sinks, 0.0, 0.0, s.err.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    check(s, w.reference(), "loose bound")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 def test_prefill_window_bad_block(dtype):
     w = WindowCase(dtype, [300, 200], [140, 60], 8, 2, 128, 16, 100, 4, seed=9)
@@ -459,6 +474,15 @@ def test_window_calls_refuse_wrong_tensors(pa):
         decode(alibi_slopes=torch.zeros(3, device="cuda"))
     with pytest.raises(pa.PaError):
         pa.pa_decode_window(**good, scale=0.1, window=0)
+    # a descriptor of another pool: more blocks than there are, another type
+    right = pa.cache_desc(s.k)
+    for field, value in (("num_blocks", right.num_blocks + 1), ("head_size", 64), ("dtype", pa.PA_F16)):
+        desc = pa.cache_desc(s.k)
+        setattr(desc, field, value)
+        for call in (decode, prefill):
+            with pytest.raises(ValueError):
+                call(desc=desc)
+    decode(desc=right)
     torch.cuda.synchronize()
 
 
