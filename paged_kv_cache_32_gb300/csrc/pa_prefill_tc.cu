@@ -511,32 +511,36 @@ __device__ __forceinline__ bool block_whole(const PfWindowItem& it, int pos, int
   return pos >= it.lo_chunk || pos + w <= it.s_chunk;
 }
 
-// 16 codes, or zeros; volatile, so that the load stays where it is issued, a tile before its use (as an ordinary
-// load it was moved down to it, and every tile waited for its 16 loads one after the other)
+// the 16 codes at src + OFF, or zeros; volatile, so that the load stays where it is issued, a tile before its use (as
+// an ordinary load it was moved down to it, and every tile waited for its 16 loads one after the other)
+template <int OFF>
 __device__ __forceinline__ uint4 load_codes(const uint8_t* src, bool take) {
   uint4 v;
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
       "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4 + %6];\n\t}"
       : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(src), "r"((int)take));
+      : "l"(src), "r"((int)take), "n"(OFF));
   return v;
 }
 
 // A producer warp over an FP8 cache: of every tile, warps 0..3 take the keys 32 w .. 32 w + 31 of K (a lane 16 of a
 // row's 128 codes), warps 4..7 the same keys of V (a lane the 16 tokens of a group at one dimension).  A warp alone
-// on its scheduler takes some six cycles an instruction, hence eight warps; a group's loads for the next tile are issued when its present codes are stored.
-// `bar` counts the filled stages, `freed` the MMAs that have read a tile (one phase per tile held by an S buffer).
+// on its scheduler takes some six cycles an instruction, hence eight warps and few instructions a vector; a group's
+// loads for the next tile are issued when its present codes are stored.  `bar` counts the filled stages, `freed` the
+// MMAs that have read a tile (one phase per tile held by an S buffer).
 constexpr int kFp8Producers = 8;
 constexpr int kFp8LoadWarp0 = kSoftmaxWarps + 4;  // (whole warpgroups share a register limit: two warps idle)
 constexpr int kFp8Threads = (kFp8LoadWarp0 + kFp8Producers) * 32;
 // Registers: 20 warps are launched with 96 a thread (five warps a scheduler); the softmax warps, which hold a row's
-// 64 scores, take what the producers give back.  16 chunks of 256-1024 tokens, W = 1024: 329 us with 120 / 72
-// registers for softmax / producers, 397 with 112 / 80, 461 with 128 / 64 (the producers spill), 512 with 96 for
-// all, 804 with four producer warps at 128.
-constexpr int kFp8LaunchRegs = 96, kFp8SoftmaxRegs = 120, kFp8LoadRegs = 72;
-static_assert(8 * 32 * kFp8SoftmaxRegs + 4 * 32 * kFp8LaunchRegs + kFp8Producers * 32 * kFp8LoadRegs <=
+// 64 scores, take what the producers and the issuers give back.  16 chunks of 256-1024 tokens, W = 1024, 32 / 8 heads:
+// 254 us with 128 / 80 / 64 registers for softmax / producers / issuers, 280 with 120 / 88 / 64, 325 with 128 / 72 / 72
+// and 422 with 144 / 72 / 40 (the producers spill); 16 producer warps: 271 with 128 / 48 / 56 of 72.  The limits are
+// not raised again at the roles' ends: a producer that finished before the softmax warps had started would take the
+// registers that they wait for.
+constexpr int kFp8LaunchRegs = 96, kFp8SoftmaxRegs = 128, kFp8LoadRegs = 80, kFp8IssueRegs = 64;
+static_assert(8 * 32 * kFp8SoftmaxRegs + 4 * 32 * kFp8IssueRegs + kFp8Producers * 32 * kFp8LoadRegs <=
                   kFp8Threads * kFp8LaunchRegs,
               "a raised limit waits for registers that the launch does not have");
 template <int N>
@@ -547,15 +551,26 @@ template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-template <typename Item>
-__device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, int lane, int idx0, int idx_step,
+template <typename Item, bool kV>
+__device__ __forceinline__ void fp8_producer(const PrefillParams& p, int w, int lane, int idx0, int idx_step,
                                              int n_items, uint8_t* ring, uint64_t* bar, uint64_t* freed,
                                              volatile int* abort_flag) {
-  constexpr int kPastEnd = INT_MIN, kLoads = 8;  // loads of a lane and tile: two groups of 16 keys x 4
-  const bool is_v = role >= kFp8Producers / 2;
-  const int w = role & 3, B = p.block_size, log2_b = __ffs(B) - 1, blocks_per_tile = kTile / B;
-  // this lane's place in a group: K: row 4 i + lane / 8, codes 16 (lane % 8) ..; V: dimension 32 i + lane
-  const uint8_t* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + lane * 16;
+  constexpr int kPastEnd = INT_MIN, kGroups = 16 / kFp8Producers;  // groups of 16 keys of a warp and tile
+  const int B = p.block_size, log2_b = __ffs(B) - 1, blocks_per_tile = kTile / B;
+  // This lane's places in a group, four vectors i of 16 codes.  V: dimension 32 i + lane, the group's tokens.  K: row
+  // 4 i + row, codes 64 half + 16 c ..: eight lanes whose stores go together hold two neighbouring rows of one half,
+  // which the swizzle puts into different banks.
+  const int c = lane & 3, half = (lane >> 3) & 1, row = ((lane >> 2) & 1) + 2 * (lane >> 4);
+  const uint8_t* cache =
+      static_cast<const uint8_t*>(kV ? p.v_cache : p.k_cache) + (kV ? lane * 16 : row * kFp8D + half * 64 + c * 16);
+  // where its two 16-byte halves go in the tile: at `at` and `at ^ 16` (K: odd i at ^ 64, 4 rows on)
+  int at[kGroups];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const int group = kGroups * w + g;
+    at[g] = kV ? (group >> 2) * kHalf + (int)swz128(lane, 2 * (group & 3))
+               : half * kHalf + (int)swz128(16 * group + row, 2 * c);
+  }
   int tg = 0;
   bool ok = true;
   for (int idx = idx0; ok && idx < n_items; idx += idx_step) {
@@ -569,24 +584,26 @@ __device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, i
                  ? __ldg(table + bi)
                  : kPastEnd;
     };
-    uint4 raw[kLoads];
+    uint4 raw[4 * kGroups];
     // the table entries of a tile, -1 outside the pool
     auto checked = [&](int entry) {
       const bool in_pool = entry >= 0 && entry < p.num_blocks;
-      if (role == 0 && entry != kPastEnd && !in_pool) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+      if (!kV && w == 0 && entry != kPastEnd && !in_pool) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
       return in_pool ? entry : -1;
     };
     auto load = [&](int entry, int g) {
-      const int key0 = 32 * w + 16 * g;  // the group lies in one block
+      const int key0 = 16 * (kGroups * w + g);  // the group lies in one block
       const int e = __shfl_sync(0xffffffffu, entry, key0 >> log2_b);
       // 16 tokens of one head: 2 KB side by side, rows of K or [D][16] of V
       const uint8_t* src = cache + (((size_t)(e * p.num_kv_heads + it.hkv) << log2_b) + (key0 & (B - 1))) * kFp8D;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) raw[4 * g + i] = load_codes(src + 512 * i, e >= 0);
+      raw[4 * g] = load_codes<0>(src, e >= 0);
+      raw[4 * g + 1] = load_codes<512>(src, e >= 0);
+      raw[4 * g + 2] = load_codes<1024>(src, e >= 0);
+      raw[4 * g + 3] = load_codes<1536>(src, e >= 0);
     };
     const int first = checked(fetch(0));
-    load(first, 0);
-    load(first, 1);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) load(first, g);
     int entry = fetch(1);
     for (int t = 0; t < it.key_tiles; ++t, ++tg) {
       const int ahead = checked(entry);  // of the next tile
@@ -595,40 +612,35 @@ __device__ __forceinline__ void fp8_producer(const PrefillParams& p, int role, i
       if (!ok) break;
       uint8_t* st = ring + (tg & 1) * 2 * kHalf;
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-        if (is_v) {
+      for (int g = 0; g < kGroups; ++g) {
+        if constexpr (kV) {
           // values of tokens that no query of the chunk sees may be NaN codes: zeros
-          const int pos = key_pos(it, (first_tile(it) + t) * kTile + 32 * w + 16 * g);
+          const int pos = key_pos(it, (first_tile(it) + t) * kTile + 16 * (kGroups * w + g));
           if (!(pos + 16 <= it.L && block_whole(it, pos, 16))) {
             const int mine = pos + (lane & 15);
             const unsigned some = __ballot_sync(0xffffffffu, mine < it.L && block_seen(it, mine, 1));
             // a word's four tokens: bit b of the nibble -> byte b
+            uint32_t keep[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) keep[i] = ((((some >> (4 * i)) & 15u) * 0x00204081u) & 0x01010101u) * 0xffu;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4& x = raw[4 * g + i];
+              x.x &= keep[0], x.y &= keep[1], x.z &= keep[2], x.w &= keep[3];
+            }
           }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 c = raw[4 * g + i];
+          const uint4 x = raw[4 * g + i];
           uint4 a, b;
-          codes_to_half(c.x & keep[0], a.x, a.y);
-          codes_to_half(c.y & keep[1], a.z, a.w);
-          codes_to_half(c.z & keep[2], b.x, b.y);
-          codes_to_half(c.w & keep[3], b.z, b.w);
-          if (is_v) {
-            // V^T: row = dimension, 64 keys a half
-            uint8_t* half = st + (w >> 1) * kHalf;
-            const int chunk = 4 * (w & 1) + 2 * g;
-            *reinterpret_cast<uint4*>(half + swz128(32 * i + lane, chunk)) = a;
-            *reinterpret_cast<uint4*>(half + swz128(32 * i + lane, chunk + 1)) = b;
-          } else {
-            // the upper four lanes of a row, whose chunks fall into the banks of the lower four, swap their stores
-            const int r = 32 * w + 16 * g + 4 * i + (lane >> 3), up = (lane >> 2) & 1, chunk = 2 * (lane & 3);
-            uint8_t* half = st + up * kHalf;
-            *reinterpret_cast<uint4*>(half + swz128(r, chunk + up)) = up ? b : a;
-            *reinterpret_cast<uint4*>(half + swz128(r, chunk + 1 - up)) = up ? a : b;
-          }
+          codes_to_half(x.x, a.x, a.y);
+          codes_to_half(x.y, a.z, a.w);
+          codes_to_half(x.z, b.x, b.y);
+          codes_to_half(x.w, b.z, b.w);
+          const int to = kV ? at[g] : at[g] ^ ((i & 1) * 64), step = kV ? 32 * 128 * i : 4 * 128 * i;
+          *reinterpret_cast<uint4*>(st + to + step) = a;
+          *reinterpret_cast<uint4*>(st + (to ^ 16) + step) = b;
         }
         if (t + 1 < it.key_tiles) load(ahead, g);
       }
@@ -763,13 +775,16 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
   };
 
-  if (kFp8 && warp >= kSoftmaxWarps + 2) {
+  if (kFp8 && warp >= kFp8LoadWarp0) {
     // =================================================================== producers over an FP8 cache
-    if (warp >= kFp8LoadWarp0) {
+    if constexpr (kFp8) {
       regs_dec<kFp8LoadRegs>();
-      const bool v = warp >= kFp8LoadWarp0 + kFp8Producers / 2;
-      fp8_producer<Item>(p, warp - kFp8LoadWarp0, lane, idx0, idx_step, n_items, smem + (v ? kVOff : kKOff),
-                         v ? bar_v : bar_k, v ? bar_o : bar_s, abort_flag);
+      const int w = warp - kFp8LoadWarp0;
+      if (w < kFp8Producers / 2)
+        fp8_producer<Item, false>(p, w, lane, idx0, idx_step, n_items, smem + kKOff, bar_k, bar_s, abort_flag);
+      else
+        fp8_producer<Item, true>(p, w - kFp8Producers / 2, lane, idx0, idx_step, n_items, smem + kVOff, bar_v, bar_o,
+                                 abort_flag);
     }
   } else if (!kFp8 && warp >= kLoadWarp0) {
     // =================================================================== producers: one half of K or V tiles
@@ -851,9 +866,10 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         ++n_issued;
       }
     }
-  } else if (warp == kSWarp) {
-    // =================================================================== S = Q K^T issuer
-    if (lane == 0) {
+  } else if (warp >= kSoftmaxWarps) {
+    if constexpr (kFp8) regs_dec<kFp8IssueRegs>();
+    if (warp == kSWarp && lane == 0) {
+      // ================================================================= S = Q K^T issuer
       const uint32_t id_s = idesc<T>(0, kTile);
       tma_prefetch_descriptor(&tmap_q);
       // This thread also schedules: it publishes item k (the first one with queries at or after index
@@ -923,10 +939,8 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         it = nx;
       }
     }
-    __syncwarp();
-  } else if (warp == kPVWarp) {
-    // =================================================================== O += P V issuer
-    if (lane == 0) {
+    if (warp == kPVWarp && lane == 0) {
+      // ================================================================= O += P V issuer
       const uint32_t id_o = idesc<T>(kFp8 ? 0 : 1, D);  // FP8 caches: V^T, rows of 64 keys
       bool ok = true;
       int tg = 0, item_no = 0;
