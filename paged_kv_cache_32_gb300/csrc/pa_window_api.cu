@@ -160,7 +160,7 @@ bool tiles_faster(const pa_cache_desc* cache, pa::WindowParams p, int pack) {
   spread(cache->dtype, (long long)std::min(groups, 1e9), (long long)keys, p);
   const double slabs = ceil(keys / (fp8 ? 32.0 : 16.0) / (p.warps * p.cluster));
   const bool narrow = cache->head_size == 64;
-  const double rate = fp8 ? 35000.0 : narrow ? 26000.0 : 30000.0, per_tile = fp8 || narrow ? 1.6 : 1.3;
+  const double rate = fp8 ? 35000.0 : narrow ? 26000.0 : 30000.0, per_tile = narrow ? 1.6 : 1.3;
   const double rows_us = 6.0 + std::max(groups * keys / rate, slabs * (fp8 ? 1.3 : 0.85));
   const double items = kv * ceil((double)p.max_query_len / queries) * (G >> pack), share = items / kSms;
   const double tiles = ceil(keys / 128.0) / tile_split((long long)std::min(items, 1e9), (long long)keys);
@@ -304,7 +304,7 @@ int pa_prefill_window(void* out, const void* q, const void* k_cache, const void*
   p.v_scale = v_scale;
   p.query_start = query_start;
   p.num_query_tokens = num_query_tokens;
-  p.max_query_len = max_query_len;
+  p.max_query_len = std::min(max_query_len, num_query_tokens);  // no valid chunk is longer
   const int pack = pack_log2(num_q_heads / cache->num_kv_heads);
   if (tile_kernel_takes(cache) && tiles_faster(cache, p, pack))
     return launch_tiles(cache, p, pack, static_cast<cudaStream_t>(stream));
