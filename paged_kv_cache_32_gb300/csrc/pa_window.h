@@ -35,6 +35,14 @@ struct WindowParams {
   void* v_cache_out;
 };
 
+// What a rows kernel needs before its launch: its shared memory, and clusters beyond the portable eight CTAs.
+template <typename Kernel>
+cudaError_t prepare_rows(Kernel kernel, size_t smem, int cluster) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
+}
+
 // items of a rows launch: eight query rows of one kv head each
 inline long long window_items(const WindowParams& p) { return (long long)p.num_seqs * p.num_kv_heads * p.tiles; }
 

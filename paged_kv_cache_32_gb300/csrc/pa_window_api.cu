@@ -17,27 +17,32 @@ using namespace pa::host;
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kMaxCluster = 8;     // the portable cluster size
+constexpr int kMaxCluster = 8;     // the portable cluster size (rows kernels also take the largest, twice that)
 constexpr int kMinCtaTokens = 64;  // tokens of a CTA below which a split no longer pays
 
 // How the rows kernels spread over the SMs.  A warp holds 16 KB of slabs, so an SM takes 4 CTAs of 3 warps, 3 of 4
 // or 2 of 6.
 //  * Few items (at most half the SMs): CTAs of 6 warps, an item's keys split over a cluster until the CTAs fill the
 //    SMs twice.  One sequence, 8 kv heads, 4096 keys: 10.8 us (clusters of 4: 15.4; 4 warps: 12.4); 64 items of
-//    4096 keys: 27.1 us (4 warps: 29.4; clusters of 2: 29.2).
+//    4096 keys: 27.1 us (4 warps: 29.4; clusters of 2: 29.2).  Clusters of 16 where each CTA has an SM of its own
+//    and 256 keys: those 4096 keys 10.2 us, 16384 keys 25.2 -> 17.7 (1024 keys 7.0 -> 7.7; 16 such items, whose
+//    clusters do not all find room at once, 12.2 -> 18.4).
 //  * More: no split (a cluster waits for as many free places at once: two of 4 warps cost 94 -> 109 us on 1024
 //    items of 1024 keys), and the CTA size whose last round is fullest, the smallest among equals.  1024 keys:
 //    256 items 26.6 / 27.9 / 28.7 us with 6 / 4 / 3 warps, 384 items 42.8 / 37.4 / 38.7, 512 items 48.6 / 58.0 /
 //    48.3, 768 items 69.9 / 67.8 / 74.5, 1024 items 92.2 / 93.4 / 87.9.
 //    (Splitting long items in two all the same evens out a last round of unequal contexts, 96 FP8 sequences of
 //    2500 to 40000 tokens with a window of 8192: 240 -> 226 us, and costs as much when they are equal, 246 -> 264.)
-//  * fp32 (CUDA cores): four warps a CTA, three CTAs an SM, split while that many are not there.
+//  * fp32 (CUDA cores): four warps a CTA, three CTAs an SM, split while that many are not there, in clusters of 16
+//    up to two an SM (8 kv heads, 1024 / 4096 keys: 18.7 -> 15.0 and 45.2 -> 29.8 us; 16 items 20.0 -> 17.0 and
+//    52.3 -> 37.2).
 void spread(int32_t dtype, long long items, long long max_keys, pa::WindowParams& p) {
   p.cluster = 1;
   if (dtype == PA_F32) {
     p.warps = 4;
     while (p.cluster < kMaxCluster && items * p.cluster * 2 <= 3 * kSms && max_keys / (2 * p.cluster) >= kMinCtaTokens)
       p.cluster *= 2;
+    if (items * 2 * kMaxCluster <= 2 * kSms && max_keys / (2 * kMaxCluster) >= kMinCtaTokens) p.cluster = 2 * kMaxCluster;
     return;
   }
   if (items <= kSms / 2) {
@@ -45,6 +50,8 @@ void spread(int32_t dtype, long long items, long long max_keys, pa::WindowParams
     while (p.cluster < kMaxCluster && items * p.cluster * 2 <= 2 * kSms &&
            max_keys / (2 * p.cluster) >= kMinCtaTokens)
       p.cluster *= 2;
+    if (items * 2 * kMaxCluster <= kSms && max_keys / (2 * kMaxCluster) >= 4 * kMinCtaTokens)
+      p.cluster = 2 * kMaxCluster;
     return;
   }
   double best = 0.0;

@@ -208,7 +208,7 @@ template <int D>
 cudaError_t launch_f32(const WindowParams& p, cudaStream_t stream) {
   auto kernel = window_rows_f32_kernel<D>;
   constexpr size_t kSmem = (size_t)kF32Warps * kRing * 8 * D * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  cudaError_t e = prepare_rows(kernel, kSmem, p.cluster);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(kF32Warps * 32), kSmem, p.cluster,
                         true, stream, p);

@@ -129,6 +129,18 @@ def test_decode_window_many_sequences(dtype):
         check(s, w.reference(), f"{n} sequences")
 
 
+@pytest.mark.parametrize("dtype,hkv,append", [("f32", 2, False), ("f16", 1, True), ("bf16", 8, False), ("bf16", 4, True),
+                                              ("fp8", 8, True), ("fp8", 2, False)])
+def test_decode_window_few_long_sequences(dtype, hkv, append):
+    """One sequence over thousands of keys: an item's keys go to the largest clusters."""
+    for lens, window in (([9001], 4200), ([6000], BIG), ([4100], 4096)):
+        w = WindowCase(dtype, lens, [1], hkv * 5, hkv, 128, 16, window, 3, seed=29, append=append)
+        s = Step(w)
+        ref = w.reference()
+        s.decode()
+        check(s, ref, f"{dtype} {lens} window {window}")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
 def test_decode_window_alibi(dtype):
     import torch
