@@ -28,7 +28,7 @@
  *    every cudaHostAlloc / cudaMallocHost allocation is under unified
  *    addressing: the kernels then read and write them in place over the host
  *    link (NVLink-C2C on GB300), with no copy in between, and the results are
- *    the same bytes as with device buffers.  pa_prefill moves q and out by
+ *    the same bytes as with device buffers.  pa_prefill and pa_prefill_window move q and out by
  *    tensor-map copies: those two must be device memory there.
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *    Every call is asynchronous on that stream.
