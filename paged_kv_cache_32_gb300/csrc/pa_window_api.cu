@@ -30,7 +30,10 @@ constexpr int kMinCtaTokens = 64;  // tokens of a CTA below which a split no lon
 //  * More: no split (a cluster waits for as many free places at once: two of 4 warps cost 94 -> 109 us on 1024
 //    items of 1024 keys), and the CTA size whose last round is fullest, the smallest among equals.  1024 keys:
 //    256 items 26.6 / 27.9 / 28.7 us with 6 / 4 / 3 warps, 384 items 42.8 / 37.4 / 38.7, 512 items 48.6 / 58.0 /
-//    48.3, 768 items 69.9 / 67.8 / 74.5, 1024 items 92.2 / 93.4 / 87.9.
+//    48.3, 768 items 69.9 / 67.8 / 74.5, 1024 items 92.2 / 93.4 / 87.9.  Six warps hold few slabs each of short items
+//    (2048 FP8 items of 512 / 1024 keys: 71.5 / 109 us, with four 66 / 103), so not for many of those; of long ones,
+//    whose lengths are seldom equal, they also win ties (96 sequences, 8 kv heads, W = 8192, contexts of up to 20000
+//    tokens: bf16 351 -> 326 us, FP8 220 -> 204; equal lengths within 1%, but for 512 FP8 items of 4096, 89 -> 94).
 //    (Splitting long items in two all the same evens out a last round of unequal contexts, 96 FP8 sequences of
 //    2500 to 40000 tokens with a window of 8192: 240 -> 226 us, and costs as much when they are equal, 246 -> 264.)
 //  * fp32 (CUDA cores): four warps a CTA, three CTAs an SM, split while that many are not there, in clusters of 16
@@ -58,7 +61,8 @@ void spread(int32_t dtype, long long items, long long max_keys, pa::WindowParams
   for (int warps : {3, 4, 6}) {
     const double rounds = (double)items / (kSms * (12 / warps));
     const double full = rounds / ceil(rounds);
-    if (full > best + 1e-9) {
+    if (warps == 6 && max_keys < 1536 && items > 4 * kSms) break;
+    if (full > best + (warps == 6 && max_keys >= 4096 ? -1e-9 : 1e-9)) {
       best = full;
       p.warps = warps;
     }
