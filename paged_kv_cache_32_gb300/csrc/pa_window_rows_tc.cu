@@ -3,9 +3,11 @@
 // take (see pa_window_rows.cuh for the rows, the visible slabs and the split).
 //
 // Bound by HBM bandwidth: each visible token costs 2 D elements and 4 D flops a
-// row.  A CTA of four warps streams 16-token slabs of K and V; every warp fills
-// its own ring of NS slab buffers with tensor-map copies and drains it in
-// order, so that an SM with three CTAs has up to 24 slabs (192 KB) in flight.
+// row.  A CTA of three, four or six warps streams 16-token slabs of K and V; every
+// warp fills its own ring of NS slab buffers with tensor-map copies and drains it
+// in order, so that an SM's twelve warps have up to 24 slabs (192 KB) in flight.
+// 128 sequences, 64 / 8 heads of 128, bf16, the last 1024 of up to 16384 tokens:
+// 88 us, 6.2 TB/s.
 // A slab takes two mma.m16n8k16 contractions, S^T[16 tokens x 8 rows] = K Q^T
 // and O^T[D x 8 rows] += V^T P^T, fp32 accumulation and an online softmax.  The
 // weights enter the second one as two 16-bit terms (rounded part and residual:
