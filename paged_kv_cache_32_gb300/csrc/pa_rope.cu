@@ -15,10 +15,11 @@
 // Bound by HBM bandwidth: 4 + (cache / element) bytes moved an element.  Work is
 // cut into units of two vectors of V elements (elements V u .. of both halves of
 // the pairs, or 2 V neighbouring elements), D / 2 V units a head whatever r is.
-// A CTA walks groups of tokens (or a part of each, when a token has more units
-// than its threads hold); a thread has the same units of every group, so their
-// heads, elements and offsets are worked out once, and the next group's loads
-// are issued as soon as the present one is stored.  Two more warps, a thread
+// A CTA walks groups of tokens, or a part of each (where a token has more units
+// than its threads hold, or several tokens cut into parts fill them better); a
+// thread has the same units of every group, so their heads, elements and offsets
+// are worked out once, and the next group's loads are issued as soon as the
+// present one is stored.  Two more warps, a thread
 // per pair, work out the next group's slots and angles meanwhile (their chain of
 // a load, a 64-bit division and a sine is longer than a group's stores).  (c, s)
 // lie in shared memory so that the units of a head read neighbouring banks: by
@@ -29,10 +30,12 @@
 // their own (the grid's first CTAs) take up to 16 tokens of one head, quantise
 // them into shared memory and write each run of slots that follow one another
 // inside a 16-token group with as few stores as its length allows, 16 bytes for
-// a whole group (9001 tokens: single bytes from the units 118 us, these 81).
+// a whole group (9001 tokens, 64 / 8 heads: single bytes from the units 118 us, these 74).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "pa.h"
 #include "pa_device.cuh"
@@ -43,14 +46,15 @@ namespace {
 
 // Threads with units (two warps more for the angles), CTAs of an SM, units of a thread.  Measured on a prompt of
 // 9001 tokens, 64 / 8 heads of 128, bf16 (halves), and of 24576, 32 / 32 heads, fp16 (neighbours): 60 and 183 us
-// (6.1 and 6.6 TB/s); 256 x 2 x 4: 85 and 318, 256 x 3 x 2: 78 and 248, 256 x 4 x 2: 101 and 329, 384 x 3 x 2: 95
+// (6.1 and 6.6 TB/s; 57 and 182 with groups in parts); 256 x 2 x 4: 85 and 318, 256 x 3 x 2: 78 and 248, 256 x 4 x 2: 101 and 329, 384 x 3 x 2: 95
 // and 311, 768 x 1 x 1: 72 and 217 us.  More rows at once than these 304 tokens lose more in DRAM than the
 // loads in flight gain; issuing a unit's next load right after its stores, between its neighbours', made a
 // warp's waits cover loads just issued (71 and 216 us).
 constexpr int kRopeThreads = 384;
 constexpr int kRopeResident = 2;
 // narrow vectors, for halves that no 16 bytes divide: more units a thread (the 9001 tokens with 36 and 34 turned
-// elements: 95 and 167 us; with two units 136 and 208, with eight, which spill, 145 and 332)
+// elements: 85 and 150 us; before a token's parts were evened out 95 and 167, then with two units 136 and 208, with
+// eight, which spill, 145 and 332)
 template <typename T, int V>
 constexpr int kUnits = sizeof(T) * V >= 16 ? 2 : 4;
 
@@ -117,7 +121,7 @@ constexpr int kRopeWarps = (kRopeThreads + kMaxHalf) / 32;
 constexpr int kMaxGroup = 16; // tokens of a group
 
 // How the units are dealt out: groups of `tokens` tokens, each cut into `parts` parts of `part_units` units (a
-// multiple of the units of a head; parts > 1 only for groups of one token).  The CTAs of a part walk its groups.
+// multiple of the units of a head).  The CTAs of a part walk its groups.
 struct RopePlan {
   int tokens, parts, part_units, groups;
   int log2_per_head;  // units of a head
@@ -125,25 +129,29 @@ struct RopePlan {
   int value_tokens;
 };
 
-// One warp: values of kv head `head` of the tokens t0 .. t0 + n - 1 (n <= 16) into an FP8 cache, through `codes`
-// (n rows of kCodeRow bytes).
+// One warp: values of kv head `head` into an FP8 cache, through `codes` (kValueTokens rows of kCodeRow bytes): the runs
+// of slots, inside one 16-token group each, that start with one of the tokens t0 .. t0 + n - 1 (n <= 16; a run that
+// started earlier belongs to the warp of its start, one that goes on past them to this one).  So every group that a
+// prompt fills is written with 16-byte stores, wherever it starts in the batch.
 constexpr int kValueTokens = 16;
 constexpr int kCodeRow = 128 + 8;  // a token's codes, padded
 __device__ __forceinline__ void fp8_values(const RopeParams& p, int t0, int n, int head, uint8_t* codes) {
   constexpr int D = 128;  // of every FP8 cache
   const int lane = threadIdx.x & 31;
-  const __half* src = static_cast<const __half*>(p.value) + (long long)t0 * p.value_stride + (size_t)head * D;
-  long long slot = lane < n ? p.slot_mapping[t0 + lane] : -1;
+  const bool real = t0 + lane < p.num_tokens;
+  // the tokens' rows (256 bytes each) are on their way while the slots are looked at
+  if (lane < 2 * n)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __half*>(p.value) +
+                                                  (long long)(t0 + lane / 2) * p.value_stride + (size_t)head * D + lane % 2 * 64));
+  long long slot = real ? p.slot_mapping[t0 + lane] : -1;
+  long long before = lane == 0 && t0 > 0 ? p.slot_mapping[t0 - 1] : -1;
+  // the tokens outside the pool end a run like padding
   if (slot >= (long long)p.num_blocks * p.block_size) {
-    if (head == 0) report_error(p.err_flag, PA_DEVERR_SLOT);
+    if (head == 0 && lane < n) report_error(p.err_flag, PA_DEVERR_SLOT);
     slot = -1;
   }
-  Vec<__half, 8> x[kValueTokens / 2];  // lane: dimensions 8 (lane % 16) .. of the tokens lane / 16 + 2 i
-#pragma unroll
-  for (int i = 0; i < kValueTokens / 2; ++i) {
-    const int t = (lane >> 4) + 2 * i;
-    if (t < n) x[i] = *reinterpret_cast<const Vec<__half, 8>*>(src + (long long)t * p.value_stride + 8 * (lane & 15));
-  }
+  const long long left = __shfl_up_sync(0xffffffffu, slot, 1);
+  if (lane > 0) before = left;
   // where a lane's token goes, and whether it starts a run
   long long at = 0;
   int off = 0;
@@ -152,51 +160,66 @@ __device__ __forceinline__ void fp8_values(const RopeParams& p, int t0, int n, i
     off = (int)(slot - block * p.block_size);
     at = ((block * p.num_kv_heads + head) * p.block_size + off / 16 * 16) * D + off % 16;
   }
-  const long long before = __shfl_up_sync(0xffffffffu, slot, 1);
-  const bool start = lane == 0 || slot < 0 || slot != before + 1 || off % 16 == 0;
-  unsigned starts = __ballot_sync(0xffffffffu, start || lane >= n);
+  const unsigned all_starts =
+      __ballot_sync(0xffffffffu, !real || slot < 0 || slot != before + 1 || off % 16 == 0);
   const unsigned live = __ballot_sync(0xffffffffu, slot >= 0);
+  const unsigned mine = all_starts & live & (0xffffffffu >> (32 - n));
+  if (mine == 0) return;
+  // (a run has at most 16 tokens, so the next start after the n tokens is among the 32)
+  const int first = __ffs(mine) - 1, last = __ffs(all_starts & (0xffffffffu << n)) - 1;
+  for (int base = first; base < last; base += kValueTokens) {
+    const int end = min(last, base + kValueTokens);
+    Vec<__half, 8> x[kValueTokens / 2];  // lane: dimensions 8 (lane % 16) .. of the tokens base + lane / 16 + 2 i
+    const __half* src =
+        static_cast<const __half*>(p.value) + (long long)(t0 + base) * p.value_stride + (size_t)head * D + 8 * (lane & 15);
 #pragma unroll
-  for (int i = 0; i < kValueTokens / 2; ++i) {
-    const int t = (lane >> 4) + 2 * i;
-    if (t < n) {
-      float f[8];
-      x[i].get(f);
-      *reinterpret_cast<Vec<uint8_t, 8>*>(codes + t * kCodeRow + 8 * (lane & 15)) = codes_of(f, p.v_scale);
+    for (int i = 0; i < kValueTokens / 2; ++i) {
+      const int t = (lane >> 4) + 2 * i;
+      if (base + t < end) x[i] = *reinterpret_cast<const Vec<__half, 8>*>(src + (long long)t * p.value_stride);
     }
-  }
-  __syncwarp();
-  for (int a = 0; a < n;) {
-    starts &= starts - 1;  // (bit a, the lowest left, is this run's start)
-    const int next = starts ? min(n, __ffs(starts) - 1) : n, len = next - a;
-    const long long to = __shfl_sync(0xffffffffu, at, a);
-    const int o = __shfl_sync(0xffffffffu, off, a) % 16;
-    if ((live >> a) & 1u) {
+    __syncwarp();  // the codes of the tokens before have been read
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const int d = 32 * j + lane;
-        const uint8_t* from = codes + a * kCodeRow + d;
-        uint8_t* dst = static_cast<uint8_t*>(p.v_cache) + to + d * 16;
-        auto word = [&](int i) {
-          return from[i * kCodeRow] | from[(i + 1) * kCodeRow] << 8 | from[(i + 2) * kCodeRow] << 16 |
-                 (uint32_t)from[(i + 3) * kCodeRow] << 24;
-        };
-        if (len == 16) {
-          *reinterpret_cast<uint4*>(dst) = make_uint4(word(0), word(4), word(8), word(12));
-        } else {
-          for (int i = 0; i < len;) {
-            if ((o + i) % 4 == 0 && len - i >= 4) {
-              *reinterpret_cast<uint32_t*>(dst + i) = word(i);
-              i += 4;
-            } else {
-              dst[i] = from[i * kCodeRow];
-              ++i;
+    for (int i = 0; i < kValueTokens / 2; ++i) {
+      const int t = (lane >> 4) + 2 * i;
+      if (base + t < end) {
+        float f[8];
+        x[i].get(f);
+        *reinterpret_cast<Vec<uint8_t, 8>*>(codes + t * kCodeRow + 8 * (lane & 15)) = codes_of(f, p.v_scale);
+      }
+    }
+    __syncwarp();
+    for (int a = base; a < end;) {
+      const unsigned later = a < 31 ? all_starts & (0xffffffffu << (a + 1)) : 0u;
+      const int next = later ? min(end, __ffs(later) - 1) : end, len = next - a;
+      const long long to = __shfl_sync(0xffffffffu, at, a);
+      const int o = __shfl_sync(0xffffffffu, off, a) % 16;
+      if ((live >> a) & 1u) {
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const int d = 32 * j + lane;
+          const uint8_t* from = codes + (a - base) * kCodeRow + d;
+          uint8_t* dst = static_cast<uint8_t*>(p.v_cache) + to + d * 16;
+          auto word = [&](int i) {
+            return from[i * kCodeRow] | from[(i + 1) * kCodeRow] << 8 | from[(i + 2) * kCodeRow] << 16 |
+                   (uint32_t)from[(i + 3) * kCodeRow] << 24;
+          };
+          if (len == 16) {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(word(0), word(4), word(8), word(12));
+          } else {
+            for (int i = 0; i < len;) {
+              if ((o + i) % 4 == 0 && len - i >= 4) {
+                *reinterpret_cast<uint32_t*>(dst + i) = word(i);
+                i += 4;
+              } else {
+                dst[i] = from[i * kCodeRow];
+                ++i;
+              }
             }
           }
         }
       }
+      a = next;
     }
-    a = next;
   }
 }
 
@@ -229,16 +252,28 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
   }
   const int part = cta % plan.parts;
   const int first = cta / plan.parts, step = (gridDim.x - plan.value_ctas) / plan.parts;
+  // this part's units of a group and the tokens they belong to
+  const int begin = part * plan.part_units, end = min(plan.tokens * per_token, begin + plan.part_units);
+  const int tok_lo = begin / per_token, tok_hi = (end + per_token - 1) / per_token;
 
   if (threadIdx.x >= kRopeThreads) {
     // ---- slots and angles, one group ahead of the units
     const int j = threadIdx.x - kRopeThreads;
     const unsigned long long f = j < half ? turn_fraction(p.inv_freq[j]) : 0ull;
-    int buf = 0;
+    // lane t: slot and position of token t of a group, loaded a group ahead
+    const int lane = threadIdx.x & 31;
+    auto fetch = [&](int group, long long& slot, int& position) {
+      const long long t = (long long)group * plan.tokens + lane;
+      const bool real = lane < plan.tokens && t < p.num_tokens;
+      slot = real ? p.slot_mapping[t] : -1;
+      position = real ? p.positions[t] : 0;
+    };
+    long long slot;
+    int position, buf = 0;
+    fetch(first, slot, position);
     for (int group = first; group < plan.groups; group += step, buf ^= 1) {
-      const int t0 = group * plan.tokens, nt = min(plan.tokens, p.num_tokens - t0);
+      const int nt = min(plan.tokens, p.num_tokens - group * plan.tokens);
       if (j < nt) {
-        const long long slot = p.slot_mapping[t0 + j];
         long long row = -1;
         if (slot >= 0) {
           const long long block = slot / p.block_size;
@@ -249,14 +284,16 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
         }
         tok_all[buf][j] = row;
       }
-      if (j < half) {
-        for (int t = 0; t < nt; ++t) {
-          const long long turns = (long long)(f * (unsigned long long)(long long)p.positions[t0 + t]);
+      for (int t = tok_lo; t < min(nt, tok_hi); ++t) {
+        const long long at = __shfl_sync(0xffffffffu, position, t);
+        if (j < half) {
+          const long long turns = (long long)(f * (unsigned long long)at);
           float s, c;
           sincospif(__ll2float_rn(turns) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns in [-1, 1]
           cs_all[buf][t * kMaxHalf + cs_at(j / V, j % V)] = make_float2(c * p.magnitude, s * p.magnitude);
         }
       }
+      fetch(group + step, slot, position);
       __syncthreads();
     }
     return;
@@ -266,10 +303,9 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
   int kind[kBatch], tl[kBatch], unit[kBatch], apart[kBatch];
   const T* src[kBatch];     // in token 0's row of the group's first token's array
   long long dst[kBatch];    // elements from the row of q_out, or of kv head 0 in the cache
-  const int end = plan.parts > 1 ? min(per_token, (part + 1) * plan.part_units) : plan.tokens * per_token;
 #pragma unroll
   for (int k = 0; k < kBatch; ++k) {
-    const int i = part * plan.part_units + k * kRopeThreads + threadIdx.x;
+    const int i = begin + k * kRopeThreads + threadIdx.x;
     kind[k] = kNone;
     tl[k] = unit[k] = apart[k] = 0;
     src[k] = nullptr;
@@ -376,15 +412,31 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   plan.tokens = (int)(most / per_token);
   plan.tokens = plan.tokens < 1 ? 1 : plan.tokens > kMaxGroup ? kMaxGroup : plan.tokens;
   plan.parts = plan.tokens > 1 ? 1 : (int)((per_token + most - 1) / most);
-  plan.part_units = plan.parts > 1 ? (int)((per_token + plan.parts - 1) / plan.parts + per_head - 1) / per_head * per_head : 0;
-  plan.groups = (int)(((long long)p.num_tokens + plan.tokens - 1) / plan.tokens);
-  const int walkers = kCtas / plan.parts > 0 ? kCtas / plan.parts : 1;  // CTAs of a part
+  auto groups = [&](int tokens) { return ((long long)p.num_tokens + tokens - 1) / tokens; };
+  auto walkers = [&](int parts) { return (long long)(kCtas / parts > 0 ? kCtas / parts : 1); };  // CTAs of a part
+  auto rounds = [&](int tokens, int parts) { return (groups(tokens) + walkers(parts) - 1) / walkers(parts); };
+  // a prompt's groups are of the size that takes the fewest rounds, by at least a twentieth, since then the threads
+  // hold most units: 512 units a token and room for 768: three tokens in two parts, not one in one (9001 tokens, 64 / 8
+  // heads, bf16: 60.2 -> 57.3 us; 13619 tokens, 40 / 8 heads, fp32: 138 -> 119; an FP8 cache of 40 heads a token, whose
+  // pace its conversions set, 85 -> 90)
+  long long best = rounds(plan.tokens, plan.parts);
+  for (int tokens = 1; best > 4 && tokens <= kMaxGroup; ++tokens) {
+    const int parts = (int)((per_token * tokens + most - 1) / most);
+    if (rounds(tokens, parts) * 20 <= best * 19) {
+      best = rounds(tokens, parts);
+      plan.tokens = tokens;
+      plan.parts = parts;
+    }
+  }
+  const long long group_units = per_token * plan.tokens;
+  plan.part_units = (int)((group_units + plan.parts - 1) / plan.parts + per_head - 1) / per_head * per_head;
+  plan.groups = (int)groups(plan.tokens);
   // (a step's tokens lie in groups of their own: fewer a warp, more warps)
   plan.value_tokens = p.num_tokens <= 256 ? 1 : p.num_tokens <= 2048 ? 4 : kValueTokens;
   const long long value_warps =
       ((long long)p.num_tokens + plan.value_tokens - 1) / plan.value_tokens * p.num_kv_heads;
   plan.value_ctas = FP8 ? (int)((value_warps + kRopeWarps - 1) / kRopeWarps) : 0;
-  const int grid = plan.value_ctas + (plan.groups < walkers ? plan.groups : walkers) * plan.parts;
+  const int grid = plan.value_ctas + (int)std::min(groups(plan.tokens), walkers(plan.parts)) * plan.parts;
   return launch_dependent(rope_kernel<T, FP8, INTERLEAVED, V>, dim3((unsigned)grid), dim3(kRopeThreads + kMaxHalf), 0, stream, p,
                           plan);
 }

@@ -178,6 +178,47 @@ def test_rope_prompt_runs_of_slots(pa, dtype):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype,hq,tokens", [("fp8", 8, 200), ("fp8", 8, 1000), ("fp8", 58, 2600), ("bf16", 60, 2600),
+                                             ("f32", 60, 2700), ("f16", 73, 2500)])
+def test_rope_prompts_with_holes(pa, dtype, hq, tokens):
+    """Prompts over shuffled blocks, with padding and slots outside the pool between and inside them; enough tokens
+    that groups of several are cut into parts."""
+    B = 32
+    r = Rope(pa, dtype, tokens, hq, 2, 128, B, 128, tokens % 200 == 0, seed=tokens + hq)
+    rng = np.random.default_rng(tokens)
+    r.num_blocks = tokens // B + 64
+    r.k, r.v = r.k[:1].repeat(r.num_blocks, 1, 1, 1), r.v[:1].repeat(r.num_blocks, *([1] * (r.v.dim() - 1)))
+    blocks, at, free = rng.permutation(r.num_blocks), 0, 0
+    while at < tokens:
+        length = min(int(rng.choice([1, 3, 16, 31, 47, 200])), tokens - at)
+        first = int(rng.integers(0, B)) if free + 8 < len(blocks) - (tokens - at) // B else 0
+        for _ in range(length):
+            if at == tokens or free == len(blocks):
+                break
+            r.slots[at] = blocks[free] * B + first
+            at, first = at + 1, first + 1
+            if first == B:
+                first, free = 0, free + 1
+        free += first > 0
+        if free >= len(blocks):
+            break
+    r.slots[at:] = -1
+    assert at > tokens // 2
+    live = r.slots[r.slots >= 0]
+    assert len(np.unique(live)) == len(live)
+    holes = rng.choice(tokens, tokens // 12, replace=False)
+    r.slots[holes] = -1
+    bad = rng.choice(at, 9, replace=False)
+    good = r.slots.copy()
+    r.slots[bad[:6]], r.slots[bad[6:]] = r.num_blocks * B, 2 ** 62
+    r.run()
+    assert int(r.err.item()) == 2
+    r.err.zero_()
+    r.slots = good
+    r.slots[bad] = -1
+    r.check()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
 def test_rope_in_place_and_padding(pa, dtype):
     r = Rope(pa, dtype, 37, 8, 2, 128, 16, 96, False, seed=4, padding=(0, 5, 36))
