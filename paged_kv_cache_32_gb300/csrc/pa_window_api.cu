@@ -19,6 +19,7 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kMaxCluster = 8;     // the portable cluster size (rows kernels also take the largest, twice that)
 constexpr int kMinCtaTokens = 64;  // tokens of a CTA below which a split no longer pays
+constexpr int kLongShare = 600;    // fp32: tokens of a CTA that is split though every SM has its CTAs
 
 // How the rows kernels spread over the SMs.  A warp holds 16 KB of slabs, so an SM takes 4 CTAs of 3 warps, 3 of 4
 // or 2 of 6.
@@ -38,7 +39,9 @@ constexpr int kMinCtaTokens = 64;  // tokens of a CTA below which a split no lon
 //    2500 to 40000 tokens with a window of 8192: 240 -> 226 us, and costs as much when they are equal, 246 -> 264.)
 //  * fp32 (CUDA cores): four warps a CTA, three CTAs an SM, split while that many are not there, in clusters of 16
 //    up to two an SM (8 kv heads, 1024 / 4096 keys: 18.7 -> 15.0 and 45.2 -> 29.8 us; 16 items 20.0 -> 17.0 and
-//    52.3 -> 37.2).
+//    52.3 -> 37.2).  A warp walks its keys slowly there, so that the longest item sets the time: long ones are split
+//    on as long as a CTA keeps kLongShare keys (392 items of head size 64, up to 1285 keys 118 -> 75 us, W = 3538 389
+//    -> 279; 128 items, W = 4096, 212 -> 138; equal items of 1024 keys would lose, 118 -> 129).
 void spread(int32_t dtype, long long items, long long max_keys, pa::WindowParams& p) {
   p.cluster = 1;
   if (dtype == PA_F32) {
@@ -46,6 +49,8 @@ void spread(int32_t dtype, long long items, long long max_keys, pa::WindowParams
     while (p.cluster < kMaxCluster && items * p.cluster * 2 <= 3 * kSms && max_keys / (2 * p.cluster) >= kMinCtaTokens)
       p.cluster *= 2;
     if (items * 2 * kMaxCluster <= 2 * kSms && max_keys / (2 * kMaxCluster) >= kMinCtaTokens) p.cluster = 2 * kMaxCluster;
+    while (p.cluster < kMaxCluster && items * p.cluster * 2 <= 12 * kSms && max_keys / (2 * p.cluster) >= kLongShare)
+      p.cluster *= 2;
     return;
   }
   if (items <= kSms / 2) {

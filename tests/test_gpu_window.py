@@ -129,6 +129,16 @@ def test_decode_window_many_sequences(dtype):
         check(s, w.reference(), f"{n} sequences")
 
 
+def test_decode_window_many_long_sequences():
+    """fp32: more items than the SMs hold, long enough to be split all the same."""
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(1, 2600, 60)]
+    w = WindowCase("f32", lens, [1] * 60, 8, 8, 64, 16, 2400, 4, seed=31)
+    s = Step(w)
+    s.decode()
+    check(s, w.reference(), "f32, 480 items")
+
+
 @pytest.mark.parametrize("dtype,hkv,append", [("f32", 2, False), ("f16", 1, True), ("bf16", 8, False), ("bf16", 4, True),
                                               ("fp8", 8, True), ("fp8", 2, False)])
 def test_decode_window_few_long_sequences(dtype, hkv, append):
