@@ -37,6 +37,17 @@ __device__ __forceinline__ void copy_row(float* slot, const float* src, bool tak
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(slot)), "l"(src), "r"(bytes) : "memory");
 }
 
+// a * b + c of two pairs, one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const WindowParams p) {
   constexpr int VEC = D / 32, OROW = D, STRIDE = 8 * D + 16;
@@ -59,14 +70,16 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
   const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
   const int B = p.block_size;
 
-  float q[8][VEC], o[8][VEC];
+  float2 q[4][VEC], o[4][VEC];  // rows 2r and 2r + 1
+  auto q_at = [&](int r, int e) {  // (q is 4-byte aligned only)
+    return r < it.gcount ? __ldg(static_cast<const float*>(p.q) + rows_offset(p, it, r) * D + lane * VEC + e) : 0.f;
+  };
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
+  for (int r = 0; r < 4; ++r) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      // (q is 4-byte aligned only)
-      q[r][e] = r < it.gcount ? __ldg(static_cast<const float*>(p.q) + rows_offset(p, it, r) * D + lane * VEC + e) : 0.f;
-      o[r][e] = 0.f;
+      q[r][e] = make_float2(q_at(2 * r, e), q_at(2 * r + 1, e));
+      o[r][e] = make_float2(0.f, 0.f);
     }
   }
   // this lane's row and its token of four (lane = 8 * token + row); rows past the item: the last row's position
@@ -79,7 +92,7 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
   float* ring = ring_all + warp * (kRing * STEP) + lane * VEC;
   const int mine_n = it.v1 - it.v0, n_my = mine_n > warp ? (mine_n - warp + kF32Warps - 1) / kF32Warps : 0;
   auto slab_tok = [&](int k) { return rows_slab(it, it.v0 + warp + k * kF32Warps) * kF32Slab; };
-  // lane t < 16: the block of token t of slab k (-1: seen by no row, or not in the pool)
+  // lane t < 16: the cache row of token t of slab k (-1: seen by no row, or not in the pool)
   auto fetch = [&](int k) {
     int e = -1;
     if (k < n_my && lane < kF32Slab) {
@@ -89,6 +102,8 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
         if (e < 0 || e >= p.num_blocks) {
           report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
           e = -1;
+        } else {
+          e = (e * p.num_kv_heads + it.hkv) * B + t % B;  // (every row's number fits int32)
         }
       }
     }
@@ -107,12 +122,12 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
         live_prev = live;
         live = __ballot_sync(0xffffffffu, entry >= 0);
       }
-      const int t0 = 4 * (i % 4), tok0 = slab_tok(i / 4) + t0;
+      const int t0 = 4 * (i % 4);
       float* st = ring + (i % kRing) * STEP;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int e = __shfl_sync(0xffffffffu, entry, t0 + t);
-        const size_t row = e >= 0 ? (((size_t)e * p.num_kv_heads + it.hkv) * B + (tok0 + t) % B) * D : 0;
+        const size_t row = (size_t)max(e, 0) * D;
         copy_row<VEC>(st + t * D, kc + row, e >= 0);
         copy_row<VEC>(st + (4 + t) * D, vc + row, e >= 0);
       }
@@ -140,11 +155,12 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          float d = q[r][0] * k[t][0];
+        for (int r = 0; r < 4; ++r) {
+          float2 d = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 1; i < VEC; ++i) d = fmaf(q[r][i], k[t][i], d);
-          dot[8 * t + r] = d;
+          for (int i = 0; i < VEC; ++i) d = fma2(q[r][i], make_float2(k[t][i], k[t][i]), d);
+          dot[8 * t + 2 * r] = d.x;
+          dot[8 * t + 2 * r + 1] = d.y;
         }
       // halving exchange: after the step with offset w, a lane keeps the values whose bit w equals its own
 #pragma unroll
@@ -167,10 +183,10 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
         m = mn;
         l *= al;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float a = __shfl_sync(0xffffffffu, al, r);
+        for (int r = 0; r < 4; ++r) {
+          const float a0 = __shfl_sync(0xffffffffu, al, 2 * r), a1 = __shfl_sync(0xffffffffu, al, 2 * r + 1);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) o[r][i] *= a;
+          for (int i = 0; i < VEC; ++i) o[r][i].x *= a0, o[r][i].y *= a1;
         }
       }
       const float pe = fast_exp2(s - (m == -INFINITY ? 0.f : m));
@@ -182,10 +198,11 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float w = __shfl_sync(0xffffffffu, pe, 8 * t + r);
+        for (int r = 0; r < 4; ++r) {
+          const float2 w = make_float2(__shfl_sync(0xffffffffu, pe, 8 * t + 2 * r),
+                                       __shfl_sync(0xffffffffu, pe, 8 * t + 2 * r + 1));
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) o[r][i] = fmaf(w, x[t][i], o[r][i]);
+          for (int i = 0; i < VEC; ++i) o[r][i] = fma2(w, make_float2(x[t][i], x[t][i]), o[r][i]);
         }
     }
   }
@@ -196,7 +213,7 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
 #pragma unroll
   for (int r = 0; r < 8; ++r)
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) wo[r * OROW + lane * VEC + i] = o[r][i];
+    for (int i = 0; i < VEC; ++i) wo[r * OROW + lane * VEC + i] = r % 2 ? o[r / 2][i].y : o[r / 2][i].x;
   if (lane < 8) {
     wo[8 * OROW + 2 * lane] = m;
     wo[8 * OROW + 2 * lane + 1] = l;
