@@ -38,10 +38,10 @@ constexpr int kLongShare = 600;    // fp32: tokens of a CTA that is split though
 //    (Splitting long items in two all the same evens out a last round of unequal contexts, 96 FP8 sequences of
 //    2500 to 40000 tokens with a window of 8192: 240 -> 226 us, and costs as much when they are equal, 246 -> 264.)
 //  * fp32 (CUDA cores): four warps a CTA, three CTAs an SM, split while that many are not there, in clusters of 16
-//    up to two an SM (8 kv heads, 1024 / 4096 keys: 18.7 -> 15.0 and 45.2 -> 29.8 us; 16 items 20.0 -> 17.0 and
-//    52.3 -> 37.2).  A warp walks its keys slowly there, so that the longest item sets the time: long ones are split
-//    on as long as a CTA keeps kLongShare keys (392 items of head size 64, up to 1285 keys 118 -> 75 us, W = 3538 389
-//    -> 279; 128 items, W = 4096, 212 -> 138; equal items of 1024 keys would lose, 118 -> 129).
+//    up to two an SM (8 kv heads, 1024 / 4096 keys: 13.3 -> 11.7 and 28.0 -> 20.7 us; 16 items 15.1 -> 13.6 and
+//    34.6 -> 26.9).  A warp walks its keys slowly there, so that the longest item sets the time: long ones are split
+//    on as long as a CTA keeps kLongShare keys (392 items of head size 64, up to 1285 keys 77 -> 56 us, W = 3538 263
+//    -> 187; 128 items, W = 4096, 137 -> 96; equal items of 1024 keys would lose, 80 -> 90).
 void spread(int32_t dtype, long long items, long long max_keys, pa::WindowParams& p) {
   p.cluster = 1;
   if (dtype == PA_F32) {

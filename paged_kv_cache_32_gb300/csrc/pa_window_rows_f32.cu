@@ -7,12 +7,13 @@
 // the four K and V rows, the 8 rows x 4 tokens = 32 partial dot products are
 // reduced together (a halving exchange: 31 shuffles leave score j in lane j,
 // where a sum of each alone would take 160), the online softmax works on one
-// score a lane, and the 32 weights are passed round for O += P V.  About 420
-// instructions per 4 KB of K/V at D = 128, as many cycles again in waits between
-// them: three warps a scheduler keep up with HBM if no load is waited for.  So
+// score a lane, and the 32 weights are passed round for O += P V.  Bound by
+// instruction issue as much as by HBM: the products go as packed pairs of rows, and
+// a lane works out its token's cache row once a slab (single products and a row for
+// every copy: 304 us where it now takes 191).  No load is waited for either:
 // each lane copies its own elements kRing - 1 steps ahead into shared memory
 // (cp.async: no registers, and no barrier, since it alone reads them back).
-// 128 sequences, 8 kv heads of 128, 1024 keys: 304 us, 3.5 TB/s.
+// 128 sequences, 64 / 8 heads of 128, 1024 keys: 191 us, 5.7 TB/s.
 #include <cuda.h>
 #include <math.h>
 
