@@ -432,7 +432,7 @@ int pa_decode_window(void* out, const void* q, void* k_cache, void* v_cache, con
  *   have been released).  Value rows of positions that some queries of the chunk see and others do not must
  *   be finite.
  *   scale        finite and > 0;  window >= 1;  num_sinks >= 0
- *   k_scale, v_scale  FP8 caches (> 0; 0 means 1): q and out are fp16
+ *   k_scale, v_scale  FP8 caches (> 0; 0 means 1): q and out are fp16.  Ignored for other caches.
  *   Every cache type, head size and block size of pa_decode.  No workspace.
  */
 int pa_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,

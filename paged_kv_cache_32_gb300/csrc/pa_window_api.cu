@@ -88,10 +88,11 @@ int check_window(const pa_cache_desc* cache, int32_t num_seqs, int32_t num_q_hea
   return PA_OK;
 }
 
+// The scales of an FP8 cache; those of any other are 1, whatever the caller passes (the kernels multiply by them).
 int check_scales(const pa_cache_desc* cache, float* k_scale, float* v_scale) {
-  if (*k_scale == 0.f) *k_scale = 1.f;
-  if (*v_scale == 0.f) *v_scale = 1.f;
-  if (cache->dtype != PA_FP8_E4M3) return PA_OK;
+  const bool fp8 = cache->dtype == PA_FP8_E4M3;
+  if (!fp8 || *k_scale == 0.f) *k_scale = 1.f;
+  if (!fp8 || *v_scale == 0.f) *v_scale = 1.f;
   return *k_scale > 0.f && !isinf(*k_scale) && *v_scale > 0.f && !isinf(*v_scale) ? PA_OK : PA_ERR_INVALID_ARG;
 }
 
