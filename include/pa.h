@@ -403,7 +403,8 @@ int pa_rope_and_cache(void* q_out, void* k_cache, void* v_cache, const void* q, 
  *     i <= p  with  i > p - window  or  i < num_sinks.
  *   A window no shorter than the sequence sees all of it.  Table entries of blocks that hold no visible
  *   position are never read and their blocks never touched: they may have been released.  Other positions of
- *   a block that holds a visible one are loaded and have no effect, whatever they contain.
+ *   a block that holds a visible one are loaded and have no effect, whatever they contain.  A NaN in a query or
+ *   in a key that it sees makes the whole row NaN (pa_decode: zeros), one in a value that element of it.
  *
  *   key, value   both NULL, or the step's append as in pa_decode_append (f16, bf16, FP8 caches): each
  *                sequence's new token is stored at position seq_lens[s] - 1 and attended in the same launch
@@ -430,7 +431,7 @@ int pa_decode_window(void* out, const void* q, void* k_cache, void* v_cache, con
  *                written.  A sequence whose chunk breaks the rules there is skipped (PA_DEVERR_QUERY).
  *   Table entries of blocks without a position that some query of the chunk sees are never read (they may
  *   have been released).  Value rows of positions that some queries of the chunk see and others do not must
- *   be finite.
+ *   be finite.  NaN queries and keys as for pa_decode_window: only the rows that see them become NaN.
  *   scale        finite and > 0;  window >= 1;  num_sinks >= 0
  *   k_scale, v_scale  FP8 caches (> 0; 0 means 1): q and out are fp16.  Ignored for other caches.
  *   Every cache type, head size and block size of pa_decode.  No workspace.

@@ -134,7 +134,7 @@ __device__ __forceinline__ void rows_zero(const WindowParams& p, const RowsItem&
 // and then (m, l)[8 rows] (max score in log2 units, sum of 2^(s - m)).  With m* = max m and weights
 // 2^(m - m*), O = sum weight O and l = sum weight l over the warps, then in the same way over the CTAs of the
 // cluster, whose results sit in each CTA's `mine` (8 x D floats, then 8 pairs); each CTA writes its share of
-// the output elements.  Called by every thread after the barrier that follows the warps' stores; wt: 8 * NW
+// the output elements: O / l, zeros where l is 0 (no weight), NaN where a score was NaN (l is).  Called by every thread after the barrier that follows the warps' stores; wt: 8 * NW
 // + 16 floats apart from the parts.
 template <typename TOut, int D, int NW, int OROW, int STRIDE>
 __device__ __forceinline__ void rows_finish(const WindowParams& p, const RowsItem& it, const float* parts, float* wt,
@@ -173,7 +173,7 @@ __device__ __forceinline__ void rows_finish(const WindowParams& p, const RowsIte
     for (int w = 0; w < NW; ++w) acc += wt[r * NW + w] * parts[w * STRIDE + r * OROW + d];
     if (C == 1) {
       const float l = lsum[r];
-      reinterpret_cast<TOut*>(p.out)[rows_offset(p, it, r) * D + d] = from_float<TOut>(l > 0.f ? acc / l : 0.f);
+      reinterpret_cast<TOut*>(p.out)[rows_offset(p, it, r) * D + d] = from_float<TOut>(l == 0.f ? 0.f : acc / l);
     } else {
       mine[i] = acc;
     }
@@ -193,7 +193,7 @@ __device__ __forceinline__ void rows_finish(const WindowParams& p, const RowsIte
       l = fmaf(x, ld_cluster(mine + 8 * D + 2 * r + 1, c), l);
       acc = fmaf(x, ld_cluster(mine + i, c), acc);
     }
-    reinterpret_cast<TOut*>(p.out)[rows_offset(p, it, r) * D + d] = from_float<TOut>(l > 0.f ? acc / l : 0.f);
+    reinterpret_cast<TOut*>(p.out)[rows_offset(p, it, r) * D + d] = from_float<TOut>(l == 0.f ? 0.f : acc / l);
   }
   cluster_sync_all();  // no CTA leaves while another reads its results
 }

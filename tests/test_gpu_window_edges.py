@@ -46,3 +46,75 @@ def test_scales_are_those_of_fp8_caches(dtype, form):
         assert torch.equal(s.prefill(k_scale=k_scale, v_scale=v_scale), chunk)
         assert torch.equal(t.decode(k_scale=k_scale, v_scale=v_scale), step)
         assert int(s.err.item()) == 0 and int(t.err.item()) == 0
+
+
+# ---------------------------------------------------------------- NaN where it is seen
+def nan_key(s, seq, pos, head):
+    """The key of a kv head at a position of sequence seq becomes NaN, in all dimensions."""
+    w = s.w
+    block, off = int(w.table[seq, pos // w.B]), pos % w.B
+    s.k[block, head, off] = 0x7F if w.dtype == "fp8" else float("nan")
+
+
+def check_nan_rows(s, ref, nan):
+    """The rows of `nan` [queries, heads] are NaN from end to end, the others right."""
+    from harness import out_f64, within_bound
+    got = out_f64(s.out)
+    assert int(s.err.item()) == 0
+    assert np.isnan(got[nan]).all(), f"{np.sum(~np.isnan(got[nan]).all(-1))} of {nan.sum()} rows are not NaN"
+    assert not np.isnan(got[~nan]).any()
+    ok, err, ratio = within_bound(got[~nan], ref[~nan], s.w.qdt)
+    assert ok, f"max abs err {err}, worst err/bound {ratio}"
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 128), ("f32", 64), ("f16", 128), ("bf16", 64), ("bf16", 128), ("fp8", 128)])
+@pytest.mark.parametrize("lens", [[40, 700, 1, 300], [9001]])
+def test_decode_window_nan_is_not_hidden(dtype, d, lens):
+    """A NaN in a query, or in a key that it sees, makes the row NaN, whoever computes it (a CTA, a large cluster);
+    where nothing sees the key it has no effect."""
+    hq, hkv = 8, 2
+    w = WindowCase(dtype, lens, [1] * len(lens), hq, hkv, d, 16, 4200 if len(lens) == 1 else 200, 3, seed=3)
+    ref = w.reference()
+    for what in ("query", "key", "first key", "unseen key"):
+        s = Step(w)
+        nan = np.zeros((len(lens), hq), bool)
+        seq = int(np.argmax(lens))
+        if what == "query":
+            s.q[seq, 5] = float("nan")
+            nan[seq, 5] = True
+        else:
+            pos = {"key": lens[seq] - 9, "first key": 1, "unseen key": 12}[what]
+            if what == "unseen key":  # in the block of the first keys, which is loaded
+                assert w.sinks <= pos <= lens[seq] - 1 - w.window and pos // w.B == 0
+            nan_key(s, seq, pos, 1)
+            nan[seq, hq // hkv:] = what != "unseen key"
+        s.decode()
+        check_nan_rows(s, ref, nan)
+
+
+@pytest.mark.parametrize("form", CHUNK_FORMS)
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16", "fp8"])
+def test_prefill_window_nan_is_not_hidden(dtype, form):
+    """The same for the queries of a chunk: those that see the key are NaN, those before it and those whose window
+    has passed it are right."""
+    w = chunk_case(form, dtype, seed=3)
+    ref = w.reference()
+    start, G = w.query_start(), w.hq // w.hkv
+    rows = np.arange(start[-1])
+    seq = int(np.argmax(w.chunks))
+    L, n = w.lens[seq], w.chunks[seq]
+    pos = np.arange(L - n, L)  # of the sequence's queries
+    for what in ("query", "key", "first key"):
+        s = Step(w)
+        nan = np.zeros((len(rows), w.hq), bool)
+        if what == "query":
+            s.q[start[seq] + n // 2, 1] = float("nan")
+            nan[start[seq] + n // 2, 1] = True
+        else:
+            at = L - n + n // 2 if what == "key" else 1
+            nan_key(s, seq, at, w.hkv - 1)
+            sees = (at <= pos) & ((at > pos - w.window) | (at < w.sinks))
+            nan[start[seq]:start[seq + 1], (w.hkv - 1) * G:] = sees[:, None]
+            assert sees.any() and (what == "first key" or not sees.all() or n <= 2)
+        s.prefill()
+        check_nan_rows(s, ref, nan)
