@@ -387,12 +387,13 @@ def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, method: int = PA
     PA_ROPE_NTK, PA_ROPE_YARN or PA_ROPE_BANDS, the ways to stretch the frequencies for contexts longer than the
     trained one."""
     import torch
-    inv = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64)
+    # (the call writes rotary_dim / 2 numbers, and ctypes would wrap an integer past int32 into another)
+    if not 2 <= int(rotary_dim) <= 128 or not PA_ROPE_PLAIN <= int(method) <= PA_ROPE_BANDS:
+        raise PaError(3, "pa_rope_frequencies")
+    inv = torch.empty(int(rotary_dim) // 2, dtype=torch.float64)
     mag = ctypes.c_float(1.0)
     s = pa_rope_scaling(int(method), factor, original_max_position, beta_fast, beta_slow, attention_factor,
                         low_freq_factor, high_freq_factor)
-    if int(rotary_dim) > 128:
-        raise PaError(3, "pa_rope_frequencies")
     _check(lib().pa_rope_frequencies(_ptr(inv), ctypes.addressof(mag), int(rotary_dim), float(base), ctypes.byref(s)),
            "pa_rope_frequencies")
     return (inv if device is None else inv.to(device)), mag.value
