@@ -310,8 +310,13 @@ def pa_copy_blocks(k_cache, v_cache, block_pairs, err_flag=None, stream=None, de
 # ---------------------------------------------------------------- rotary positions and windowed attention
 # A step makes one of these calls per layer, and a small one takes the GPU a few microseconds, so the checks are
 # written out: each call tests types and devices in one expression, and looks for the reason only when that fails.
-_INT32_MAX = 2 ** 31 - 1  # (ctypes would wrap longer windows)
+_INT32_MIN, _INT32_MAX = -2 ** 31, 2 ** 31 - 1
 _ROWS: dict = {}  # cache dtype -> (dtype code, dtype of queries and new rows)
+
+
+def _int32(x) -> int:
+    """x, or the end of int32 on its side (ctypes would wrap it into another number)."""
+    return max(_INT32_MIN, min(int(x), _INT32_MAX))
 
 
 def _rows_of(dtype, where: str):
@@ -518,8 +523,8 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, scale: fl
         opts = pa_decode_options(slopes, float(k_scale or 0.0), float(v_scale or 0.0), int(test_flags))
     _launch(lib().pa_decode_window, dev, (
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, block_tables.data_ptr(),
-        seq_lens.data_ptr(), shape[0], shape[1], table[1], desc, float(scale), min(int(window), _INT32_MAX),
-        min(int(num_sinks), _INT32_MAX), err, _stream_of(dev, stream), opts), where)
+        seq_lens.data_ptr(), shape[0], shape[1], table[1], desc, float(scale), _int32(window),
+        _int32(num_sinks), err, _stream_of(dev, stream), opts), where)
 
 
 def pa_prefill_window(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_query_len: int, scale: float,
@@ -540,6 +545,6 @@ def pa_prefill_window(out, q, k_cache, v_cache, block_tables, seq_lens, query_st
     _launch(lib().pa_prefill_window, dev, (
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), query_start.data_ptr(), table[0], shape[0], shape[1], table[1],
-        min(int(max_query_len), shape[0]), desc,
-        float(scale), min(int(window), _INT32_MAX), min(int(num_sinks), _INT32_MAX), float(k_scale or 0.0),
+        min(_int32(max_query_len), shape[0]), desc,
+        float(scale), _int32(window), _int32(num_sinks), float(k_scale or 0.0),
         float(v_scale or 0.0), err, _stream_of(dev, stream)), where)
