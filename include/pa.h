@@ -352,7 +352,8 @@ int pa_decode_noalloc(void* out, const void* q, const void* k_cache, const void*
  *                     inv_freq / factor * (1 - keep_j) + inv_freq * keep_j,
  *                     keep_j = clamp((n_j - low_freq_factor) / (high_freq_factor - low_freq_factor), 0, 1)
  *   *magnitude is 1 except for PA_ROPE_YARN.  rotary_dim even, 2 .. 128; base, and the fields that the
- *   method names, finite and > 0 (attention_factor >= 0, high_freq_factor > low_freq_factor).
+ *   method names, finite and > 0 (attention_factor >= 0, high_freq_factor > low_freq_factor), such that the
+ *   frequencies and the magnitude are finite; otherwise PA_ERR_INVALID_ARG, and inv_freq holds nothing of use.
  */
 enum { PA_ROPE_PLAIN = 0, PA_ROPE_LINEAR = 1, PA_ROPE_NTK = 2, PA_ROPE_YARN = 3, PA_ROPE_BANDS = 4 };
 typedef struct {

@@ -31,11 +31,13 @@ int pa_rope_frequencies(double* inv_freq, float* magnitude, int32_t rotary_dim, 
   if (method == PA_ROPE_NTK) {
     if (r < 4) return PA_ERR_INVALID_ARG;  // the base's exponent r / (r - 2)
     base *= pow(factor, (double)r / (r - 2));
+    if (!positive(base)) return PA_ERR_INVALID_ARG;
   }
   double lo = 0.0, hi = 0.0, mag = 1.0;
   if (method == PA_ROPE_YARN) {
     if (!positive(scaling->original_max_position) || !positive(scaling->beta_fast) ||
-        !positive(scaling->beta_slow) || base == 1.0 || !(scaling->attention_factor >= 0.0))
+        !positive(scaling->beta_slow) || base == 1.0 ||
+        !(scaling->attention_factor == 0.0 || positive(scaling->attention_factor)))
       return PA_ERR_INVALID_ARG;
     // the pair whose wavelength makes n turns over the trained length
     auto pair_of = [&](double n) {
@@ -44,10 +46,11 @@ int pa_rope_frequencies(double* inv_freq, float* magnitude, int32_t rotary_dim, 
     lo = fmax(0.0, floor(pair_of(scaling->beta_fast)));
     hi = fmin(r - 1.0, ceil(pair_of(scaling->beta_slow)));
     mag = scaling->attention_factor > 0.0 ? scaling->attention_factor : factor > 1.0 ? 0.1 * log(factor) + 1.0 : 1.0;
+    if (isinf((float)mag)) return PA_ERR_INVALID_ARG;
   }
   if (method == PA_ROPE_BANDS &&
       (!positive(scaling->original_max_position) || !positive(scaling->low_freq_factor) ||
-       !(scaling->high_freq_factor > scaling->low_freq_factor)))
+       !positive(scaling->high_freq_factor) || !(scaling->high_freq_factor > scaling->low_freq_factor)))
     return PA_ERR_INVALID_ARG;
   for (int j = 0; j < r / 2; ++j) {
     double f = pow(base, -2.0 * j / r);
@@ -62,6 +65,7 @@ int pa_rope_frequencies(double* inv_freq, float* magnitude, int32_t rotary_dim, 
                                                   (scaling->high_freq_factor - scaling->low_freq_factor)));
       f = f / factor * (1.0 - keep) + f * keep;
     }
+    if (!isfinite(f)) return PA_ERR_INVALID_ARG;  // a factor so small that 1 / factor is none
     inv_freq[j] = f;
   }
   *magnitude = (float)mag;

@@ -85,3 +85,18 @@ def test_window_integers_keep_their_side_of_zero(launched, value):
     assert decode(value, 0) == [want, 0] and decode(5, value) == [5, want]
     assert prefill(value, 0) == [want, 0, 3] and prefill(5, value) == [5, want, 3]
     assert prefill(5, 0, value) == [5, 0, min(want, 6)]  # (a batch of six queries)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(method=3, factor=2.0, original_max_position=100.0, attention_factor=float("inf")),
+    dict(method=3, factor=2.0, original_max_position=100.0, attention_factor=1e39),   # past fp32, the magnitude's type
+    dict(method=4, factor=2.0, original_max_position=100.0, high_freq_factor=float("inf")),
+    dict(method=1, factor=1e-320),                                                    # 1 / factor past fp64
+    dict(method=3, factor=1e-320, original_max_position=100.0),
+    dict(method=2, factor=1e300),                                                     # base * factor^(r / (r - 2))
+])
+def test_rope_frequencies_are_finite(kw):
+    """Frequencies and magnitude that come out without a NaN or an infinity, or an error."""
+    pa.build()
+    with pytest.raises(pa.PaError):
+        pa.pa_rope_frequencies(64, **{"base": 10000.0, **kw})
