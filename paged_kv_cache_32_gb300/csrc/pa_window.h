@@ -1,6 +1,8 @@
 // pa_window.h - launch parameters of the windowed attention kernels (not part of the public ABI).
 #pragma once
 
+#include <atomic>
+
 #include "pa_launch.h"
 
 namespace pa {
@@ -35,12 +37,48 @@ struct WindowParams {
   void* v_cache_out;
 };
 
-// What a rows kernel needs before its launch: its shared memory, and clusters beyond the portable eight CTAs.
+// Whether devices have room for a cluster of a kernel's beyond the portable eight CTAs, one of these per kernel.
+struct ClusterRoom {
+  static constexpr int kDevices = 64;
+  std::atomic<signed char> known[kDevices] = {};  // 0: not asked yet, 1: yes, -1: no
+};
+constexpr int kPortableCluster = 8;
+
+// What a rows kernel needs before its launch: its shared memory, and a cluster size that the current device places:
+// a larger one than eight may not fit any of its GPCs (of which some have fewer SMs, or a context may hold few), and
+// a launch of one that does not is an error, so *cluster becomes eight there.  The device is asked once.
 template <typename Kernel>
-cudaError_t prepare_rows(Kernel kernel, size_t smem, int cluster) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess && cluster > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  return e;
+cudaError_t prepare_rows(Kernel kernel, ClusterRoom& room, int threads, size_t smem, int32_t* cluster) {
+  const void* f = reinterpret_cast<const void*>(kernel);
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess || *cluster <= kPortableCluster) return e;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev < ClusterRoom::kDevices;
+  int fits = kept ? room.known[dev].load(std::memory_order_relaxed) : 0;
+  if (fits == 0) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)*cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)*cluster);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, f, &cfg) != cudaSuccess) {
+      clusters = 0;
+      (void)cudaGetLastError();  // the answer is no: the call goes on
+    }
+    fits = clusters > 0 ? 1 : -1;
+    if (kept) room.known[dev].store((signed char)fits, std::memory_order_relaxed);
+  }
+  if (fits < 0) *cluster = kPortableCluster;
+  return cudaSuccess;
 }
 
 // items of a rows launch: eight query rows of one kv head each

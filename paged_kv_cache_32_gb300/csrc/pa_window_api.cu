@@ -17,7 +17,7 @@ using namespace pa::host;
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kMaxCluster = 8;     // the portable cluster size (rows kernels also take the largest, twice that)
+constexpr int kMaxCluster = pa::kPortableCluster;  // (rows kernels also take the largest, twice that, where it fits)
 constexpr int kMinCtaTokens = 64;  // tokens of a CTA below which a split no longer pays
 constexpr int kLongShare = 600;    // fp32: tokens of a CTA that is split though every SM has its CTAs
 

@@ -224,10 +224,11 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
 }
 
 template <int D>
-cudaError_t launch_f32(const WindowParams& p, cudaStream_t stream) {
+cudaError_t launch_f32(WindowParams p, cudaStream_t stream) {
   auto kernel = window_rows_f32_kernel<D>;
   constexpr size_t kSmem = (size_t)kF32Warps * kRing * 8 * D * sizeof(float);
-  cudaError_t e = prepare_rows(kernel, kSmem, p.cluster);
+  static ClusterRoom room;
+  cudaError_t e = prepare_rows(kernel, room, kF32Warps * 32, kSmem, &p.cluster);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(kF32Warps * 32), kSmem, p.cluster,
                         true, stream, p);

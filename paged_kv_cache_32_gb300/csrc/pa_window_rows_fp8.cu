@@ -353,11 +353,11 @@ __global__ void __launch_bounds__(RowsFp8Shape<D, NW, NS>::THREADS)
 }  // namespace
 
 template <int NW>
-static cudaError_t launch_warps(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p,
-                                cudaStream_t stream) {
+static cudaError_t launch_warps(const CUtensorMap& tk, const CUtensorMap& tk32, WindowParams p, cudaStream_t stream) {
   using S = RowsFp8Shape<128, NW, 2>;
   auto kernel = window_rows_fp8_kernel<128, NW, 2>;
-  cudaError_t e = prepare_rows(kernel, S::SMEM_BYTES, p.cluster);
+  static ClusterRoom room;
+  cudaError_t e = prepare_rows(kernel, room, S::THREADS, S::SMEM_BYTES, &p.cluster);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
                         p.cluster, true, stream, tk, tk32, p);

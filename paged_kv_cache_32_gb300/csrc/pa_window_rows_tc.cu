@@ -334,10 +334,11 @@ __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
 }
 
 template <typename T, int D, int NW, int NS, bool SPLIT>
-cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const WindowParams& p, cudaStream_t stream) {
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, WindowParams p, cudaStream_t stream) {
   using S = RowsShape<D, NW, NS>;
   auto kernel = window_rows_tc_kernel<T, D, NW, NS, SPLIT>;
-  cudaError_t e = prepare_rows(kernel, S::SMEM_BYTES, p.cluster);
+  static ClusterRoom room;
+  cudaError_t e = prepare_rows(kernel, room, S::THREADS, S::SMEM_BYTES, &p.cluster);
   if (e != cudaSuccess) return e;
   return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
                         p.cluster, true, stream, tk, tv, p);
