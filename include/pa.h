@@ -427,6 +427,8 @@ int pa_decode_window(void* out, const void* q, void* k_cache, void* v_cache, con
  *   tokens of pa_decode_window: query j of sequence s, at position p = L - n + j, sees the positions i <= p
  *   with i > p - window or i < num_sinks.  The chunk's own K/V are in the cache already (pa_rope_and_cache,
  *   pa_reshape_and_cache).  Chunks of one token (a decode step) to whole prompts, and any mixture of them.
+ *   (Many single tokens beside long chunks run faster as two calls, theirs to pa_decode_window: 1023 and a prompt of 4096,
+ *   64 / 8 heads, window 1024, bf16: 0.66 ms for 1.62.)
  *
  *   out, q, query_start, seq_lens, max_query_len  as for pa_prefill; out rows outside every chunk are not
  *                written.  A sequence whose chunk breaks the rules there is skipped (PA_DEVERR_QUERY).

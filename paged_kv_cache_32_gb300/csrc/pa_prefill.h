@@ -41,7 +41,10 @@ bool encode_query_map(CUtensorMap* map, const void* base, const pa_cache_desc* c
 // tq: q as [tokens][heads][D] (box 64 columns x 1 head x 128 tokens, windowed 2^pack_log2 heads x the tile's
 // tokens, 128-byte swizzle); to: out, the same
 // dtype: the cache's (FP8: windowed form only, tk and tv not used)
+// mixed: windowed form, most sequences' chunks are far shorter than max_query_len (no field of the parameters: one
+// more there, wherever it stood, moved the kernels' spills about and cost FP8 chunks 3 to 20 %)
 cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
-                              const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream);
+                              const CUtensorMap& to, const PrefillParams& p, bool mixed,
+                              cudaStream_t stream);
 
 }  // namespace pa

@@ -90,7 +90,7 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
   p.split = 1;
   p.max_query_len = max_query_len;
   p.v_scale = 1.f;
-  cudaError_t e = pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, static_cast<cudaStream_t>(stream));
+  cudaError_t e = pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, false, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

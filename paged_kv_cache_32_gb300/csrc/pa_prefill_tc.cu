@@ -441,6 +441,12 @@ __device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfItem&
   return true;
 }
 
+// Is the chunk outside q / out, longer than the caller's bound or than its sequence, or the sequence past its table?
+__device__ __forceinline__ bool pf_bad_chunk(const PrefillParams& p, const PfItem& it) {
+  return it.q0 < 0 || it.n < 0 || (long long)it.q0 + it.n > p.num_query_tokens || it.n > p.max_query_len ||
+         it.L < it.n || (long long)it.L > (long long)p.max_blocks * p.block_size;
+}
+
 // An item of the windowed form: rows of 2^pack_log2 heads from h on, queries tile0 ..
 struct PfWindowItem : PfItem {
   int xs, shift;          // keys x >= xs of the item are positions x + shift (a multiple of the block size)
@@ -458,8 +464,7 @@ __device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfWindo
   it.n = __ldg(p.query_start + it.s + 1) - it.q0;
   it.L = __ldg(p.seq_lens + it.s);
   const int B = p.block_size;
-  if (it.q0 < 0 || it.n < 0 || (long long)it.q0 + it.n > p.num_query_tokens || it.n > p.max_query_len ||
-      it.L < it.n || (long long)it.L > (long long)p.max_blocks * B) {
+  if (pf_bad_chunk(p, it)) {
     if (report && qt == 0 && it.h == 0) report_error(p.err_flag, PA_DEVERR_QUERY);
     return false;
   }
@@ -486,6 +491,9 @@ struct PfSplitItem : PfWindowItem {
   int first;
 };
 
+// Mixed batches: see pf_skip.
+struct PfMixedItem : PfWindowItem {};
+
 __device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfSplitItem& it, bool report) {
   if (!pf_item(p, idx, static_cast<PfWindowItem&>(it), report)) return false;
   // a CTA without a tile takes one past the end, of which its rows see nothing
@@ -494,6 +502,24 @@ __device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfSplit
   it.key_tiles = (int)((long long)all * (rank + 1) / p.split) - it.first;
   if (it.key_tiles == 0) it.first = all, it.key_tiles = 1;
   return true;
+}
+
+// A walk over the items idx, idx + step, ... takes the next one after an item without queries.
+__device__ __forceinline__ int pf_skip(const PrefillParams&, int, int, const PfItem&, bool) { return 0; }
+// A batch that mixes a long chunk with many short ones has almost none but such items, and a step over each (some 0.6
+// us) adds up: to more than the waits of the other roles last (a quarter of a second) at a thousand sequences and a
+// chunk of 128 thousand tokens, 64 / 8 heads.  Those of a sequence come first among its items and are passed over at
+// once here: what to add to idx before its next step.  (A form of its own: over chunks of 256-1024 tokens, W = 1024,
+// it costs 1 to 3 %.)
+__device__ __forceinline__ int pf_skip(const PrefillParams& p, int idx, int step, const PfMixedItem& it, bool report) {
+  const int groups = p.num_q_heads >> p.pack_log2, per_seq = p.q_tiles * groups;
+  int tiles = 0;
+  if (!pf_bad_chunk(p, it))
+    tiles = (it.n + (kTile >> p.pack_log2) - 1) >> (7 - p.pack_log2);
+  else if (report)  // by the walk that has the sequence's first item, and perhaps by others
+    report_error(p.err_flag, PA_DEVERR_QUERY);
+  const int empty = it.s * per_seq + (p.q_tiles - tiles) * groups - idx;  // items from idx on without queries
+  return (empty - 1) / step * step;
 }
 __device__ __forceinline__ int first_tile(const PfItem&) { return 0; }
 __device__ __forceinline__ int first_tile(const PfSplitItem& it) { return it.first; }
@@ -578,7 +604,10 @@ __device__ __forceinline__ void fp8_producer(const PrefillParams& p, int w, int 
   bool ok = true;
   for (int idx = idx0; ok && idx < n_items; idx += idx_step) {
     Item it;
-    if (!pf_item(p, idx, it, false)) continue;
+    if (!pf_item(p, idx, it, false)) {
+      idx += pf_skip(p, idx, idx_step, it, false);
+      continue;
+    }
     const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
     // lane b < blocks_per_tile: the table entry of the tile's block b
     auto fetch = [&](int kt) -> int {
@@ -694,8 +723,8 @@ __device__ __forceinline__ void split_merge(const PrefillParams& p, const float*
   cluster_sync_all();  // no CTA leaves while another reads its rows
 }
 
-// kWindow: see the file comment; kSplit: windowed, a cluster of p.split CTAs an item
-enum class PfForm { kPlain, kWindow, kSplit };
+// kWindow: see the file comment; kSplit: windowed, a cluster of p.split CTAs an item; kMixed: windowed, see pf_skip
+enum class PfForm { kPlain, kWindow, kSplit, kMixed };
 
 // Persistent: each CTA takes items blockIdx.x, blockIdx.x + gridDim.x, ...  Every role walks the same
 // items; the K/V rings, the S buffers and their barriers run on across items (tg counts this CTA's
@@ -710,8 +739,9 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
   constexpr bool kWindow = kForm != PfForm::kPlain, kSplit = kForm == PfForm::kSplit;
   constexpr int kHalves = D / 64;  // 64-column halves of a row
   static_assert(D == 128 || (D == 64 && kWindow && !kFp8), "head size");
-  using Item = typename std::conditional<kSplit, PfSplitItem,
-                                         typename std::conditional<kWindow, PfWindowItem, PfItem>::type>::type;
+  using Item = std::conditional_t<
+      kSplit, PfSplitItem,
+      std::conditional_t<kForm == PfForm::kMixed, PfMixedItem, std::conditional_t<kWindow, PfWindowItem, PfItem>>>;
   // split: the CTAs of a cluster take the same items
   const int idx0 = kSplit ? blockIdx.x / (unsigned)p.split : blockIdx.x;
   const int idx_step = kSplit ? gridDim.x / (unsigned)p.split : gridDim.x;
@@ -803,7 +833,10 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     int tg = 0;
     for (int idx = idx0; ok && idx < n_items; idx += idx_step) {
       Item it;
-      if (!pf_item(p, idx, it, false)) continue;
+      if (!pf_item(p, idx, it, false)) {
+        idx += pf_skip(p, idx, idx_step, it, false);
+        continue;
+      }
       const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
       // the table entry of this lane's block, read one tile ahead
       auto fetch = [&](int kt) -> int {
@@ -879,10 +912,12 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       // idx) in items[k % 2] and starts the copy of its Q tile into Q buffer k % 2, both completing
       // phase k of bar_qs.  Item k + 1 is published once every softmax warp has read item k (bar_q
       // phase k), which also means the S MMAs of item k - 1, the last readers of that Q buffer, have
-      // finished.  It reports inconsistent chunks: every item of this CTA passes through here once.
+      // finished.  It reports inconsistent chunks: this CTA's walk over the items passes through here once.
       auto publish = [&](int idx, int k, Item& it) {
-        for (; idx < n_items; idx += idx_step)
+        for (; idx < n_items; idx += idx_step) {
           if (pf_item(p, idx, it, true)) break;
+          idx += pf_skip(p, idx, idx_step, it, true);
+        }
         if (idx >= n_items) it.s = -1;
         items[k & 1] = it;
         ++n_pub;
@@ -963,7 +998,10 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       };
       for (int idx = idx0; ok && idx < n_items; idx += idx_step) {
         Item it;
-        if (!pf_item(p, idx, it, false)) continue;
+        if (!pf_item(p, idx, it, false)) {
+          idx += pf_skip(p, idx, idx_step, it, false);
+          continue;
+        }
         // the first P V overwrites O: the previous item's epilogue must have read it (the barrier's
         // next phase is this item's epilogue, which needs these MMAs, so the wait is exact)
         if (item_no > 0) ok = wait_bar_spin(bar_ofree, (item_no - 1) & 1, abort_flag);
@@ -1377,26 +1415,27 @@ static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, 
 
 template <typename T, bool kFp8, int D>
 static cudaError_t launch_window(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
-                                 const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
+                                 const CUtensorMap& to, const PrefillParams& p, bool mixed, cudaStream_t stream) {
   return p.split > 1 ? launch_prefill<T, PfForm::kSplit, kFp8, D>(tk, tv, tq, to, p, stream)
+         : mixed     ? launch_prefill<T, PfForm::kMixed, kFp8, D>(tk, tv, tq, to, p, stream)
                      : launch_prefill<T, PfForm::kWindow, kFp8, D>(tk, tv, tq, to, p, stream);
 }
 
 cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
-                              const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
+                              const CUtensorMap& to, const PrefillParams& p, bool mixed, cudaStream_t stream) {
   const bool window = p.window > 0;
   if (p.head_size == 64) {
-    if (dtype == PA_F16 && window) return launch_window<__half, false, 64>(tk, tv, tq, to, p, stream);
-    if (dtype == PA_BF16 && window) return launch_window<__nv_bfloat16, false, 64>(tk, tv, tq, to, p, stream);
+    if (dtype == PA_F16 && window) return launch_window<__half, false, 64>(tk, tv, tq, to, p, mixed, stream);
+    if (dtype == PA_BF16 && window) return launch_window<__nv_bfloat16, false, 64>(tk, tv, tq, to, p, mixed, stream);
     return cudaErrorInvalidValue;
   }
   if (dtype == PA_F16)
-    return window ? launch_window<__half, false, 128>(tk, tv, tq, to, p, stream)
+    return window ? launch_window<__half, false, 128>(tk, tv, tq, to, p, mixed, stream)
                   : launch_prefill<__half, PfForm::kPlain>(tk, tv, tq, to, p, stream);
   if (dtype == PA_BF16)
-    return window ? launch_window<__nv_bfloat16, false, 128>(tk, tv, tq, to, p, stream)
+    return window ? launch_window<__nv_bfloat16, false, 128>(tk, tv, tq, to, p, mixed, stream)
                   : launch_prefill<__nv_bfloat16, PfForm::kPlain>(tk, tv, tq, to, p, stream);
-  if (dtype == PA_FP8_E4M3 && window) return launch_window<__half, true, 128>(tk, tv, tq, to, p, stream);
+  if (dtype == PA_FP8_E4M3 && window) return launch_window<__half, true, 128>(tk, tv, tq, to, p, mixed, stream);
   return cudaErrorInvalidValue;
 }
 

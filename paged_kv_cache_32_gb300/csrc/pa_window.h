@@ -23,7 +23,7 @@ struct WindowParams {
   int32_t num_query_tokens;     // rows of q and out
   int32_t max_query_len;        // bound on a sequence's queries (1 without query_start)
   int32_t window, sinks;        // >= 1, >= 0
-  int32_t tiles;                // row groups (8 rows) or query tiles of a sequence's kv head in the grid
+  int32_t tiles;                // row groups (8 rows) of a kv head in the grid: each sequence's, or (slots) all of theirs
   int32_t cluster;              // rows kernels: CTAs that share one item's keys,
   int32_t warps;                // and warps of a CTA (3, 4 or 6; fp32: 4)
   float scale_log2;             // scale * log2(e)
@@ -82,11 +82,14 @@ cudaError_t prepare_rows(Kernel kernel, ClusterRoom& room, int threads, size_t s
 }
 
 // items of a rows launch: eight query rows of one kv head each
-inline long long window_items(const WindowParams& p) { return (long long)p.num_seqs * p.num_kv_heads * p.tiles; }
+inline long long window_items(const WindowParams& p, bool slots) {
+  return (long long)(slots ? 1 : p.num_seqs) * p.num_kv_heads * p.tiles;
+}
 
+// slots: the sequences' row groups lie one after the other in p.tiles slots (see rows_find)
 cudaError_t launch_window_rows_tc(int dtype, int head_size, const CUtensorMap& tk, const CUtensorMap& tv,
-                                  const WindowParams& p, cudaStream_t stream);
-cudaError_t launch_window_rows_fp8(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p,
+                                  const WindowParams& p, bool slots, cudaStream_t stream);
+cudaError_t launch_window_rows_fp8(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p, bool slots,
                                    cudaStream_t stream);
-cudaError_t launch_window_rows_f32(int head_size, const WindowParams& p, cudaStream_t stream);
+cudaError_t launch_window_rows_f32(int head_size, const WindowParams& p, bool slots, cudaStream_t stream);
 }  // namespace pa

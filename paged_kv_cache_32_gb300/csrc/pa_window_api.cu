@@ -19,6 +19,7 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kMaxCluster = pa::kPortableCluster;  // (rows kernels also take the largest, twice that, where it fits)
 constexpr int kMinCtaTokens = 64;  // tokens of a CTA below which a split no longer pays
+constexpr int kFewItems = 4096;    // work items whose empty ones cost a few microseconds at most
 constexpr int kLongShare = 600;    // fp32: tokens of a CTA that is split though every SM has its CTAs
 
 // How the rows kernels spread over the SMs.  A warp holds 16 KB of slabs, so an SM takes 4 CTAs of 3 warps, 3 of 4
@@ -112,33 +113,46 @@ bool encode_slab_map(CUtensorMap* map, const void* base, const pa_cache_desc* c,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Does a batch mix long chunks with many short ones, so that most items of a grid of `items` (the longest chunk's for
+// every sequence) have no queries, when at most `real` have?  The forms for such batches pay for their search: a rows
+// CTA about what two or three empty ones do.  A prompt of P among N - 1 single tokens, 64 / 8 heads, W = 1024, us with
+// these forms and with the others: tiles, bf16, N = 32, P = 512 86 / 87, N = 128, P = 2048 285 / 624, N = 1024, P = 4096
+// 1620 / 7890; fp32 rows 602 / 718, 2845 / 5120, 7080 / 46200.
+bool mixes(long long items, long long real) { return items > kFewItems && items > 4 * real; }
+
 // Launches the rows kernel of the cache's type; p.tiles (row groups), p.cluster and p.warps are set here.
 int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t stream) {
   const long long rows = (long long)p.max_query_len * (p.num_q_heads / p.num_kv_heads);
   if (rows > kInt32Max - 8) return PA_ERR_TOO_LARGE;
   p.tiles = (int32_t)((rows + 7) / 8);
+  bool slots = false;
+  if (p.query_start != nullptr) {
+    const long long real = (long long)p.num_query_tokens * (p.num_q_heads / p.num_kv_heads) / 8 + p.num_seqs;
+    slots = real <= kInt32Max && mixes(pa::window_items(p, false), real * p.num_kv_heads);
+    if (slots) p.tiles = (int32_t)real;
+  }
   // keys that an item may see: its rows' windows, the first tokens, all within the table
   const long long cap = (long long)p.max_blocks * p.block_size;
   const long long reach = (long long)p.window + p.sinks + 8;
-  const long long items = pa::window_items(p);
+  const long long items = pa::window_items(p, slots);
   spread(cache->dtype, items, reach < cap ? reach : cap, p);
   if (items * p.cluster > kInt32Max) return PA_ERR_TOO_LARGE;
   cudaError_t e;
   if (cache->dtype == PA_F32) {
-    e = pa::launch_window_rows_f32(cache->head_size, p, stream);
+    e = pa::launch_window_rows_f32(cache->head_size, p, slots, stream);
   } else if (cache->dtype == PA_FP8_E4M3) {
     CUtensorMap tk, tk32;
     if (!encode_fp8_key_map(&tk, p.k_cache, cache, pa::kTcSlabTokens) ||
         !encode_fp8_key_map(&tk32, p.k_cache, cache, 2 * pa::kTcSlabTokens))
       return PA_ERR_CUDA;
-    e = pa::launch_window_rows_fp8(tk, tk32, p, stream);
+    e = pa::launch_window_rows_fp8(tk, tk32, p, slots, stream);
   } else {
     CUtensorMap tk, tv;
     // a slab is one 16-row box, or (8-token blocks) two 8-row boxes from two blocks
     const int box_rows = cache->block_size < pa::kTcSlabTokens ? cache->block_size : pa::kTcSlabTokens;
     if (!encode_slab_map(&tk, p.k_cache, cache, box_rows) || !encode_slab_map(&tv, p.v_cache, cache, box_rows))
       return PA_ERR_CUDA;
-    e = pa::launch_window_rows_tc(cache->dtype, cache->head_size, tk, tv, p, stream);
+    e = pa::launch_window_rows_tc(cache->dtype, cache->head_size, tk, tv, p, slots, stream);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -185,10 +199,14 @@ bool tiles_faster(const pa_cache_desc* cache, pa::WindowParams p, int pack) {
   return tile_us < rows_us;
 }
 
-int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack, cudaStream_t stream) {
+// the tile kernel's work items: the longest chunk's tiles for every sequence and head group
+long long tile_items(const pa::WindowParams& w, int pack) {
   const long long q_tiles = ((long long)w.max_query_len + (128 >> pack) - 1) / (128 >> pack);
-  // work items are counted in int32, with room for one grid stride past the end
-  if ((long long)w.num_seqs * (w.num_q_heads >> pack) * q_tiles > kInt32Max - 4096) return PA_ERR_TOO_LARGE;
+  return w.num_seqs * q_tiles * (w.num_q_heads >> pack);
+}
+
+int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack, cudaStream_t stream) {
+  const long long items = tile_items(w, pack);
   CUtensorMap tk, tv, tq, to;
   const bool fp8 = cache->dtype == PA_FP8_E4M3;  // read by plain loads
   if ((!fp8 && (!encode_cache_map(&tk, w.k_cache, cache, cache->block_size) ||
@@ -212,7 +230,7 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   p.block_size = w.block_size;
   p.num_blocks = w.num_blocks;
   p.head_size = cache->head_size;
-  p.q_tiles = (int32_t)q_tiles;
+  p.q_tiles = (int32_t)(items / w.num_seqs / (w.num_q_heads >> pack));
   p.num_query_tokens = w.num_query_tokens;
   p.scale_log2 = w.scale_log2 * w.k_scale;
   p.v_scale = w.v_scale;
@@ -220,10 +238,11 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   p.sinks = w.sinks;
   p.pack_log2 = pack;
   p.max_query_len = w.max_query_len;
-  p.split = tile_split((long long)w.num_seqs * (w.num_q_heads >> pack) * q_tiles,
-                       std::min((long long)w.max_blocks * w.block_size, (long long)w.window + w.sinks + 128));
+  const bool mixed =
+      mixes(items, ((long long)w.num_query_tokens / (128 >> pack) + w.num_seqs) * (w.num_q_heads >> pack));
+  p.split = tile_split(items, std::min((long long)w.max_blocks * w.block_size, (long long)w.window + w.sinks + 128));
   if (fp8) tk = tv = tq;
-  return pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, mixed, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa::WindowParams base_params(const pa_cache_desc* cache, void* out, const void* q, const void* k_cache,
@@ -323,7 +342,8 @@ int pa_prefill_window(void* out, const void* q, const void* k_cache, const void*
   p.num_query_tokens = num_query_tokens;
   p.max_query_len = std::min(max_query_len, num_query_tokens);  // no valid chunk is longer
   const int pack = pack_log2(num_q_heads / cache->num_kv_heads);
-  if (tile_kernel_takes(cache) && tiles_faster(cache, p, pack))
+  // (the tile kernel counts its items in int32, with room for one grid stride past the end; the rows kernels' slots fit)
+  if (tile_kernel_takes(cache) && tile_items(p, pack) <= kInt32Max - 4096 && tiles_faster(cache, p, pack))
     return launch_tiles(cache, p, pack, static_cast<cudaStream_t>(stream));
   return launch_rows(cache, p, static_cast<cudaStream_t>(stream));
 }

@@ -51,35 +51,100 @@ struct RowsItem {
   bool empty;           // a decode row of an empty sequence: zeros
 };
 
+// The queries of sequence s: q rows q0 .. q0 + n - 1, the last of L tokens.  bad: a chunk outside q / out, longer than
+// the caller's bound or than its sequence, or a sequence past its table.
+struct RowsChunk {
+  int q0, n, L;
+  bool bad;
+};
+__device__ __forceinline__ RowsChunk rows_chunk(const WindowParams& p, int s) {
+  RowsChunk c = {s, 1, __ldg(p.seq_lens + s), false};
+  c.bad = c.L < 0 || (long long)c.L > (long long)p.max_blocks * p.block_size;
+  if (p.query_start != nullptr) {
+    c.q0 = __ldg(p.query_start + s);
+    const long long len = (long long)__ldg(p.query_start + s + 1) - c.q0;
+    c.bad = c.bad || c.q0 < 0 || len < 0 || c.q0 + len > p.num_query_tokens || len > p.max_query_len || c.L < len;
+    c.n = (int)len;
+  }
+  return c;
+}
+
+// Slots (batches that mix long chunks with many short ones): the row groups of all sequences lie one after the other,
+// so the grid holds no more than the rows of q fill and one a sequence, where the longest chunk's groups for every
+// sequence would be mostly empty (1024 sequences, a chunk of 4096 among single tokens: 33.5 million items of which 41
+// thousand exist, and past 2^31 no grid at all).  The CTA's threads add up the sequences' groups, each over a run of
+// them, and find the one whose group lies in `slot`.  False: none does.  Called by all threads; sums: 8 + 1 numbers of
+// shared memory, free again after the next barrier.  Chunks that overlap may need more slots than there are: reported.
+__device__ __forceinline__ bool rows_find(const WindowParams& p, int slot, long long* sums, bool report, int& s,
+                                          int& rg) {
+  const int G = p.num_q_heads / p.num_kv_heads, threads = (int)blockDim.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long run = (p.num_seqs + threads - 1) / threads;
+  const int begin = (int)min((long long)p.num_seqs, run * threadIdx.x);
+  const int end = (int)min((long long)p.num_seqs, run * (threadIdx.x + 1));
+  auto groups = [&](const RowsChunk& c) {
+    return c.bad ? 0 : (int)(((long long)c.n * G + kRowsGroup - 1) / kRowsGroup);
+  };
+  long long mine = 0;
+  for (int i = begin; i < end; ++i) {
+    const RowsChunk c = rows_chunk(p, i);
+    if (c.bad && report) report_error(p.err_flag, PA_DEVERR_QUERY);
+    mine += groups(c);
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += x;
+  }
+  int* found = reinterpret_cast<int*>(sums + 8);
+  if (lane == 31) sums[warp] = upto;
+  if (threadIdx.x == 0) found[0] = -1;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += sums[w];
+  if (report && threadIdx.x == threads - 1 && upto > p.tiles) report_error(p.err_flag, PA_DEVERR_QUERY);
+  long long at = upto - mine;
+  if (slot >= at && slot < upto) {
+    int i = begin;
+    for (int n; (n = groups(rows_chunk(p, i))) <= slot - at; ++i) at += n;
+    found[0] = i;
+    found[1] = (int)(slot - at);
+  }
+  __syncthreads();
+  s = found[0];
+  rg = found[1];
+  return s >= 0;
+}
+
 // The item of this CTA's cluster and the CTA's share of its slabs (SB tokens each).  False: nothing to do (the
-// same for every CTA of the cluster).  A chunk outside q / out, longer than the grid covers or than its
-// sequence, or a sequence past its table is reported by the sequence's first item, and nothing of it is done.
-template <int SB>
-__device__ __forceinline__ bool rows_item(const WindowParams& p, RowsItem& it) {
+// same for every CTA of the cluster).  A bad chunk is reported once, and nothing of it is done.  Called by all
+// threads.  SLOTS: the row groups lie in p.tiles slots, sums as for rows_find (a form of its own: with the choice at run
+// time the fp32 kernel kept 130 registers for 157 and lost 5 %).
+template <int SB, bool SLOTS>
+__device__ __forceinline__ bool rows_item(const WindowParams& p, RowsItem& it, long long* sums) {
   const int C = p.cluster;
   const int rank = (int)(blockIdx.x % (unsigned)C);
-  int id = (int)(blockIdx.x / (unsigned)C);
-  const int rg = id % p.tiles;
-  id /= p.tiles;
-  it.hkv = id % p.num_kv_heads;
-  it.s = id / p.num_kv_heads;
+  int id = (int)(blockIdx.x / (unsigned)C), rg;
+  if constexpr (SLOTS) {
+    it.hkv = id % p.num_kv_heads;
+    id /= p.num_kv_heads;
+    if (!rows_find(p, id, sums, id == 0 && it.hkv == 0 && rank == 0, it.s, rg)) return false;
+  } else {
+    rg = id % p.tiles;
+    id /= p.tiles;
+    it.hkv = id % p.num_kv_heads;
+    it.s = id / p.num_kv_heads;
+  }
   it.G = p.num_q_heads / p.num_kv_heads;
   it.row0 = rg * kRowsGroup;
   it.empty = false;
-  const int L = __ldg(p.seq_lens + it.s);
-  int n = 1;
-  it.q0 = it.s;
-  bool bad = L < 0 || (long long)L > (long long)p.max_blocks * p.block_size;
-  if (p.query_start != nullptr) {
-    it.q0 = __ldg(p.query_start + it.s);
-    const long long len = (long long)__ldg(p.query_start + it.s + 1) - it.q0;
-    bad = bad || it.q0 < 0 || len < 0 || it.q0 + len > p.num_query_tokens || len > p.max_query_len || L < len;
-    n = (int)len;
-  }
-  if (bad) {
+  const RowsChunk chunk = rows_chunk(p, it.s);
+  if (chunk.bad) {
     if (rg == 0 && it.hkv == 0 && rank == 0 && threadIdx.x == 0) report_error(p.err_flag, PA_DEVERR_QUERY);
     return false;
   }
+  const int L = chunk.L, n = chunk.n;
+  it.q0 = chunk.q0;
   it.L = L;
   it.gcount = min((long long)kRowsGroup, (long long)n * it.G - it.row0);
   if (it.gcount <= 0) return false;
@@ -134,8 +199,8 @@ __device__ __forceinline__ void rows_zero(const WindowParams& p, const RowsItem&
 // and then (m, l)[8 rows] (max score in log2 units, sum of 2^(s - m)).  With m* = max m and weights
 // 2^(m - m*), O = sum weight O and l = sum weight l over the warps, then in the same way over the CTAs of the
 // cluster, whose results sit in each CTA's `mine` (8 x D floats, then 8 pairs); each CTA writes its share of
-// the output elements: O / l, zeros where l is 0 (no weight), NaN where a score was NaN (l is).  Called by every thread after the barrier that follows the warps' stores; wt: 8 * NW
-// + 16 floats apart from the parts.
+// the output elements: O / l, zeros where l is 0 (no weight), NaN where a score was NaN (l is).  Called by every
+// thread after the barrier that follows the warps' stores; wt: 8 * NW + 16 floats apart from the parts.
 template <typename TOut, int D, int NW, int OROW, int STRIDE>
 __device__ __forceinline__ void rows_finish(const WindowParams& p, const RowsItem& it, const float* parts, float* wt,
                                             float* mine) {

@@ -49,18 +49,18 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-template <int D>
+template <int D, bool SLOTS>
 __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const WindowParams p) {
   constexpr int VEC = D / 32, OROW = D, STRIDE = 8 * D + 16;
   constexpr int STEP = 8 * D;  // floats of a step: four rows of K, then of V
   // [warp][step of the ring][K: token 0..3, V: token 0..3][D]; at the end a warp's partial result
   extern __shared__ __align__(16) float ring_all[];
-  __shared__ float wt[8 * kF32Warps + 16];
+  __shared__ __align__(16) float wt[8 * kF32Warps + 16];
   __shared__ float mine[8 * D + 16];
   static_assert(kRing * STEP >= STRIDE, "a warp's ring holds its partial result");
   griddep_begin();
   RowsItem it;
-  if (!rows_item<kF32Slab>(p, it)) return;
+  if (!rows_item<kF32Slab, SLOTS>(p, it, reinterpret_cast<long long*>(wt))) return;
   if (it.empty) {
     rows_zero<float, D>(p, it);
     return;
@@ -223,22 +223,22 @@ __global__ void __launch_bounds__(kF32Warps * 32) window_rows_f32_kernel(const W
   rows_finish<float, D, kF32Warps, OROW, kRing * STEP>(p, it, ring_all, wt, mine);
 }
 
-template <int D>
-cudaError_t launch_f32(WindowParams p, cudaStream_t stream) {
-  auto kernel = window_rows_f32_kernel<D>;
+template <int D, bool SLOTS>
+cudaError_t launch_form(WindowParams p, cudaStream_t stream) {
+  auto kernel = window_rows_f32_kernel<D, SLOTS>;
   constexpr size_t kSmem = (size_t)kF32Warps * kRing * 8 * D * sizeof(float);
   static ClusterRoom room;
   cudaError_t e = prepare_rows(kernel, room, kF32Warps * 32, kSmem, &p.cluster);
   if (e != cudaSuccess) return e;
-  return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(kF32Warps * 32), kSmem, p.cluster,
+  return launch_cluster(kernel, dim3((unsigned)(window_items(p, SLOTS) * p.cluster)), dim3(kF32Warps * 32), kSmem, p.cluster,
                         true, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_window_rows_f32(int head_size, const WindowParams& p, cudaStream_t stream) {
-  if (head_size == 64) return launch_f32<64>(p, stream);
-  if (head_size == 128) return launch_f32<128>(p, stream);
+cudaError_t launch_window_rows_f32(int head_size, const WindowParams& p, bool slots, cudaStream_t stream) {
+  if (head_size == 64) return slots ? launch_form<64, true>(p, stream) : launch_form<64, false>(p, stream);
+  if (head_size == 128) return slots ? launch_form<128, true>(p, stream) : launch_form<128, false>(p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -148,7 +148,7 @@ __device__ __forceinline__ uint32_t quantise4(uint2 h, float scale) {
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-template <int D, int NW, int NS>
+template <int D, int NW, int NS, bool SLOTS>
 __global__ void __launch_bounds__(RowsFp8Shape<D, NW, NS>::THREADS)
     window_rows_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_k32,
                            const WindowParams p) {
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(RowsFp8Shape<D, NW, NS>::THREADS)
   __syncthreads();
   griddep_begin();
   RowsItem it;
-  if (!rows_item<S::SB>(p, it)) return;
+  if (!rows_item<S::SB, SLOTS>(p, it, reinterpret_cast<long long*>(smem + S::WT_OFF))) return;
   if (it.empty) {
     rows_zero<__half, D>(p, it);
     return;
@@ -352,22 +352,28 @@ __global__ void __launch_bounds__(RowsFp8Shape<D, NW, NS>::THREADS)
 
 }  // namespace
 
-template <int NW>
-static cudaError_t launch_warps(const CUtensorMap& tk, const CUtensorMap& tk32, WindowParams p, cudaStream_t stream) {
+template <int NW, bool SLOTS>
+static cudaError_t launch_form(const CUtensorMap& tk, const CUtensorMap& tk32, WindowParams p, cudaStream_t stream) {
   using S = RowsFp8Shape<128, NW, 2>;
-  auto kernel = window_rows_fp8_kernel<128, NW, 2>;
+  auto kernel = window_rows_fp8_kernel<128, NW, 2, SLOTS>;
   static ClusterRoom room;
   cudaError_t e = prepare_rows(kernel, room, S::THREADS, S::SMEM_BYTES, &p.cluster);
   if (e != cudaSuccess) return e;
-  return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
+  return launch_cluster(kernel, dim3((unsigned)(window_items(p, SLOTS) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
                         p.cluster, true, stream, tk, tk32, p);
 }
 
-cudaError_t launch_window_rows_fp8(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p,
+template <int NW>
+static cudaError_t launch_warps(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p, bool slots,
+                                cudaStream_t stream) {
+  return slots ? launch_form<NW, true>(tk, tk32, p, stream) : launch_form<NW, false>(tk, tk32, p, stream);
+}
+
+cudaError_t launch_window_rows_fp8(const CUtensorMap& tk, const CUtensorMap& tk32, const WindowParams& p, bool slots,
                                    cudaStream_t stream) {
-  if (p.warps == 3) return launch_warps<3>(tk, tk32, p, stream);
-  if (p.warps == 4) return launch_warps<4>(tk, tk32, p, stream);
-  if (p.warps == 6) return launch_warps<6>(tk, tk32, p, stream);
+  if (p.warps == 3) return launch_warps<3>(tk, tk32, p, slots, stream);
+  if (p.warps == 4) return launch_warps<4>(tk, tk32, p, slots, stream);
+  if (p.warps == 6) return launch_warps<6>(tk, tk32, p, slots, stream);
   return cudaErrorInvalidValue;
 }
 

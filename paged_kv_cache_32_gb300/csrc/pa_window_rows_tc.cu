@@ -135,7 +135,7 @@ __device__ __forceinline__ void window_slab(const uint8_t* kst, const uint8_t* v
   }
 }
 
-template <typename T, int D, int NW, int NS, bool SPLIT>
+template <typename T, int D, int NW, int NS, bool SPLIT, bool SLOTS>
 __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
     window_rows_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                           const WindowParams p) {
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
   __syncthreads();
   griddep_begin();
   RowsItem it;
-  if (!rows_item<S::SB>(p, it)) return;
+  if (!rows_item<S::SB, SLOTS>(p, it, reinterpret_cast<long long*>(smem + S::WT_OFF))) return;
   if (it.empty) {
     rows_zero<T, D>(p, it);
     return;
@@ -333,43 +333,53 @@ __global__ void __launch_bounds__(RowsShape<D, NW, NS>::THREADS)
                                                     reinterpret_cast<float*>(smem + S::MINE_OFF));
 }
 
-template <typename T, int D, int NW, int NS, bool SPLIT>
-cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, WindowParams p, cudaStream_t stream) {
+template <typename T, int D, int NW, int NS, bool SPLIT, bool SLOTS>
+cudaError_t launch_form(const CUtensorMap& tk, const CUtensorMap& tv, WindowParams p, cudaStream_t stream) {
   using S = RowsShape<D, NW, NS>;
-  auto kernel = window_rows_tc_kernel<T, D, NW, NS, SPLIT>;
+  auto kernel = window_rows_tc_kernel<T, D, NW, NS, SPLIT, SLOTS>;
   static ClusterRoom room;
   cudaError_t e = prepare_rows(kernel, room, S::THREADS, S::SMEM_BYTES, &p.cluster);
   if (e != cudaSuccess) return e;
-  return launch_cluster(kernel, dim3((unsigned)(window_items(p) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
+  return launch_cluster(kernel, dim3((unsigned)(window_items(p, SLOTS) * p.cluster)), dim3(S::THREADS), S::SMEM_BYTES,
                         p.cluster, true, stream, tk, tv, p);
 }
 
+template <typename T, int D, int NW, int NS, bool SPLIT>
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const WindowParams& p, bool slots,
+                        cudaStream_t stream) {
+  return slots ? launch_form<T, D, NW, NS, SPLIT, true>(tk, tv, p, stream)
+               : launch_form<T, D, NW, NS, SPLIT, false>(tk, tv, p, stream);
+}
+
 template <typename T, int D, int NS, bool SPLIT>
-cudaError_t launch_warps(const CUtensorMap& tk, const CUtensorMap& tv, const WindowParams& p, cudaStream_t stream) {
-  if (p.warps == 3) return launch_rows<T, D, 3, NS, SPLIT>(tk, tv, p, stream);
-  if (p.warps == 4) return launch_rows<T, D, 4, NS, SPLIT>(tk, tv, p, stream);
-  if (p.warps == 6) return launch_rows<T, D, 6, NS, SPLIT>(tk, tv, p, stream);
+cudaError_t launch_warps(const CUtensorMap& tk, const CUtensorMap& tv, const WindowParams& p, bool slots,
+                         cudaStream_t stream) {
+  if (p.warps == 3) return launch_rows<T, D, 3, NS, SPLIT>(tk, tv, p, slots, stream);
+  if (p.warps == 4) return launch_rows<T, D, 4, NS, SPLIT>(tk, tv, p, slots, stream);
+  if (p.warps == 6) return launch_rows<T, D, 6, NS, SPLIT>(tk, tv, p, slots, stream);
   return cudaErrorInvalidValue;
 }
 
 // two slabs a warp (four of head size 64): a deeper ring leaves fewer warps an SM and gained nothing
 template <typename T>
 cudaError_t launch_type(int head_size, const CUtensorMap& tk, const CUtensorMap& tv, const WindowParams& p,
-                        cudaStream_t stream) {
+                        bool slots, cudaStream_t stream) {
   const bool split = p.block_size < kTcSlabTokens;
   if (head_size == 128)
-    return split ? launch_warps<T, 128, 2, true>(tk, tv, p, stream) : launch_warps<T, 128, 2, false>(tk, tv, p, stream);
+    return split ? launch_warps<T, 128, 2, true>(tk, tv, p, slots, stream)
+                 : launch_warps<T, 128, 2, false>(tk, tv, p, slots, stream);
   if (head_size == 64)
-    return split ? launch_warps<T, 64, 4, true>(tk, tv, p, stream) : launch_warps<T, 64, 4, false>(tk, tv, p, stream);
+    return split ? launch_warps<T, 64, 4, true>(tk, tv, p, slots, stream)
+                 : launch_warps<T, 64, 4, false>(tk, tv, p, slots, stream);
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_window_rows_tc(int dtype, int head_size, const CUtensorMap& tk, const CUtensorMap& tv,
-                                  const WindowParams& p, cudaStream_t stream) {
-  if (dtype == PA_F16) return launch_type<__half>(head_size, tk, tv, p, stream);
-  if (dtype == PA_BF16) return launch_type<__nv_bfloat16>(head_size, tk, tv, p, stream);
+                                  const WindowParams& p, bool slots, cudaStream_t stream) {
+  if (dtype == PA_F16) return launch_type<__half>(head_size, tk, tv, p, slots, stream);
+  if (dtype == PA_BF16) return launch_type<__nv_bfloat16>(head_size, tk, tv, p, slots, stream);
   return cudaErrorInvalidValue;
 }
 

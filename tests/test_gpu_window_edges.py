@@ -118,3 +118,102 @@ def test_prefill_window_nan_is_not_hidden(dtype, form):
             assert sees.any() and (what == "first key" or not sees.all() or n <= 2)
         s.prefill()
         check_nan_rows(s, ref, nan)
+
+
+# ---------------------------------------------------------------- batches that mix chunk lengths
+def mixed(dtype, d, block_size, hq, hkv, n=70, prompt=700, seed=0):
+    """n sequences of single tokens, one among them with a prompt, a few with two to nine tokens or none."""
+    rng = np.random.default_rng(seed)
+    chunks = [1] * n
+    chunks[n // 3] = prompt
+    for s in range(5, n, 11):
+        chunks[s] = int(rng.integers(0, 10))
+    lens = [c + int(x) for c, x in zip(chunks, rng.integers(0, 300, n))]
+    return WindowCase(dtype, lens, chunks, hq, hkv, d, block_size, 130, 4, seed=seed)
+
+
+# (block sizes that do not divide 128 and fp32 caches go to the rows kernels, in slots)
+MIXED = [("f16", 128, 16, 8, 2), ("bf16", 128, 32, 12, 2), ("bf16", 64, 16, 8, 1), ("fp8", 128, 16, 8, 2),
+         ("f16", 64, 48, 8, 2), ("bf16", 128, 48, 12, 2), ("fp8", 128, 48, 8, 1), ("f32", 64, 16, 14, 2),
+         ("f32", 128, 5, 4, 4)]
+
+
+@pytest.mark.parametrize("dtype,d,block_size,hq,hkv", MIXED)
+def test_prefill_window_mixed_batch(dtype, d, block_size, hq, hkv):
+    """Single tokens, short chunks, empty ones and a prompt in one call."""
+    import torch
+    from test_gpu_window import check
+    w = mixed(dtype, d, block_size, hq, hkv)
+    s = Step(w)
+    s.prefill()
+    check(s, w.reference(), "mixed")
+    # a looser bound on the chunks: the same rows
+    t = Step(w)
+    pad = torch.zeros((4000, hq, d), dtype=t.q.dtype, device="cuda")
+    t.q, t.out = torch.cat([t.q, pad]), torch.cat([t.out, pad + 123.0])
+    t.prefill(max_query_len=4000 + s.q.shape[0])
+    n = s.q.shape[0]  # (rows past the last chunk keep what they held)
+    assert int(t.err.item()) == 0 and torch.all(t.out[n:] == 123.0)
+    t.out = t.out[:n].contiguous()
+    check(t, w.reference(), "mixed, loose bound")
+
+
+@pytest.mark.parametrize("dtype,d,block_size,hq,hkv", MIXED)
+def test_prefill_window_mixed_batch_bad_chunks(dtype, d, block_size, hq, hkv):
+    """Inconsistent chunks of a mixed batch are reported and skipped, wherever they stand; the others are right."""
+    import torch
+    from harness import out_f64, within_bound
+    w = mixed(dtype, d, block_size, hq, hkv, seed=1)
+    ref, start, n = w.reference(), w.query_start(), len(w.chunks)
+    for bad in (0, n // 3, n - 1):
+        s = Step(w)
+        s.lens[bad] = w.width * block_size + 1
+        s.prefill()
+        got, rows = out_f64(s.out), np.ones(len(ref), bool)
+        rows[start[bad]:start[bad + 1]] = False
+        assert int(s.err.item()) == 5 and np.all(got[~rows] == 123.0)
+        ok, err, _ = within_bound(got[rows], ref[rows], w.qdt)
+        assert ok, err
+    # a start that falls: sequence 2 begins before the batch, 1 ends before it starts
+    s = Step(w)
+    s.start[2] = -4
+    s.prefill()
+    got, rows = out_f64(s.out), np.ones(len(ref), bool)
+    rows[start[1]:start[3]] = False
+    assert int(s.err.item()) == 5 and np.all(got[~rows] == 123.0)
+    ok, err, _ = within_bound(got[rows], ref[rows], w.qdt)
+    assert ok, err
+    # chunks that overlap from the start on may not all be done, which is reported
+    s = Step(w)
+    s.start[:] = torch.arange(n + 1, dtype=torch.int32, device="cuda") % 2 * 600
+    s.lens.fill_(w.width * block_size)
+    s.table.fill_(0)
+    s.prefill()
+    assert int(s.err.item()) == 5
+
+
+@pytest.mark.parametrize("dtype,d,block_size,hq,hkv,n,rows", [
+    ("f32", 64, 16, 16, 1, 8200, 131072),    # 2.1e9 groups of rows for a grid of the longest chunk's
+    ("bf16", 64, 16, 128, 1, 33000, 65536),  # 2.2e9 tiles
+    ("bf16", 64, 16, 128, 1, 4096, 65536),   # 2.7e8 tiles, 1.8 million for each CTA to step over
+    ("bf16", 64, 48, 128, 1, 4096, 65536),
+])
+def test_prefill_window_capacity_buffers(dtype, d, block_size, hq, hkv, n, rows):
+    """A batch of single tokens in buffers of a capacity, which also bounds the chunks (a captured graph's): the call
+    goes by what is there."""
+    import torch
+    from test_gpu_window import check
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.integers(1, 4, n)]
+    w = WindowCase(dtype, lens, [1] * n, hq, hkv, d, block_size, 2, 1, seed=n, slack_blocks=3)
+    s = Step(w)
+    out = torch.full((rows, hq, d), 123.0, dtype=s.q.dtype, device="cuda")
+    q = torch.zeros_like(out)
+    q[:n] = s.q
+    s.q, s.out = q, out
+    s.prefill(max_query_len=rows)
+    assert int(s.err.item()) == 0 and torch.all(out[n:] == 123.0)
+    s.out = out[:n].contiguous()
+    check(s, w.reference(), "capacity buffers")
+    del q, out
+    torch.cuda.empty_cache()
