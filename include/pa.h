@@ -427,17 +427,24 @@ int pa_decode_window(void* out, const void* q, void* k_cache, void* v_cache, con
  *   tokens of pa_decode_window: query j of sequence s, at position p = L - n + j, sees the positions i <= p
  *   with i > p - window or i < num_sinks.  The chunk's own K/V are in the cache already (pa_rope_and_cache,
  *   pa_reshape_and_cache).  Chunks of one token (a decode step) to whole prompts, and any mixture of them.
- *   (Many single tokens beside long chunks run faster as two calls, theirs to pa_decode_window: 1023 and a prompt of 4096,
- *   64 / 8 heads, window 1024, bf16: 0.66 ms for 1.62.)
+ *   (Many single tokens beside long chunks run faster as two calls, theirs to pa_decode_window: 1023 and a
+ *   prompt of 4096, 64 / 8 heads, window 1024, bf16: 0.66 ms for 1.62.)
  *
- *   out, q, query_start, seq_lens, max_query_len  as for pa_prefill; out rows outside every chunk are not
- *                written.  A sequence whose chunk breaks the rules there is skipped (PA_DEVERR_QUERY).
+ *   out, q, query_start, seq_lens, max_query_len  as for pa_prefill; query_start does not fall; out rows
+ *                outside every chunk are not written.  A sequence whose chunk breaks the rules there is
+ *                skipped (PA_DEVERR_QUERY).
  *   Table entries of blocks without a position that some query of the chunk sees are never read (they may
  *   have been released).  Value rows of positions that some queries of the chunk see and others do not must
  *   be finite.  NaN queries and keys as for pa_decode_window: only the rows that see them become NaN.
  *   scale        finite and > 0;  window >= 1;  num_sinks >= 0
  *   k_scale, v_scale  FP8 caches (> 0; 0 means 1): q and out are fp16.  Ignored for other caches.
- *   Every cache type, head size and block size of pa_decode.  No workspace.
+ *   Every cache type, head size and block size of pa_decode.  No workspace.  Prompts are fast where the block
+ *   size divides 128 (8 to 128; 16-bit and FP8 caches); others, and fp32, take the kernels for few queries,
+ *   which read the keys again for every eight rows (a chunk of 4096, window 4096, 32 / 8 heads, fp16: blocks
+ *   of 16 0.23 ms, of 48 or 256 2.5 ms).
+ *   Softmax weights enter the value product as fp32 numbers over fp32 caches; as two bf16 terms (16 bits or
+ *   more) over bf16; as one fp16 term, off by at most 2^-11 of a weight or 2^-25 of the row's largest, over FP8
+ *   (pa_decode_window too) and for longer chunks over fp16, where few queries get two.
  */
 int pa_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                       const int32_t* seq_lens, const int32_t* query_start, int32_t num_seqs,

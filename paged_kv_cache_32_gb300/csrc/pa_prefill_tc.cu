@@ -83,7 +83,11 @@
 //  * Head size 64: one 64-column half of each tile, N = 64 for P V, two producers.
 //  * Bound like the plain form: 16 chunks of 256-1024 queries, 32 / 8 heads, W = 1024
 //    take 264 us in bf16 (676 TFLOP/s of the formula's work), 207 in fp16, 254 over an
-//    FP8 cache; one chunk of 4096, W = 4096, fp16: 225 us, 1240 TFLOP/s.
+//    FP8 cache; one chunk of 4096, W = 4096, fp16: 225 us, 1240 TFLOP/s (replayed
+//    graphs; called eagerly, with other inputs each time, 271 us, 658 TFLOP/s, and 241
+//    us, 1160).
+//  * Batches that mix chunk lengths (kMixed) pass over the tiles that a sequence lacks
+//    of the longest chunk's: see pf_skip.
 //  * FP8 caches (kFp8, fp16 queries): the producers load the codes into registers
 //    a tile ahead, convert them to fp16 (exact) and store the swizzled tiles
 //    themselves.  Values lie in the cache with a dimension's 16 tokens side by

@@ -8,8 +8,9 @@
 // Angles.  t f_j reaches millions of radians, where an fp32 product is off by
 // whole fractions of a turn.  f_j / 2 pi is therefore held as a 64-bit fixed-point
 // fraction of a turn: the 64-bit product with the integer t drops whole turns
-// exactly.  What is left of rounding is that of f_j / 2 pi to 53 bits, 2^-53 t f_j / 2 pi
-// turns (f_j <= 1 and any int32 t: 2^-24.6), and of the fraction to fp32 for sincospif.
+// exactly.  What is left of rounding is that of 1 / 2 pi and of its product with f_j to 53
+// bits, together at most 2^-52 t f_j / 2 pi turns (f_j <= 1 and any int32 t: 2^-23.6), and of
+// the fraction to fp32 for sincospif.
 // One angle per (token, pair) and CTA, kept in shared memory for all heads.
 //
 // Bound by HBM bandwidth: 4 + (cache / element) bytes moved an element.  Work is

@@ -16,7 +16,7 @@ using namespace pa::host;
 
 namespace {
 
-constexpr int kSms = 152;
+constexpr int kSms = 152;          // of a GB300, which the choices below were measured on: elsewhere slower, not wrong
 constexpr int kMaxCluster = pa::kPortableCluster;  // (rows kernels also take the largest, twice that, where it fits)
 constexpr int kMinCtaTokens = 64;  // tokens of a CTA below which a split no longer pays
 constexpr int kFewItems = 4096;    // work items whose empty ones cost a few microseconds at most
