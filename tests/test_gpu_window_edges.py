@@ -158,6 +158,19 @@ def test_prefill_window_mixed_batch(dtype, d, block_size, hq, hkv):
     check(t, w.reference(), "mixed, loose bound")
 
 
+def test_prefill_window_mixed_batch_long_windows():
+    """fp32 row groups in slots whose keys a cluster shares: all of its CTAs find the same group, or none."""
+    from test_gpu_window import check
+    rng = np.random.default_rng(4)
+    chunks = [1] * 70
+    chunks[40] = 700
+    lens = [c + int(x) for c, x in zip(chunks, rng.integers(0, 2600, 70))]
+    w = WindowCase("f32", lens, chunks, 4, 1, 64, 16, 2500, 4, seed=4)
+    s = Step(w)
+    s.prefill()
+    check(s, w.reference(), "mixed, long windows")
+
+
 @pytest.mark.parametrize("dtype,d,block_size,hq,hkv", MIXED)
 def test_prefill_window_mixed_batch_bad_chunks(dtype, d, block_size, hq, hkv):
     """Inconsistent chunks of a mixed batch are reported and skipped, wherever they stand; the others are right."""
