@@ -406,7 +406,7 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
   plan.log2_per_head = 0;
   while ((1 << plan.log2_per_head) < per_head) ++plan.log2_per_head;
   const long long per_token = (long long)(p.num_q_heads + (FP8 ? 1 : 2) * p.num_kv_heads) * per_head;
-  constexpr int kCtas = 152 * kRopeResident;
+  constexpr int kCtas = 152 * kRopeResident;  // of a GB300 (elsewhere slower, not wrong: no CTA waits for another)
   // units of a CTA and group: as many as its threads hold, or, while that leaves SMs idle (a decode step), fewer
   long long most = (long long)kUnits<T, V> * kRopeThreads;
   while (most > kRopeThreads && per_token * p.num_tokens < kCtas * most) most /= 2;

@@ -44,9 +44,9 @@ struct ClusterRoom {
 };
 constexpr int kPortableCluster = 8;
 
-// What a rows kernel needs before its launch: its shared memory, and a cluster size that the current device places:
-// a larger one than eight may not fit any of its GPCs (of which some have fewer SMs, or a context may hold few), and
-// a launch of one that does not is an error, so *cluster becomes eight there.  The device is asked once.
+// What a rows kernel needs before its launch: its shared memory, and a cluster size that the current device places: a
+// larger one than eight may fit none of its GPCs (a partition of a GPU may hold few SMs of each), and its launch would
+// be an error, so *cluster becomes eight there.  The device is asked once.
 template <typename Kernel>
 cudaError_t prepare_rows(Kernel kernel, ClusterRoom& room, int threads, size_t smem, int32_t* cluster) {
   const void* f = reinterpret_cast<const void*>(kernel);
