@@ -573,6 +573,7 @@ constexpr int kFp8Threads = (kFp8LoadWarp0 + kFp8Producers) * 32;
 // not raised again at the roles' ends: a producer that finished before the softmax warps had started would take the
 // registers that they wait for.
 constexpr int kFp8LaunchRegs = 96, kFp8SoftmaxRegs = 128, kFp8LoadRegs = 80, kFp8IssueRegs = 64;
+// (that the build launches with as many is checked before the first launch)
 static_assert(8 * 32 * kFp8SoftmaxRegs + 4 * 32 * kFp8IssueRegs + kFp8Producers * 32 * kFp8LoadRegs <=
                   kFp8Threads * kFp8LaunchRegs,
               "a raised limit waits for registers that the launch does not have");
@@ -1413,6 +1414,11 @@ static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, 
   auto kernel = prefill_tc_kernel<T, kForm, kFp8, D>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
+  if constexpr (kFp8) {
+    static std::atomic<bool> known;
+    e = require_registers(reinterpret_cast<const void*>(kernel), kFp8LaunchRegs, known);
+    if (e != cudaSuccess) return e;
+  }
   return launch_cluster(kernel, dim3(grid), dim3(kFp8 ? kFp8Threads : kThreads), kSmemBytes, p.split, false, stream, tk,
                         tv, tq, to, p);
 }
