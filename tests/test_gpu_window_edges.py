@@ -230,3 +230,39 @@ def test_prefill_window_capacity_buffers(dtype, d, block_size, hq, hkv, n, rows)
     check(s, w.reference(), "capacity buffers")
     del q, out
     torch.cuda.empty_cache()
+
+
+FIRST_CALL = """
+import torch
+import paged_kv_cache_32_gb300 as pa
+for dtype in (torch.bfloat16, torch.uint8, torch.float32):
+    rows = torch.float16 if dtype == torch.uint8 else dtype
+    k = torch.randint(0, 64, (600, 1, 16, 128), device="cuda").to(dtype)
+    v = k.view(600, 1, 1, 128, 16) if dtype == torch.uint8 else k
+    q = torch.ones(1, 8, 128, device="cuda", dtype=rows)
+    out, again = torch.zeros_like(q), torch.zeros_like(q)
+    table = torch.arange(600, device="cuda", dtype=torch.int32)[None]
+    lens, start = (torch.tensor(x, device="cuda", dtype=torch.int32) for x in ([9000], [0, 1]))
+    calls = (lambda o: pa.pa_decode_window(o, q, k, v, table, lens, 0.01, 8000, num_sinks=4),
+             lambda o: pa.pa_prefill_window(o, q, k, v, table, lens, start, 1, 0.01, 8000, num_sinks=4))
+    for call in calls:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(out)
+        graph.replay()
+        call(again)
+        torch.cuda.synchronize()
+        assert torch.equal(out, again) and torch.count_nonzero(out) > 0
+print("same")
+"""
+
+
+def test_window_first_call_captured():
+    """A process whose first call of each kernel is captured: what the call asks the device once is no obstacle."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr
