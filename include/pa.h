@@ -55,16 +55,16 @@
 extern "C" {
 #endif
 
-typedef enum { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_FP8_E4M3 = 3 } pa_dtype;
+typedef enum { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_FP8_E4M3 = 3, PA_FP4_E2M1 = 4 } pa_dtype;
 
 /* Shape of one layer's KV cache pair. */
 typedef struct {
   int32_t num_blocks;   /* physical blocks in the pool */
-  int32_t block_size;   /* tokens per block B: f16/bf16 8 or a multiple of 16 (<= 256); fp8 a multiple of 16
+  int32_t block_size;   /* tokens per block B: f16/bf16 8 or a multiple of 16 (<= 256); fp8, fp4 a multiple of 16
                            (<= 256); f32 any B >= 1 */
   int32_t num_kv_heads; /* Hkv */
-  int32_t head_size;    /* D: 64 or 128 (fp8: 128) */
-  int32_t dtype;        /* pa_dtype of the cache, and of q/out and new key/value except for fp8 (see below) */
+  int32_t head_size;    /* D: 64 or 128 (fp8, fp4: 128) */
+  int32_t dtype;        /* pa_dtype of the cache, and of q/out and new key/value except for fp8, fp4 (see below) */
 } pa_cache_desc;
 
 /*
@@ -83,6 +83,21 @@ typedef struct {
  *   - q, out and the key/value rows written by pa_reshape_and_cache_fp8 are fp16;
  *   - written codes are the E4M3 code nearest to x / scale (fp32 division,
  *     ties to even; magnitudes past 448, infinities included, saturate to 448).
+ */
+
+/*
+ * FP4 caches (dtype PA_FP4_E2M1): 4 bits an element and a scale for every 16, 72 bytes a row of 128.
+ *   - a group is 16 neighbouring elements x of a row.  Its scale is s = e4m3(max |x| / (6 u)), u the cache's unit
+ *     (k_scale or v_scale, one fp32 number per cache, passed per call, 2^-100 .. 2^100), ties to even, at most 448;
+ *   - an element is held as the OCP E2M1 code (sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6)
+ *     nearest to x * (1 / (s u)), ties to even, magnitudes past 6 as 6; it stands for e2m1 * s * u.  6 u, the quotient,
+ *     s u, its inverse and the product are single fp32 operations.  A group whose scale is 0 holds zeros.  Rows should be
+ *     finite: an infinity becomes the largest number that the cache holds, a NaN some finite one;
+ *   - keys and values alike are [num_blocks][num_kv_heads][block_size / 16][1152] bytes: of 16 tokens [16][64] bytes of
+ *     codes (dimension 2 i in the low half of byte i, 2 i + 1 in the high one), then [16][8] bytes of scales;
+ *   - q, out and new key/value rows are fp16 or bf16, as the calls' row_dtype says.
+ * They are taken by pa_reshape_and_cache_fp4, pa_read_cache_fp4, pa_decode_fp4, pa_prefill_fp4, pa_rope_axes_and_cache
+ * and pa_copy_blocks; the other calls return PA_ERR_UNSUPPORTED.
  */
 
 /* Host-side status codes. */
@@ -104,8 +119,10 @@ enum {
   PA_DEVERR_SLOT = 2,     /* a slot_mapping entry >= num_blocks * block_size */
   PA_DEVERR_PAIR = 3,     /* a copy pair with an ID outside [0, num_blocks) */
   PA_DEVERR_TIMEOUT = 4,  /* a bounded wait on an asynchronous copy expired */
-  PA_DEVERR_QUERY = 5     /* pa_prefill: a chunk outside [0, num_query_tokens), longer than
+  PA_DEVERR_QUERY = 5,    /* pa_prefill: a chunk outside [0, num_query_tokens), longer than
                              max_query_len or than its sequence, or a sequence past its table */
+  PA_DEVERR_TABLES = 6,   /* pa_tables_*: lengths, blocks held or tokens wanted that do not fit together */
+  PA_DEVERR_NO_BLOCKS = 7 /* pa_tables_extend: more blocks needed than are free */
 };
 
 /*
@@ -145,7 +162,8 @@ enum {
  *   they read anything else (q, the caches, key/value, the workspace) or write
  *   anything, so stream order holds as for a plain launch provided that those
  *   two inputs are not written by a kernel that lets its dependents start
- *   early (no kernel of this library writes them; copies, and kernels that do
+ *   early (of this library only pa_tables_extend and pa_tables_trim write them, and
+ *   let none start early; copies, and kernels that do
  *   not execute griddepcontrol.launch_dependents, complete first).  Stream
  *   capture records the dependencies as programmatic edges.
  */
@@ -451,6 +469,100 @@ int pa_prefill_window(void* out, const void* q, const void* k_cache, const void*
                       int32_t num_query_tokens, int32_t num_q_heads, int32_t max_blocks_per_seq,
                       int32_t max_query_len, const pa_cache_desc* cache, float scale, int32_t window,
                       int32_t num_sinks, float k_scale, float v_scale, int32_t* err_flag, void* stream);
+
+/*
+ * pa_reshape_and_cache_fp4 - the append for an FP4 cache (see "FP4 caches" above): key[t][h][:] and value[t][h][:] go to
+ *   the slot of token t.  A slot's bytes are its own: no write touches another token's.
+ *
+ *   key, value   [num_tokens][num_kv_heads][128] of row_dtype (PA_F16, PA_BF16), *_stride elements from one token to
+ *                the next (at least the row of its heads, a multiple of 8), 16-byte aligned
+ *   slot_mapping int64 [num_tokens], as for pa_reshape_and_cache
+ */
+int pa_reshape_and_cache_fp4(void* k_cache, void* v_cache, const void* key, const void* value, int64_t key_stride,
+                             int64_t value_stride, const int64_t* slot_mapping, int32_t num_tokens,
+                             const pa_cache_desc* cache, int32_t row_dtype, float k_scale, float v_scale,
+                             int32_t* err_flag, void* stream);
+
+/*
+ * pa_read_cache_fp4 - the rows that the slots of an FP4 cache hold, back in 16 bits (to move a prefix into another
+ *   cache, to look at what was written): e2m1 * s * u, the fp32 product rounded once to row_dtype.  Arguments as for
+ *   pa_reshape_and_cache_fp4; rows of negative slots, and of slots outside the pool (PA_DEVERR_SLOT), are not written.
+ */
+int pa_read_cache_fp4(void* key, void* value, const void* k_cache, const void* v_cache, int64_t key_stride,
+                      int64_t value_stride, const int64_t* slot_mapping, int32_t num_tokens, const pa_cache_desc* cache,
+                      int32_t row_dtype, float k_scale, float v_scale, int32_t* err_flag, void* stream);
+
+/*
+ * pa_decode_fp4, pa_prefill_fp4 - pa_decode_window and pa_prefill_window over an FP4 cache: the same rows, window, first
+ *   tokens, append and errors.  window INT32_MAX (any number no smaller than the lengths) is attention over everything.
+ *
+ *   out, q       of row_dtype (PA_F16, PA_BF16), 16-byte aligned (pa_decode_fp4's out: 4)
+ *   key, value   pa_decode_fp4: both NULL, or each sequence's new token of row_dtype, [num_seqs][num_kv_heads][128],
+ *                stored at position seq_lens[s] - 1 in the bytes that pa_reshape_and_cache_fp4 writes, and attended
+ *   alibi_slopes, test_flags  as in pa_decode_options (NULL, 0 in normal use)
+ *   Softmax weights enter the value product as one fp16 term (pa_prefill_fp4 with bf16 rows and longer chunks: two bf16
+ *   terms).  Queries in bf16 lose what lies more than 2^-24 below the largest element of their head's row.
+ */
+int pa_decode_fp4(void* out, const void* q, void* k_cache, void* v_cache, const void* key, const void* value,
+                  const int32_t* block_tables, const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads,
+                  int32_t max_blocks_per_seq, const pa_cache_desc* cache, int32_t row_dtype, float scale, int32_t window,
+                  int32_t num_sinks, float k_scale, float v_scale, const float* alibi_slopes, uint32_t test_flags,
+                  int32_t* err_flag, void* stream);
+int pa_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                   const int32_t* seq_lens, const int32_t* query_start, int32_t num_seqs, int32_t num_query_tokens,
+                   int32_t num_q_heads, int32_t max_blocks_per_seq, int32_t max_query_len, const pa_cache_desc* cache,
+                   int32_t row_dtype, float scale, int32_t window, int32_t num_sinks, float k_scale, float v_scale,
+                   int32_t* err_flag, void* stream);
+
+/*
+ * pa_rope_axes_and_cache - pa_rope_and_cache with a position for each of several axes (time, height and width of images
+ *   and video beside text): pair j of a token turns by a_j = positions[pair_axis[j]][t] * inv_freq[j].
+ *
+ *   positions    int32 [num_axes][num_tokens], num_axes 1 .. 4
+ *   pair_axis    HOST array of rotary_dim / 2 axis numbers, read during the call (NULL: all axis 0, num_axes 1)
+ *   row_dtype    FP4 caches: of q, q_out, key and value (PA_F16, PA_BF16), whose turned keys are rounded to it and then
+ *                held as pa_reshape_and_cache_fp4 holds them (k_scale, v_scale the units).  Ignored for other caches.
+ *   Everything else as for pa_rope_and_cache.
+ */
+int pa_rope_axes_and_cache(void* q_out, void* k_cache, void* v_cache, const void* q, const void* key, const void* value,
+                           int64_t q_out_stride, int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                           const int32_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                           const int64_t* slot_mapping, const double* inv_freq, int32_t num_tokens, int32_t num_q_heads,
+                           int32_t rotary_dim, int32_t interleaved, float magnitude, const pa_cache_desc* cache,
+                           int32_t row_dtype, float k_scale, float v_scale, int32_t* err_flag, void* stream);
+
+/*
+ * pa_tables_extend, pa_tables_trim - block tables, lengths and slot maps kept on the GPU, for loops that learn a
+ *   request's length there (captured steps, verified drafts).  The state, device memory that the caller makes once:
+ *
+ *   block_tables int32 [num_seqs][max_blocks_per_seq]: entries 0 .. held_blocks[s] - 1 are request s's blocks, its alone
+ *   seq_lens     int32 [num_seqs], at most held_blocks[s] * block_size
+ *   held_blocks  int32 [num_seqs]
+ *   free_blocks  int32 [num_blocks]: entries 0 .. *num_free - 1 are a stack of the blocks that no request holds
+ *   num_free     int32 [1]
+ *
+ *   pa_tables_extend gives request s new_tokens[s] >= 0 more tokens and the blocks that they need beyond those held
+ *   (from the top of the stack; requests in order, a request's blocks in order), and writes, of the Q_s + j-th row, for
+ *   its j-th new token (Q_s: the new tokens of the requests before):
+ *     slot_mapping int64 [num_rows], its slot; positions int32 [num_rows], its position;
+ *     query_start  int32 [num_seqs + 1], Q_s, and their sum at the end.
+ *   Rows past the sum get slot -1 (padding) and position 0.
+ *   pa_tables_trim keeps the first keep_lens[s] <= seq_lens[s] tokens of request s: the blocks past them go back, their
+ *   table entries become -1.  The first request's first such block comes out on top of the stack.  0 ends a request.
+ *
+ *   All or nothing: a request whose numbers do not fit (a negative one, more tokens than its table or than its blocks
+ *   hold, more kept than there are, more rows than num_rows, a stack that does not fit) gives PA_DEVERR_TABLES, too few
+ *   free blocks PA_DEVERR_NO_BLOCKS, and nothing of the state changes; extend then writes padding rows and zeros in
+ *   query_start.  A block outside the pool gives PA_DEVERR_BLOCK_ID; its tokens' rows are padding.
+ *   num_seqs <= 16384.  The arrays do not overlap.  Two calls on one state are ordered by the caller, on one stream.
+ */
+int pa_tables_extend(int32_t* block_tables, int32_t* seq_lens, int32_t* held_blocks, const int32_t* free_blocks,
+                     int32_t* num_free, const int32_t* new_tokens, int64_t* slot_mapping, int32_t* positions,
+                     int32_t* query_start, int32_t num_seqs, int32_t num_rows, int32_t max_blocks_per_seq,
+                     int32_t block_size, int32_t num_blocks, int32_t* err_flag, void* stream);
+int pa_tables_trim(int32_t* block_tables, int32_t* seq_lens, int32_t* held_blocks, int32_t* free_blocks,
+                   int32_t* num_free, const int32_t* keep_lens, int32_t num_seqs, int32_t max_blocks_per_seq,
+                   int32_t block_size, int32_t num_blocks, int32_t* err_flag, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* pa_status_string(int status);

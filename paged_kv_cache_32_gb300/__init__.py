@@ -17,15 +17,17 @@ import os
 
 from . import build as _build
 
-PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2, 3
+PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3, PA_FP4_E2M1 = 0, 1, 2, 3, 4
 PA_OK = 0
 PA_DEVERR = {0: "none", 1: "block id out of range", 2: "slot out of range", 3: "copy pair id out of range",
-             4: "wait on an asynchronous copy timed out", 5: "prefill chunk inconsistent with q, grid or sequence"}
+             4: "wait on an asynchronous copy timed out", 5: "prefill chunk inconsistent with q, grid or sequence",
+             6: "tables, lengths and wanted tokens do not fit together", 7: "not enough free blocks"}
 
 EXPORTED = ("pa_decode", "pa_decode_ex", "pa_decode_append", "pa_decode_partition_size", "pa_decode_workspace_size",
             "pa_reshape_and_cache", "pa_copy_blocks", "pa_status_string", "pa_version", "pa_decode_noalloc", "pa_prefill",
             "pa_reshape_and_cache_fp8", "pa_rope_frequencies", "pa_rope_and_cache", "pa_decode_window",
-            "pa_prefill_window")
+            "pa_prefill_window", "pa_reshape_and_cache_fp4", "pa_read_cache_fp4", "pa_decode_fp4", "pa_prefill_fp4",
+            "pa_rope_axes_and_cache", "pa_tables_extend", "pa_tables_trim")
 
 
 PA_DECODE_TEST_EXPIRE_FIRST_WAIT = 1
@@ -103,6 +105,23 @@ def lib() -> ctypes.CDLL:
         L.pa_prefill_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, desc_p, f32, i32, i32, f32,
                                         f32, vp, vp]
         L.pa_prefill_window.restype = ctypes.c_int
+        L.pa_reshape_and_cache_fp4.argtypes = [vp, vp, vp, vp, i64, i64, vp, i32, desc_p, i32, f32, f32, vp, vp]
+        L.pa_reshape_and_cache_fp4.restype = ctypes.c_int
+        L.pa_read_cache_fp4.argtypes = L.pa_reshape_and_cache_fp4.argtypes
+        L.pa_read_cache_fp4.restype = ctypes.c_int
+        L.pa_decode_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, desc_p, i32, f32, i32, i32, f32, f32, vp,
+                                    ctypes.c_uint32, vp, vp]
+        L.pa_decode_fp4.restype = ctypes.c_int
+        L.pa_prefill_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, desc_p, i32, f32, i32, i32, f32,
+                                     f32, vp, vp]
+        L.pa_prefill_fp4.restype = ctypes.c_int
+        L.pa_rope_axes_and_cache.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, ctypes.c_char_p, vp, vp,
+                                             i32, i32, i32, i32, f32, desc_p, i32, f32, f32, vp, vp]
+        L.pa_rope_axes_and_cache.restype = ctypes.c_int
+        L.pa_tables_extend.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+        L.pa_tables_extend.restype = ctypes.c_int
+        L.pa_tables_trim.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+        L.pa_tables_trim.restype = ctypes.c_int
         L.pa_status_string.argtypes = [ctypes.c_int]
         L.pa_status_string.restype = ctypes.c_char_p
         L.pa_version.argtypes = []
@@ -427,9 +446,21 @@ def pa_rope_and_cache(q_out, k_cache, v_cache, q, key, value, positions, slot_ma
     (views of a fused projection).  q_out may be q.  positions int32, slot_mapping int64 [num_tokens] (negative:
     padding, nothing is written); inv_freq float64 on the device, magnitude: see pa_rope_frequencies.
     ``interleaved``: pairs (2j, 2j + 1), else (j, j + rotary_dim / 2)."""
-    import torch
     where = "pa_rope_and_cache"
     dev, desc, rows = _caches(k_cache, v_cache, desc, where)
+    tokens, hq, qp, op, qs, os_, ks, vs, err = _rope(where, dev, desc, rows, q_out, q, key, value, positions, slot_mapping,
+                                                     inv_freq, 1, err_flag)
+    _launch(lib().pa_rope_and_cache, dev, (
+        op, k_cache.data_ptr(), v_cache.data_ptr(), qp, key.data_ptr(), value.data_ptr(), os_, qs, ks, vs,
+        positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), tokens, hq, 2 * inv_freq.numel(),
+        1 if interleaved else 0, float(magnitude), desc, float(k_scale or 0.0), float(v_scale or 0.0), err,
+        _stream_of(dev, stream)), where)
+
+
+def _rope(where, dev, desc, rows, q_out, q, key, value, positions, slot_mapping, inv_freq, axes, err_flag):
+    """The checks of both rotary writes: tokens, query heads, addresses of q and q_out, the four strides, address of
+    err_flag."""
+    import torch
     if not (key.dtype is rows and value.dtype is rows and positions.dtype is torch.int32 and
             slot_mapping.dtype is torch.int64 and inv_freq.dtype is torch.float64 and key.get_device() == dev and
             value.get_device() == dev and positions.get_device() == dev and slot_mapping.get_device() == dev and
@@ -439,7 +470,7 @@ def pa_rope_and_cache(q_out, k_cache, v_cache, q, key, value, positions, slot_ma
     if not (positions.is_contiguous() and slot_mapping.is_contiguous() and inv_freq.is_contiguous()):
         raise ValueError(f"{where}: positions, slot_mapping and inv_freq must be contiguous")
     tokens, d, hkv = key.shape[0], desc.head_size, desc.num_kv_heads
-    if positions.numel() != tokens or slot_mapping.numel() != tokens:
+    if positions.numel() != axes * tokens or slot_mapping.numel() != tokens:
         raise ValueError(f"{where}: positions and slot_mapping must hold {tokens} tokens")
     kv_shape = (tokens, hkv, d)
     ks, vs = _token_rows(key, "key", kv_shape, where), _token_rows(value, "value", kv_shape, where)
@@ -457,11 +488,51 @@ def pa_rope_and_cache(q_out, k_cache, v_cache, q, key, value, positions, slot_ma
     if err_flag is not None:
         _refuse(where, dev, False, (err_flag, "err_flag", torch.int32))
         err = err_flag.data_ptr()
-    _launch(lib().pa_rope_and_cache, dev, (
+    return tokens, hq, qp, op, qs, os_, ks, vs, err
+
+
+def pa_rope_axes_and_cache(q_out, k_cache, v_cache, q, key, value, positions, slot_mapping, inv_freq, pair_axis,
+                           interleaved: bool = False, magnitude: float = 1.0, err_flag=None, stream=None,
+                           desc: pa_cache_desc | None = None, k_scale: float | None = None,
+                           v_scale: float | None = None) -> None:
+    """pa_rope_and_cache with positions int32 [axes, num_tokens] along 1 to 4 axes: pair j of a head turns by
+    positions[pair_axis[j]] * inv_freq[j].  ``pair_axis``: an axis number for each pair (bytes, or any sequence on the
+    host; pa_rope_pair_axes makes one).  Over a 4-bit cache (see fp4_cache) the rows are fp16 or bf16, and ``k_scale`` /
+    ``v_scale`` its units."""
+    where = "pa_rope_axes_and_cache"
+    if k_cache.shape[-1] == FP4_TILE_BYTES:
+        dev, desc, code = _caches_fp4(k_cache, v_cache, desc, key.dtype, where)
+        rows, k_scale, v_scale = key.dtype, float(k_scale or 1.0), float(v_scale or 1.0)
+    else:
+        dev, desc, rows = _caches(k_cache, v_cache, desc, where)
+        code = 0
+    if positions.dim() != 2 or not 1 <= positions.shape[0] <= 4:
+        raise ValueError(f"{where}: positions must be [axes, num_tokens], 1 to 4 axes")
+    axes, pairs = positions.shape[0], bytes(pair_axis)
+    if len(pairs) != inv_freq.numel():
+        raise ValueError(f"{where}: pair_axis must hold {inv_freq.numel()} axis numbers")
+    tokens, hq, qp, op, qs, os_, ks, vs, err = _rope(where, dev, desc, rows, q_out, q, key, value, positions, slot_mapping,
+                                                     inv_freq, axes, err_flag)
+    _launch(lib().pa_rope_axes_and_cache, dev, (
         op, k_cache.data_ptr(), v_cache.data_ptr(), qp, key.data_ptr(), value.data_ptr(), os_, qs, ks, vs,
-        positions.data_ptr(), slot_mapping.data_ptr(), inv_freq.data_ptr(), tokens, hq, 2 * inv_freq.numel(),
-        1 if interleaved else 0, float(magnitude), desc, float(k_scale or 0.0), float(v_scale or 0.0), err,
+        positions.data_ptr(), axes, pairs, slot_mapping.data_ptr(), inv_freq.data_ptr(), tokens, hq, 2 * inv_freq.numel(),
+        1 if interleaved else 0, float(magnitude), desc, code, float(k_scale or 0.0), float(v_scale or 0.0), err,
         _stream_of(dev, stream)), where)
+
+
+def pa_rope_pair_axes(sections, interleaved: bool = False) -> bytes:
+    """The axis of each rotary pair: sections[a] pairs for axis a, one section after the other, or dealt out in turn
+    (axis 0, 1, 2, 0, 1, ..., an axis whose section is used up left out)."""
+    left = [int(n) for n in sections]
+    if not interleaved:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    got = []
+    while any(n > 0 for n in left):
+        for a in range(len(left)):
+            if left[a] > 0:
+                got.append(a)
+                left[a] -= 1
+    return bytes(got)
 
 
 def _attention(where, host, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc):
@@ -548,3 +619,227 @@ def pa_prefill_window(out, q, k_cache, v_cache, block_tables, seq_lens, query_st
         min(_int32(max_query_len), shape[0]), desc,
         float(scale), _int32(window), _int32(num_sinks), float(k_scale or 0.0),
         float(v_scale or 0.0), err, _stream_of(dev, stream)), where)
+
+
+# ---------------------------------------------------------------- caches held in 4 bits
+FP4_TILE_BYTES = 1152  # of 16 tokens of a kv head: [16, 64] bytes of codes, [16, 8] of scales
+_FP4_ROWS: dict = {}   # dtype of the rows -> code
+
+
+def fp4_cache(num_blocks: int, num_kv_heads: int, block_size: int, device="cuda"):
+    """A zeroed key or value cache held in 4 bits: uint8 [num_blocks, num_kv_heads, block_size / 16, 1152]."""
+    import torch
+    if block_size <= 0 or block_size % 16:
+        raise ValueError("fp4_cache: block_size must be a multiple of 16")
+    return torch.zeros((num_blocks, num_kv_heads, block_size // 16, FP4_TILE_BYTES), dtype=torch.uint8, device=device)
+
+
+def fp4_cache_desc(k_cache) -> pa_cache_desc:
+    """Descriptor of a cache made by fp4_cache."""
+    if k_cache.dim() != 4 or k_cache.shape[3] != FP4_TILE_BYTES or k_cache.element_size() != 1:
+        raise ValueError(f"a 4-bit cache must be uint8 [num_blocks, num_kv_heads, block_size / 16, {FP4_TILE_BYTES}]")
+    nb, hkv, tiles, _ = (int(x) for x in k_cache.shape)
+    return pa_cache_desc(nb, 16 * tiles, hkv, 128, PA_FP4_E2M1)
+
+
+def _caches_fp4(k_cache, v_cache, desc, rows, where: str):
+    """(device index, descriptor, code of the rows' dtype) of a pair of 4-bit caches."""
+    if not _FP4_ROWS:
+        import torch
+        _FP4_ROWS.update({torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.uint8: None})
+    dev = k_cache.get_device()
+    if dev < 0:
+        raise ValueError(f"{where}: the caches must be CUDA tensors")
+    if k_cache.element_size() != 1 or v_cache.dtype is not k_cache.dtype or v_cache.get_device() != dev or \
+            v_cache.shape != k_cache.shape or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError(f"{where}: k_cache and v_cache must be contiguous uint8 tensors of one shape on one device")
+    code = _FP4_ROWS.get(rows)
+    if code is None:
+        raise TypeError(f"{where}: rows over a 4-bit cache are float16 or bfloat16, got {rows}")
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != FP4_TILE_BYTES:
+        raise ValueError(f"{where}: a 4-bit cache must be [num_blocks, num_kv_heads, block_size / 16, {FP4_TILE_BYTES}]")
+    if desc is None:
+        desc = pa_cache_desc(shape[0], 16 * shape[2], shape[1], 128, PA_FP4_E2M1)
+    elif (desc.dtype, desc.num_blocks, desc.num_kv_heads, desc.block_size) != (PA_FP4_E2M1, shape[0], shape[1],
+                                                                              16 * shape[2]):
+        raise ValueError(f"{where}: desc does not describe the caches")
+    return dev, desc, code
+
+
+def _fp4_rows(name, fn, k_cache, v_cache, key, value, slot_mapping, k_scale, v_scale, err_flag, stream, desc, read):
+    import torch
+    dev, desc, code = _caches_fp4(k_cache, v_cache, desc, key.dtype, name)
+    if not (value.dtype is key.dtype and slot_mapping.dtype is torch.int64 and key.get_device() == dev and
+            value.get_device() == dev and slot_mapping.get_device() == dev):
+        _refuse(name, dev, True, (key, "key", key.dtype), (value, "value", key.dtype),
+                (slot_mapping, "slot_mapping", torch.int64))
+    tokens = key.shape[0]
+    if slot_mapping.dim() != 1 or slot_mapping.shape[0] != tokens or not slot_mapping.is_contiguous():
+        raise ValueError(f"{name}: slot_mapping must be [{tokens}]")
+    shape = (tokens, desc.num_kv_heads, 128)
+    ks, vs = _token_rows(key, "key", shape, name), _token_rows(value, "value", shape, name)
+    err = None
+    if err_flag is not None:
+        _refuse(name, dev, False, (err_flag, "err_flag", torch.int32))
+        err = err_flag.data_ptr()
+    caches, rows = (k_cache.data_ptr(), v_cache.data_ptr()), (key.data_ptr(), value.data_ptr())
+    _launch(fn, dev, (*(rows + caches if read else caches + rows), ks, vs, slot_mapping.data_ptr(), tokens, desc, code,
+                      float(k_scale), float(v_scale), err, _stream_of(dev, stream)), name)
+
+
+def pa_reshape_and_cache_fp4(k_cache, v_cache, key, value, slot_mapping, k_scale: float, v_scale: float, err_flag=None,
+                             stream=None, desc: pa_cache_desc | None = None) -> None:
+    """Write key/value [num_tokens, num_kv_heads, 128] (fp16 or bf16; a token's heads dense, tokens may lie further apart)
+    into the slots of a 4-bit cache (see fp4_cache): every 16 elements share a scale of 8 bits, k_scale / v_scale are the
+    caches' units (2688 units is the largest number that a cache holds)."""
+    _fp4_rows("pa_reshape_and_cache_fp4", lib().pa_reshape_and_cache_fp4, k_cache, v_cache, key, value, slot_mapping,
+              k_scale, v_scale, err_flag, stream, desc, False)
+
+
+def pa_read_cache_fp4(key, value, k_cache, v_cache, slot_mapping, k_scale: float, v_scale: float, err_flag=None,
+                      stream=None, desc: pa_cache_desc | None = None) -> None:
+    """The rows that the slots of a 4-bit cache hold, into key/value [num_tokens, num_kv_heads, 128] (fp16 or bf16)."""
+    _fp4_rows("pa_read_cache_fp4", lib().pa_read_cache_fp4, k_cache, v_cache, key, value, slot_mapping, k_scale, v_scale,
+              err_flag, stream, desc, True)
+
+
+def _attention_fp4(where, host, out, q, k_cache, v_cache, block_tables, seq_lens, err_flag, desc):
+    """The checks of both attention calls over a 4-bit cache, as _attention."""
+    import torch
+    rows = q.dtype
+    dev, desc, code = _caches_fp4(k_cache, v_cache, desc, rows, where)
+    if not (out.dtype is rows and block_tables.dtype is torch.int32 and seq_lens.dtype is torch.int32 and
+            out.get_device() == dev and q.get_device() == dev and block_tables.get_device() == dev and
+            seq_lens.get_device() == dev):
+        _refuse(where, dev, host, (out, "out", rows), (q, "q", rows), (block_tables, "block_tables", torch.int32),
+                (seq_lens, "seq_lens", torch.int32))
+    if not (out.is_contiguous() and q.is_contiguous() and block_tables.is_contiguous() and seq_lens.is_contiguous()):
+        raise ValueError(f"{where}: out, q, block_tables and seq_lens must be contiguous")
+    err = None
+    if err_flag is not None:
+        _refuse(where, dev, False, (err_flag, "err_flag", torch.int32))
+        err = err_flag.data_ptr()
+    shape, table = q.shape, block_tables.shape
+    if len(shape) != 3 or shape[2] != 128 or out.shape != shape:
+        raise ValueError(f"{where}: q and out must be [queries, heads, 128]")
+    if len(table) != 2 or seq_lens.dim() != 1 or seq_lens.shape[0] != table[0]:
+        raise ValueError(f"{where}: block_tables must be [num_seqs, max_blocks_per_seq], seq_lens [num_seqs]")
+    return dev, code, desc, err, shape, table
+
+
+def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, k_scale: float, v_scale: float,
+                  window: int | None = None, num_sinks: int = 0, key=None, value=None, err_flag=None, stream=None,
+                  desc: pa_cache_desc | None = None, alibi_slopes=None, test_flags: int = 0) -> None:
+    """A decode step over a 4-bit cache (see fp4_cache): out[s, h] = softmax(scale * q[s, h] K_s^T) V_s over the last
+    ``window`` (None: all) and the first ``num_sinks`` positions.  out, q [num_seqs, num_q_heads, 128] fp16 or bf16;
+    ``key`` / ``value`` [num_seqs, num_kv_heads, 128]: each sequence's new token, stored at position seq_lens[s] - 1 as
+    pa_reshape_and_cache_fp4 does and attended in the same launch.  No workspace."""
+    where = "pa_decode_fp4"
+    dev, code, desc, err, shape, table = _attention_fp4(where, True, out, q, k_cache, v_cache, block_tables, seq_lens,
+                                                        err_flag, desc)
+    if table[0] != shape[0]:
+        raise ValueError(f"{where}: one query per sequence")
+    kp = vp = slopes = None
+    if key is not None or value is not None:
+        if key is None or value is None:
+            raise ValueError(f"{where}: key and value go together")
+        if not (key.dtype is q.dtype and value.dtype is q.dtype and key.get_device() == dev and value.get_device() == dev):
+            _refuse(where, dev, True, (key, "key", q.dtype), (value, "value", q.dtype))
+        new = (shape[0], desc.num_kv_heads, 128)
+        if key.shape != new or value.shape != new or not (key.is_contiguous() and value.is_contiguous()):
+            raise ValueError(f"{where}: key and value must be {list(new)}, contiguous")
+        kp, vp = key.data_ptr(), value.data_ptr()
+    if alibi_slopes is not None:
+        import torch
+        _refuse(where, dev, True, (alibi_slopes, "alibi_slopes", torch.float32))
+        if alibi_slopes.numel() != shape[1] or not alibi_slopes.is_contiguous():
+            raise ValueError(f"{where}: one ALiBi slope per query head")
+        slopes = alibi_slopes.data_ptr()
+    _launch(lib().pa_decode_fp4, dev, (
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, block_tables.data_ptr(),
+        seq_lens.data_ptr(), shape[0], shape[1], table[1], desc, code, float(scale),
+        _INT32_MAX if window is None else _int32(window), _int32(num_sinks), float(k_scale), float(v_scale), slopes,
+        int(test_flags), err, _stream_of(dev, stream)), where)
+
+
+def pa_prefill_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_query_len: int, scale: float,
+                   k_scale: float, v_scale: float, window: int | None = None, num_sinks: int = 0, err_flag=None, stream=None,
+                   desc: pa_cache_desc | None = None) -> None:
+    """Attention of a chunk of new tokens over a 4-bit cache that already holds them: the queries
+    q[query_start[s]:query_start[s + 1]] are the last n_s of seq_lens[s] tokens; the one at position p sees the positions
+    up to p, or the last ``window`` of them and the first ``num_sinks``.  Other arguments as for pa_decode_fp4 and
+    pa_prefill_window."""
+    import torch
+    where = "pa_prefill_fp4"
+    dev, code, desc, err, shape, table = _attention_fp4(where, False, out, q, k_cache, v_cache, block_tables, seq_lens,
+                                                        err_flag, desc)
+    if query_start.dtype is not torch.int32 or query_start.get_device() != dev:
+        _refuse(where, dev, False, (query_start, "query_start", torch.int32))
+    if query_start.dim() != 1 or query_start.shape[0] != table[0] + 1 or not query_start.is_contiguous():
+        raise ValueError(f"{where}: query_start must be [num_seqs + 1]")
+    _launch(lib().pa_prefill_fp4, dev, (
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), query_start.data_ptr(), table[0], shape[0], shape[1], table[1],
+        min(_int32(max_query_len), shape[0]), desc, code, float(scale), _INT32_MAX if window is None else _int32(window),
+        _int32(num_sinks), float(k_scale), float(v_scale), err, _stream_of(dev, stream)), where)
+
+
+# ---------------------------------------------------------------- block tables on the GPU
+def _tables(where, block_tables, seq_lens, held_blocks, free_blocks, num_free, wanted, err_flag):
+    """The checks of both calls: (device, address of err_flag, num_seqs, max_blocks_per_seq)."""
+    import torch
+    dev, i32 = block_tables.get_device(), torch.int32
+    if dev < 0:
+        raise ValueError(f"{where}: the tables must be CUDA tensors")
+    for t, name in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (held_blocks, "held_blocks"),
+                    (free_blocks, "free_blocks"), (num_free, "num_free"), (wanted, "new_tokens / keep_lens")):
+        if t.dtype is not i32 or t.get_device() != dev:
+            _refuse(where, dev, False, (t, name, i32))
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+    if block_tables.dim() != 2 or num_free.numel() != 1:
+        raise ValueError(f"{where}: block_tables must be [num_seqs, max_blocks_per_seq], num_free one number")
+    n, width = block_tables.shape
+    if seq_lens.numel() != n or held_blocks.numel() != n or wanted.numel() != n:
+        raise ValueError(f"{where}: seq_lens, held_blocks and the tokens wanted must hold {n} requests")
+    err = None
+    if err_flag is not None:
+        _refuse(where, dev, False, (err_flag, "err_flag", i32))
+        err = err_flag.data_ptr()
+    return dev, err, n, width
+
+
+def pa_tables_extend(block_tables, seq_lens, held_blocks, free_blocks, num_free, new_tokens, slot_mapping, positions,
+                     query_start, block_size: int, err_flag=None, stream=None) -> None:
+    """Give request s new_tokens[s] more tokens: fresh blocks from the stack free_blocks[:num_free] into its row of
+    block_tables, seq_lens, held_blocks and num_free moved on, and for every new token its slot (int64), its position,
+    and where its request's rows start (query_start [num_seqs + 1]).  Rows past the last new token get slot -1.
+    All state is int32 on the GPU and changed in place; if the requests do not fit, nothing changes and err_flag says why
+    (6 or 7, see PA_DEVERR)."""
+    import torch
+    where = "pa_tables_extend"
+    dev, err, n, width = _tables(where, block_tables, seq_lens, held_blocks, free_blocks, num_free, new_tokens, err_flag)
+    rows = slot_mapping.numel()
+    if not (slot_mapping.dtype is torch.int64 and positions.dtype is torch.int32 and query_start.dtype is torch.int32 and
+            slot_mapping.get_device() == dev and positions.get_device() == dev and query_start.get_device() == dev):
+        _refuse(where, dev, False, (slot_mapping, "slot_mapping", torch.int64), (positions, "positions", torch.int32),
+                (query_start, "query_start", torch.int32))
+    if positions.numel() != rows or query_start.numel() != n + 1 or \
+            not (slot_mapping.is_contiguous() and positions.is_contiguous() and query_start.is_contiguous()):
+        raise ValueError(f"{where}: slot_mapping and positions must have the same rows, query_start {n + 1}, contiguous")
+    _launch(lib().pa_tables_extend, dev, (
+        block_tables.data_ptr(), seq_lens.data_ptr(), held_blocks.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
+        new_tokens.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), query_start.data_ptr(), n, rows, width,
+        _int32(block_size), free_blocks.numel(), err, _stream_of(dev, stream)), where)
+
+
+def pa_tables_trim(block_tables, seq_lens, held_blocks, free_blocks, num_free, keep_lens, block_size: int, err_flag=None,
+                   stream=None) -> None:
+    """Keep the first keep_lens[s] tokens of request s (drafts rejected; 0: the request is done): the blocks past them go
+    back on the stack.  State and errors as for pa_tables_extend."""
+    where = "pa_tables_trim"
+    dev, err, n, width = _tables(where, block_tables, seq_lens, held_blocks, free_blocks, num_free, keep_lens, err_flag)
+    _launch(lib().pa_tables_trim, dev, (
+        block_tables.data_ptr(), seq_lens.data_ptr(), held_blocks.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
+        keep_lens.data_ptr(), n, width, _int32(block_size), free_blocks.numel(), err, _stream_of(dev, stream)), where)

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "pa.h"
+#include "pa_fp4.h"
 #include "pa_internal.h"
 
 namespace pa {
@@ -356,14 +357,16 @@ int pa_reshape_and_cache_fp8(void* k_cache, void* v_cache, const void* key, cons
 
 int pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pairs, int32_t num_pairs,
                    const pa_cache_desc* cache, int32_t* err_flag, void* stream) {
-  int rc = check_cache(cache);
+  const bool fp4 = cache != nullptr && cache->dtype == PA_FP4_E2M1;
+  int rc = fp4 ? check_cache_fp4(cache) : check_cache(cache);
   if (rc != PA_OK) return rc;
   if (num_pairs < 0) return PA_ERR_INVALID_ARG;
   if (num_pairs == 0) return PA_OK;
   if (k_cache == nullptr || v_cache == nullptr || block_pairs == nullptr) return PA_ERR_NULL_POINTER;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_pairs, 4)) return PA_ERR_MISALIGNED;
   const int64_t block_bytes =
-      (int64_t)cache->num_kv_heads * cache->block_size * cache->head_size * elem_bytes(cache->dtype);
+      (int64_t)cache->num_kv_heads * cache->block_size *
+      (fp4 ? pa::kFp4TileBytes / pa::kFp4Tokens : cache->head_size * elem_bytes(cache->dtype));
   const int64_t pieces = (block_bytes + 16383) / 16384;
   if (pieces * num_pairs > kInt32Max) return PA_ERR_TOO_LARGE;
   cudaError_t e = pa::launch_copy_blocks(k_cache, v_cache, block_pairs, num_pairs, cache->num_blocks, block_bytes,

@@ -1,0 +1,45 @@
+// pa_fp4.h - caches held in 4 bits: layout and launchers (not part of the public ABI).
+#pragma once
+
+#include "pa_rope.h"
+#include "pa_window.h"
+
+namespace pa {
+
+// Of each (block, kv head), every 16 tokens are one tile: [16][64] bytes of codes, then [16][8] scales.
+constexpr int kFp4D = 128;
+constexpr int kFp4Tokens = 16;
+constexpr int kFp4RowBytes = kFp4D / 2;
+constexpr int kFp4RowScales = kFp4D / 16;
+constexpr int kFp4CodeBytes = kFp4Tokens * kFp4RowBytes;
+constexpr int kFp4TileBytes = kFp4CodeBytes + kFp4Tokens * kFp4RowScales;
+
+struct Fp4Rows {
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  void* key;    // [T][Hkv][D], 16 bits; written by the read, else only read
+  void* value;
+  int64_t key_stride, value_stride;  // elements between tokens
+  const int64_t* slot_mapping;       // [T]
+  int32_t num_tokens, num_kv_heads, num_blocks, block_size;
+  float k_scale, v_scale;
+  int32_t* err_flag;                 // nullable
+};
+cudaError_t launch_fp4_write(int row_dtype, const Fp4Rows& p, cudaStream_t stream);
+cudaError_t launch_fp4_read(int row_dtype, const Fp4Rows& p, cudaStream_t stream);
+// rotary positions with the write (p.positions: one row of num_tokens for each axis)
+cudaError_t launch_fp4_rope(int row_dtype, bool interleaved, const RopeAxesParams& p, cudaStream_t stream);
+
+// rows attention (see pa_window.h); row_dtype: of q, out and the appended rows
+cudaError_t launch_fp4_rows(int row_dtype, const WindowParams& p, bool slots, cudaStream_t stream);
+
+// the same with the split of a windowed call chosen (a PA_* status)
+int fp4_rows(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, cudaStream_t stream);
+
+namespace host {
+int check_cache_fp4(const pa_cache_desc* c);
+// A cache's unit: such that six times it, its product with any scale and the inverse of that are ordinary fp32 numbers.
+bool fp4_unit_ok(float x);
+}
+
+}  // namespace pa

@@ -37,10 +37,12 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pa.h"
 #include "pa_device.cuh"
 #include "pa_rope.h"
+#include "pa_rope_angle.cuh"
 
 namespace pa {
 namespace {
@@ -86,15 +88,6 @@ struct alignas(sizeof(T) * V) Vec {
     }
   }
 };
-
-// f / 2 pi as a fraction of a turn in units of 2^-64 (whole turns per position drop out)
-__device__ __forceinline__ unsigned long long turn_fraction(double f) {
-  const double t = f * 0.15915494309189533577;  // 1 / 2 pi
-  const double frac = t - floor(t);             // [0, 1]
-  const unsigned long long hi = (unsigned long long)(frac * 4294967296.0);  // < 2^33: wraps below
-  const double rest = frac * 4294967296.0 - (double)hi;
-  return (hi << 32) + (unsigned long long)(rest * 4294967296.0);
-}
 
 // E4M3 code of x / scale (fp32 division, ties to even, saturating)
 __device__ __forceinline__ uint8_t code_of(float x, float scale) {
@@ -225,8 +218,11 @@ __device__ __forceinline__ void fp8_values(const RopeParams& p, int t0, int n, i
 }
 
 // T: queries, keys, values; FP8: the cache holds E4M3 codes (else T); V: elements of a vector
-template <typename T, bool FP8, bool INTERLEAVED, int V>
-__global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_kernel(const RopeParams p, const RopePlan plan) {
+// Params: RopeParams, or RopeAxesParams: the angle of pair j then goes by the token's position along the pair's axis.
+template <typename Params, typename T, bool FP8, bool INTERLEAVED, int V>
+__global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_kernel(const Params p, const RopePlan plan) {
+  constexpr bool kAxes = std::is_same<Params, RopeAxesParams>::value;
+  constexpr int kPos = kAxes ? kMaxAxes : 1;
   // (c, s) of token, pair; two groups in turn (FP8: or the values' codes)
   constexpr int kBatch = kUnits<T, V>;
   constexpr int kCs = kMaxGroup * kMaxHalf, kCodes = FP8 ? kRopeWarps * kValueTokens * kCodeRow / 16 : 0;
@@ -263,14 +259,21 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
     const unsigned long long f = j < half ? turn_fraction(p.inv_freq[j]) : 0ull;
     // lane t: slot and position of token t of a group, loaded a group ahead
     const int lane = threadIdx.x & 31;
-    auto fetch = [&](int group, long long& slot, int& position) {
+    auto fetch = [&](int group, long long& slot, int (&position)[kPos]) {
       const long long t = (long long)group * plan.tokens + lane;
       const bool real = lane < plan.tokens && t < p.num_tokens;
       slot = real ? p.slot_mapping[t] : -1;
-      position = real ? p.positions[t] : 0;
+      position[0] = real ? p.positions[t] : 0;
+      if constexpr (kAxes) {
+#pragma unroll
+        for (int a = 1; a < kPos; ++a)
+          position[a] = real && a < p.num_axes ? p.positions[(long long)a * p.num_tokens + t] : 0;
+      }
     };
+    [[maybe_unused]] int axis = 0;
+    if constexpr (kAxes) axis = j < half ? p.axis[j] : 0;
     long long slot;
-    int position, buf = 0;
+    int position[kPos], buf = 0;
     fetch(first, slot, position);
     for (int group = first; group < plan.groups; group += step, buf ^= 1) {
       const int nt = min(plan.tokens, p.num_tokens - group * plan.tokens);
@@ -286,13 +289,15 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
         tok_all[buf][j] = row;
       }
       for (int t = tok_lo; t < min(nt, tok_hi); ++t) {
-        const long long at = __shfl_sync(0xffffffffu, position, t);
-        if (j < half) {
-          const long long turns = (long long)(f * (unsigned long long)at);
-          float s, c;
-          sincospif(__ll2float_rn(turns) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns in [-1, 1]
-          cs_all[buf][t * kMaxHalf + cs_at(j / V, j % V)] = make_float2(c * p.magnitude, s * p.magnitude);
+        int own = __shfl_sync(0xffffffffu, position[0], t);
+        if constexpr (kAxes) {
+#pragma unroll
+          for (int a = 1; a < kPos; ++a) {
+            const int other = __shfl_sync(0xffffffffu, position[a], t);
+            own = axis == a ? other : own;
+          }
         }
+        if (j < half) cs_all[buf][t * kMaxHalf + cs_at(j / V, j % V)] = turn_of(f, own, p.magnitude);
       }
       fetch(group + step, slot, position);
       __syncthreads();
@@ -399,8 +404,8 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
   }
 }
 
-template <typename T, bool FP8, bool INTERLEAVED, int V>
-cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
+template <typename T, bool FP8, bool INTERLEAVED, int V, typename Params>
+cudaError_t launch_vec(const Params& p, cudaStream_t stream) {
   RopePlan plan;
   const int per_head = p.head_size / (2 * V);
   plan.log2_per_head = 0;
@@ -438,12 +443,12 @@ cudaError_t launch_vec(const RopeParams& p, cudaStream_t stream) {
       ((long long)p.num_tokens + plan.value_tokens - 1) / plan.value_tokens * p.num_kv_heads;
   plan.value_ctas = FP8 ? (int)((value_warps + kRopeWarps - 1) / kRopeWarps) : 0;
   const int grid = plan.value_ctas + (int)std::min(groups(plan.tokens), walkers(plan.parts)) * plan.parts;
-  return launch_dependent(rope_kernel<T, FP8, INTERLEAVED, V>, dim3((unsigned)grid), dim3(kRopeThreads + kMaxHalf), 0, stream, p,
+  return launch_dependent(rope_kernel<Params, T, FP8, INTERLEAVED, V>, dim3((unsigned)grid), dim3(kRopeThreads + kMaxHalf), 0, stream, p,
                           plan);
 }
 
-template <typename T, bool FP8, int VMAX>
-cudaError_t launch_type(bool interleaved, const RopeParams& p, cudaStream_t stream) {
+template <typename T, bool FP8, int VMAX, typename Params>
+cudaError_t launch_type(bool interleaved, const Params& p, cudaStream_t stream) {
   if (interleaved) return launch_vec<T, FP8, true, VMAX>(p, stream);
   // halves: vectors that neither half of the pairs cuts
   const int half = p.rotary_dim / 2;
@@ -453,14 +458,23 @@ cudaError_t launch_type(bool interleaved, const RopeParams& p, cudaStream_t stre
   return launch_vec<T, FP8, false, 1>(p, stream);
 }
 
-}  // namespace
-
-cudaError_t launch_rope(int dtype, bool interleaved, const RopeParams& p, cudaStream_t stream) {
+template <typename Params>
+cudaError_t launch_dtype(int dtype, bool interleaved, const Params& p, cudaStream_t stream) {
   if (dtype == PA_F32) return launch_type<float, false, 4>(interleaved, p, stream);
   if (dtype == PA_F16) return launch_type<__half, false, 8>(interleaved, p, stream);
   if (dtype == PA_BF16) return launch_type<__nv_bfloat16, false, 8>(interleaved, p, stream);
   if (dtype == PA_FP8_E4M3) return launch_type<__half, true, 8>(interleaved, p, stream);
   return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_rope(int dtype, bool interleaved, const RopeParams& p, cudaStream_t stream) {
+  return launch_dtype(dtype, interleaved, p, stream);
+}
+
+cudaError_t launch_rope_axes(int dtype, bool interleaved, const RopeAxesParams& p, cudaStream_t stream) {
+  return launch_dtype(dtype, interleaved, p, stream);
 }
 
 }  // namespace pa

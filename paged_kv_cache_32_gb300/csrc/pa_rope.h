@@ -23,7 +23,15 @@ struct RopeParams {
   int32_t* err_flag;            // nullable
 };
 
+// Positions along several axes: positions is [axes][T], and pair j goes by the axis axis[j].
+constexpr int kMaxAxes = 4;
+struct RopeAxesParams : RopeParams {
+  uint8_t axis[64];
+  int32_t num_axes;
+};
+
 // dtype: the cache's (fp16 queries, keys and values for an FP8 cache)
 cudaError_t launch_rope(int dtype, bool interleaved, const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_rope_axes(int dtype, bool interleaved, const RopeAxesParams& p, cudaStream_t stream);
 
 }  // namespace pa

@@ -1,0 +1,308 @@
+// pa_tables.cu - block tables and slot maps kept on the GPU: requests grow by new tokens (extend) and fall back to fewer
+// (trim), blocks come from and go back to a stack.
+//
+// With L_s tokens, h_s blocks held and n_s new tokens of request s, extend needs a_s = max(0, ceil((L_s + n_s) / B) - h_s)
+// blocks.  Sums over the requests before s, Q_s of n and P_s of a, place everything: new token j of s is row Q_s + j of the
+// slot map, its i-th fresh block is entry F - 1 - (P_s + i) of the stack of F blocks.  Trim to k_s tokens releases
+// g_s = h_s - ceil(k_s / B) blocks; with sums R_s of g and R of all, its i-th one becomes entry F + R - 1 - (R_s + i), so
+// that an extend by as much hands every request its own blocks again.
+//
+// Bound by latency: a step's requests are a few KB.  Every CTA adds up all requests (each thread a run of them) and keeps
+// the sums in shared memory, so that none waits for another before it writes its rows, each of which finds its request
+// by bisection.  The lengths, read by all, are written last: after a barrier of the cluster that a small call runs in,
+// or by a second kernel.  Neither kernel lets a dependent launch start early: the decode kernels read lengths and tables
+// before they wait for the kernel in front of them.
+#include <algorithm>
+
+#include "pa.h"
+#include "pa_cluster.cuh"
+#include "pa_device.cuh"
+#include "pa_launch.h"
+
+using namespace pa::host;
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kMaxSeqs = 16384;      // whose sums fit shared memory
+constexpr int kMaxTablesCluster = 8;
+
+struct TablesParams {
+  int32_t* block_tables;     // [N][M]
+  int32_t* seq_lens;         // [N]
+  int32_t* held;             // [N]
+  int32_t* free_blocks;      // [num_blocks], entries 0 .. num_free - 1 the stack
+  int32_t* num_free;         // [1]
+  const int32_t* wanted;     // [N]: new tokens (extend), tokens kept (trim)
+  int64_t* slot_mapping;     // extend: [num_rows]
+  int32_t* positions;        // extend: [num_rows]
+  int32_t* query_start;      // extend: [N + 1]
+  int32_t num_seqs, num_rows, max_blocks, block_size, num_blocks;
+  int32_t* err_flag;         // nullable
+};
+
+struct Request {
+  int len, held, wanted;
+  int blocks;  // fresh ones, or released ones
+  bool bad;
+};
+
+template <bool kTrim>
+__device__ __forceinline__ Request request(const TablesParams& p, int s) {
+  Request r = {p.seq_lens[s], p.held[s], p.wanted[s], 0, false};
+  const int B = p.block_size;
+  const long long room = (long long)p.max_blocks * B;
+  const long long after = kTrim ? r.wanted : (long long)r.len + r.wanted;
+  r.bad = r.len < 0 || r.held < 0 || r.held > p.max_blocks || (long long)r.held * B < r.len || r.wanted < 0 ||
+          after > (kTrim ? (long long)r.len : room);
+  if (!r.bad) {
+    const int need = (int)((after + B - 1) / B);
+    r.blocks = kTrim ? r.held - need : max(0, need - r.held);
+  }
+  return r;
+}
+
+// Sums of a call, the same in every CTA.
+struct Sums {
+  long long rows, blocks;  // of all requests
+  int free;                // blocks on the stack before the call
+  bool ok;
+};
+
+// Called by all threads.  rows_of, blocks_of (nullable): [N + 1], the sums over the requests before each one.
+template <bool kTrim>
+__device__ __forceinline__ Sums add_up(const TablesParams& p, long long* scratch, int* rows_of, int* blocks_of) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int run = (p.num_seqs + kThreads - 1) / kThreads;
+  const int begin = min(p.num_seqs, run * (int)threadIdx.x), end = min(p.num_seqs, begin + run);
+  long long rows = 0, blocks = 0;
+  bool bad = false;
+  for (int s = begin; s < end; ++s) {
+    const Request r = request<kTrim>(p, s);
+    bad = bad || r.bad;
+    rows += r.bad ? 0 : r.wanted;
+    blocks += r.blocks;
+  }
+  long long rows_to = rows, blocks_to = blocks;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, rows_to, off), y = __shfl_up_sync(0xffffffffu, blocks_to, off);
+    if (lane >= off) rows_to += x, blocks_to += y;
+  }
+  if (lane == 31) scratch[2 * warp] = rows_to, scratch[2 * warp + 1] = blocks_to;
+  bad = __syncthreads_or(bad);
+  Sums sums = {0, 0, *p.num_free, false};
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) rows_to += scratch[2 * w], blocks_to += scratch[2 * w + 1];
+    sums.rows += scratch[2 * w];
+    sums.blocks += scratch[2 * w + 1];
+  }
+  const bool state = !bad && sums.free >= 0 && sums.free <= p.num_blocks;
+  sums.ok = state && (kTrim ? sums.free + sums.blocks <= p.num_blocks
+                            : sums.blocks <= sums.free && sums.rows <= p.num_rows);
+  if (sums.ok && blocks_of != nullptr) {
+    int q = (int)(rows_to - rows), b = (int)(blocks_to - blocks);
+    for (int s = begin; s < end; ++s) {
+      const Request r = request<kTrim>(p, s);
+      if (rows_of != nullptr) rows_of[s] = q;
+      blocks_of[s] = b;
+      q += r.wanted;
+      b += r.blocks;
+    }
+    if (threadIdx.x == 0) {
+      if (rows_of != nullptr) rows_of[p.num_seqs] = (int)sums.rows;
+      blocks_of[p.num_seqs] = (int)sums.blocks;
+    }
+  }
+  __syncthreads();
+  return sums;
+}
+
+// the last request whose sum is at most x (x below the total: the one that x belongs to)
+__device__ __forceinline__ int owner(const int* of, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (of[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// One CTA: the new lengths, or the error.
+template <bool kTrim>
+__device__ __forceinline__ void commit(const TablesParams& p, const Sums& sums) {
+  if (!sums.ok) {
+    if (threadIdx.x == 0) {
+      const bool short_of_blocks = !kTrim && sums.free >= 0 && sums.free <= p.num_blocks && sums.blocks > sums.free;
+      report_error(p.err_flag, short_of_blocks ? PA_DEVERR_NO_BLOCKS : PA_DEVERR_TABLES);
+    }
+    return;
+  }
+  for (int s = threadIdx.x; s < p.num_seqs; s += kThreads) {
+    const Request r = request<kTrim>(p, s);
+    p.seq_lens[s] = kTrim ? r.wanted : r.len + r.wanted;
+    p.held[s] = kTrim ? r.held - r.blocks : r.held + r.blocks;
+  }
+  if (threadIdx.x == 0) p.num_free[0] = kTrim ? sums.free + (int)sums.blocks : sums.free - (int)sums.blocks;
+}
+
+// every CTA of the one cluster has read the lengths
+__device__ __forceinline__ void all_read() {
+  if (gridDim.x > 1) cluster_sync_all();
+  else __syncthreads();
+}
+
+// kAlone: the grid is one cluster, which writes the lengths too (else commit_kernel does).
+template <bool kAlone>
+__global__ void __launch_bounds__(kThreads) extend_kernel(const TablesParams p) {
+  extern __shared__ int sums_of[];  // rows before each request, then blocks
+  __shared__ long long scratch[2 * kThreads / 32];
+  int* rows_of = sums_of;
+  int* blocks_of = sums_of + p.num_seqs + 1;
+  griddep_wait();
+  const Sums sums = add_up<false>(p, scratch, rows_of, blocks_of);
+  const int B = p.block_size, total = sums.ok ? (int)sums.rows : 0;
+  for (int s = blockIdx.x * kThreads + threadIdx.x; s <= p.num_seqs; s += gridDim.x * kThreads)
+    p.query_start[s] = sums.ok ? rows_of[s] : 0;
+  for (long long t = (long long)blockIdx.x * kThreads + threadIdx.x; t < p.num_rows; t += (long long)gridDim.x * kThreads) {
+    long long slot = -1;
+    int pos = 0;
+    if (t < total) {
+      const int s = owner(rows_of, p.num_seqs, (int)t);
+      const int held = p.held[s];
+      pos = p.seq_lens[s] + (int)t - rows_of[s];
+      const int b = pos / B, off = pos - b * B;
+      int32_t* entry = p.block_tables + (long long)s * p.max_blocks + b;
+      int block;
+      if (b < held) {
+        block = *entry;
+      } else {
+        block = p.free_blocks[sums.free - 1 - (blocks_of[s] + b - held)];
+        if (off == 0) *entry = block;  // (a fresh block's first token is new: the blocks held hold the others)
+      }
+      if (block >= 0 && block < p.num_blocks) slot = (long long)block * B + off;
+      else report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+    }
+    p.slot_mapping[t] = slot;
+    p.positions[t] = pos;
+  }
+  if constexpr (kAlone) {
+    all_read();
+    if (blockIdx.x == 0) commit<false>(p, sums);
+  }
+  __threadfence();  // see the file comment
+}
+
+template <bool kAlone>
+__global__ void __launch_bounds__(kThreads) trim_kernel(const TablesParams p) {
+  extern __shared__ int blocks_of[];
+  __shared__ long long scratch[2 * kThreads / 32];
+  griddep_wait();
+  const Sums sums = add_up<true>(p, scratch, nullptr, blocks_of);
+  const int B = p.block_size, total = sums.ok ? (int)sums.blocks : 0;
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
+    const int s = owner(blocks_of, p.num_seqs, i);
+    const int kept = (int)(((long long)p.wanted[s] + B - 1) / B);
+    int32_t* entry = p.block_tables + (long long)s * p.max_blocks + kept + (i - blocks_of[s]);
+    const int block = *entry;
+    if (block < 0 || block >= p.num_blocks) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+    p.free_blocks[sums.free + total - 1 - i] = block;
+    *entry = -1;
+  }
+  if constexpr (kAlone) {
+    all_read();
+    if (blockIdx.x == 0) commit<true>(p, sums);
+  }
+  __threadfence();
+}
+
+template <bool kTrim>
+__global__ void __launch_bounds__(kThreads) commit_kernel(const TablesParams p) {
+  __shared__ long long scratch[2 * kThreads / 32];
+  griddep_wait();
+  const Sums sums = add_up<kTrim>(p, scratch, nullptr, nullptr);
+  commit<kTrim>(p, sums);
+  __threadfence();
+}
+
+// work: rows (extend), or blocks that a call may release (trim), at most
+template <bool kTrim>
+cudaError_t launch(const TablesParams& p, long long work, cudaStream_t stream) {
+  const size_t smem = (size_t)(p.num_seqs + 1) * sizeof(int) * (kTrim ? 1 : 2);
+  auto alone = kTrim ? trim_kernel<true> : extend_kernel<true>;
+  auto grid = kTrim ? trim_kernel<false> : extend_kernel<false>;
+  const long long ctas = std::max(1ll, (work + 4 * kThreads - 1) / (4 * kThreads));
+  const bool one = kTrim || ctas <= kMaxTablesCluster;
+  cudaError_t e = cudaFuncSetAttribute(one ? alone : grid, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  if (one) {
+    int cluster = 1;
+    while (cluster < kMaxTablesCluster && cluster < ctas) cluster *= 2;
+    return launch_cluster(alone, dim3((unsigned)cluster), dim3(kThreads), smem, cluster, true, stream, p);
+  }
+  e = launch_cluster(grid, dim3((unsigned)std::min(ctas, 304ll)), dim3(kThreads), smem, 1, true, stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(commit_kernel<kTrim>, dim3(1), dim3(kThreads), 0, 1, true, stream, p);
+}
+
+// Checks that both calls share.
+int check_tables(const TablesParams& p) {
+  if (p.num_seqs < 0 || p.max_blocks < 0 || p.block_size <= 0 || p.num_blocks < 0 || p.num_rows < 0)
+    return PA_ERR_INVALID_ARG;
+  if (p.num_seqs > kMaxSeqs || (int64_t)p.max_blocks * p.block_size > kInt32Max) return PA_ERR_TOO_LARGE;
+  if (p.num_seqs == 0 && p.num_rows == 0) return PA_OK;
+  if ((p.num_seqs > 0 && (p.seq_lens == nullptr || p.held == nullptr || p.wanted == nullptr ||
+                          (p.block_tables == nullptr && p.max_blocks > 0))) ||
+      p.num_free == nullptr || (p.free_blocks == nullptr && p.num_blocks > 0))
+    return PA_ERR_NULL_POINTER;
+  if (!aligned(p.block_tables, 4) || !aligned(p.seq_lens, 4) || !aligned(p.held, 4) || !aligned(p.free_blocks, 4) ||
+      !aligned(p.num_free, 4) || !aligned(p.wanted, 4))
+    return PA_ERR_MISALIGNED;
+  return PA_OK;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+int pa_tables_extend(int32_t* block_tables, int32_t* seq_lens, int32_t* held_blocks, const int32_t* free_blocks,
+                     int32_t* num_free, const int32_t* new_tokens, int64_t* slot_mapping, int32_t* positions,
+                     int32_t* query_start, int32_t num_seqs, int32_t num_rows, int32_t max_blocks_per_seq,
+                     int32_t block_size, int32_t num_blocks, int32_t* err_flag, void* stream) {
+  const pa::TablesParams p = {block_tables, seq_lens,     held_blocks, const_cast<int32_t*>(free_blocks),
+                              num_free,     new_tokens,   slot_mapping, positions,
+                              query_start,  num_seqs,     num_rows,    max_blocks_per_seq,
+                              block_size,   num_blocks,   err_flag};
+  const int rc = pa::check_tables(p);
+  if (rc != PA_OK || (num_seqs == 0 && num_rows == 0)) return rc;
+  if (query_start == nullptr || (num_rows > 0 && (slot_mapping == nullptr || positions == nullptr)))
+    return PA_ERR_NULL_POINTER;
+  if (!aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(query_start, 4)) return PA_ERR_MISALIGNED;
+  return pa::launch<false>(p, num_rows, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_tables_trim(int32_t* block_tables, int32_t* seq_lens, int32_t* held_blocks, int32_t* free_blocks,
+                   int32_t* num_free, const int32_t* keep_lens, int32_t num_seqs, int32_t max_blocks_per_seq,
+                   int32_t block_size, int32_t num_blocks, int32_t* err_flag, void* stream) {
+  pa::TablesParams p = {};
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.held = held_blocks;
+  p.free_blocks = free_blocks;
+  p.num_free = num_free;
+  p.wanted = keep_lens;
+  p.num_seqs = num_seqs;
+  p.max_blocks = max_blocks_per_seq;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.err_flag = err_flag;
+  const int rc = pa::check_tables(p);
+  if (rc != PA_OK || num_seqs == 0) return rc;
+  const long long work = std::min((long long)num_blocks, (long long)num_seqs * max_blocks_per_seq);
+  return pa::launch<true>(p, work, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "pa.h"
+#include "pa_fp4.h"
 #include "pa_prefill.h"
 #include "pa_window.h"
 
@@ -120,8 +121,9 @@ bool encode_slab_map(CUtensorMap* map, const void* base, const pa_cache_desc* c,
 // 1620 / 7890; fp32 rows 602 / 718, 2845 / 5120, 7080 / 46200.
 bool mixes(long long items, long long real) { return items > kFewItems && items > 4 * real; }
 
-// Launches the rows kernel of the cache's type; p.tiles (row groups), p.cluster and p.warps are set here.
-int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t stream) {
+// Launches the rows kernel of the cache's type (row_dtype: of queries and outputs over a 4-bit cache); p.tiles (row
+// groups), p.cluster and p.warps are set here.
+int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t stream, int32_t row_dtype = PA_F16) {
   const long long rows = (long long)p.max_query_len * (p.num_q_heads / p.num_kv_heads);
   if (rows > kInt32Max - 8) return PA_ERR_TOO_LARGE;
   p.tiles = (int32_t)((rows + 7) / 8);
@@ -140,6 +142,8 @@ int launch_rows(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t st
   cudaError_t e;
   if (cache->dtype == PA_F32) {
     e = pa::launch_window_rows_f32(cache->head_size, p, slots, stream);
+  } else if (cache->dtype == PA_FP4_E2M1) {
+    e = pa::launch_fp4_rows(row_dtype, p, slots, stream);
   } else if (cache->dtype == PA_FP8_E4M3) {
     CUtensorMap tk, tk32;
     if (!encode_fp8_key_map(&tk, p.k_cache, cache, pa::kTcSlabTokens) ||
@@ -274,6 +278,14 @@ pa::WindowParams base_params(const pa_cache_desc* cache, void* out, const void* 
 }
 
 }  // namespace
+
+namespace pa {
+
+int fp4_rows(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, cudaStream_t stream) {
+  return launch_rows(cache, p, stream, row_dtype);
+}
+
+}  // namespace pa
 
 extern "C" {
 
