@@ -61,6 +61,15 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float (&x)[8], float inv) {
   return y;
 }
 
+// A bf16 query row whose largest magnitude is mx becomes fp16 after a multiplication by `down`, a power of two that brings
+// mx into [1, 2) (mx subnormal: below); `up` is its inverse.  1 for a row with an infinity or a NaN.
+__device__ __forceinline__ void row_power(float mx, float& up, float& down) {
+  const int e = mx < INFINITY ? max((int)(__float_as_uint(mx) >> 23), 1) : 127;
+  up = __uint_as_float((uint32_t)e << 23);
+  // 2^(127 - e); 2^-127, for an element past 2^127, has no normal fp32 form
+  down = e < 254 ? __uint_as_float((uint32_t)(254 - e) << 23) : 5.877471754111438e-39f;
+}
+
 // A row's place in a cache: its 64 bytes of codes, and its 8 bytes of scales `kFp4CodeBytes` and so on behind the tile.
 __host__ __device__ __forceinline__ size_t fp4_tile(int64_t block, int num_kv_heads, int head, int block_size, int off) {
   return (((size_t)block * num_kv_heads + head) * (block_size / kFp4Tokens) + off / kFp4Tokens) * kFp4TileBytes;

@@ -33,8 +33,9 @@ cudaError_t launch_fp4_rope(int row_dtype, bool interleaved, const RopeAxesParam
 // rows attention (see pa_window.h); row_dtype: of q, out and the appended rows
 cudaError_t launch_fp4_rows(int row_dtype, const WindowParams& p, bool slots, cudaStream_t stream);
 
-// the same with the split of a windowed call chosen (a PA_* status)
+// a decode step, with the split of a windowed call chosen; a chunk, with its kernel chosen too (a PA_* status)
 int fp4_rows(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, cudaStream_t stream);
+int fp4_chunk(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, cudaStream_t stream);
 
 namespace host {
 int check_cache_fp4(const pa_cache_desc* c);

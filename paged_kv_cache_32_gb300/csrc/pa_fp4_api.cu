@@ -188,7 +188,7 @@ int pa_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_
   p.query_start = query_start;
   p.num_query_tokens = num_query_tokens;
   p.max_query_len = std::min(max_query_len, num_query_tokens);  // no valid chunk is longer
-  return pa::fp4_rows(cache, row_dtype, p, static_cast<cudaStream_t>(stream));
+  return pa::fp4_chunk(cache, row_dtype, p, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -269,11 +269,8 @@ __global__ void __launch_bounds__(RowsFp4Shape<NW, NS>::THREADS) fp4_rows_kernel
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fmaxf(fabsf(Mma<T>::lo(x[i])), fabsf(Mma<T>::hi(x[i]))));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // the power of two below the largest element (2^-126 at least; 1 for a row with an infinity)
-      const int e = mx < INFINITY ? max((int)(__float_as_uint(mx) >> 23), 1) : 127;
-      q_unit = __uint_as_float((uint32_t)e << 23);
-      const int down = 254 - e;  // 2^(127 - e); 2^-127, of an element past 2^127, has no normal fp32 form
-      const float inv = down > 0 ? __uint_as_float((uint32_t)down << 23) : 5.877471754111438e-39f;
+      float inv;
+      row_power(mx, q_unit, inv);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = Mma<__half>::pack(Mma<T>::lo(x[i]) * inv, Mma<T>::hi(x[i]) * inv);
     }

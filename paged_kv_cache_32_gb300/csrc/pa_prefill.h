@@ -28,7 +28,7 @@ struct PrefillParams {
   int32_t window, sinks, pack_log2;
   int32_t max_query_len;        // windowed form: bound on a chunk's queries
   int32_t split;                // windowed form: CTAs of a cluster that share one item's key tiles
-  // windowed form over an FP8 cache: a value code's scale (the key codes' is part of scale_log2)
+  // windowed form over an FP8 or a 4-bit cache: a value code's scale (the key codes' is part of scale_log2)
   float v_scale;
 };
 
@@ -46,5 +46,8 @@ bool encode_query_map(CUtensorMap* map, const void* base, const pa_cache_desc* c
 cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                               const CUtensorMap& to, const PrefillParams& p, bool mixed,
                               cudaStream_t stream);
+// over a 4-bit cache, windowed form; row_dtype: of q and out
+cudaError_t launch_prefill_fp4(int row_dtype, const CUtensorMap& tq, const CUtensorMap& to, const PrefillParams& p,
+                               bool mixed, cudaStream_t stream);
 
 }  // namespace pa

@@ -96,6 +96,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cfloat>
 #include <climits>
 #include <math.h>
 
@@ -104,6 +105,7 @@
 #include "pa.h"
 #include "pa_cluster.cuh"
 #include "pa_device.cuh"
+#include "pa_fp4.cuh"
 #include "pa_fp8.cuh"
 #include "pa_internal.h"
 #include "pa_launch.h"
@@ -120,7 +122,9 @@ constexpr int kVOff = 4 * kHalf;      // V stages: 2 x 2 regions
 constexpr int kQOff = 8 * kHalf;      // Q tiles of two items (item k in buffer k % 2): 2 x 2 regions
 constexpr int kOutOff = 12 * kHalf;   // one item's output tile, staged for a tensor-map store: 2 regions
 constexpr int kBarOff = 14 * kHalf;   // barriers, flags, the published work items
+constexpr int kUnitOff = kBarOff + 512;  // the power of two of each query row of two items (bf16 queries, 4-bit cache)
 constexpr int kSmemBytes = kBarOff + 512 + 1024;
+constexpr int kSmemBytesConvert = kSmemBytes + 2 * kTile * 4;
 constexpr int kSBufs = 3;             // S buffers in tensor memory (columns 128 b .. 128 b + 127)
 constexpr uint32_t kOCol = 384;       // tensor-memory column of O
 constexpr int kSoftmaxWarps = 8;
@@ -361,20 +365,21 @@ struct SeeCausal {
 };
 // P of 8 of the 16 key pairs this thread holds in each of its two rows, pairs j0 .. j0 + 7 (v in
 // the 16x256b layout over the tile's 128 columns: pair j = keys 8j + 2c, 8j + 2c + 1, c = thread % 4;
-// v[4j], v[4j + 1] row 0, v[4j + 2], v[4j + 3] row 1) from the raw scores, the scale in log2 units
+// v[4j], v[4j + 1] row 0, v[4j + 2], v[4j + 3] row 1) from the raw scores, the rows' scales in log2 units
 // and the rows' reference maxima; keys that `mask` excludes weigh nothing.  Writes the packed words of those pairs in the 16x128b layout (hi[2i] row 0, hi[2i + 1]
 // row 1 for pair j0 + i; for bf16 also lo) and adds the rows' sums of the unrounded weights to s0, s1.
 template <typename T, typename Mask>
-__device__ __forceinline__ void make_p(const float* v, int j0, float sl2, float mr0, float mr1, const Mask& mask,
+__device__ __forceinline__ void make_p(const float* v, int j0, float2 sl2, float mr0, float mr1, const Mask& mask,
                                        uint32_t* hi, uint32_t* lo, float& s0, float& s1) {
   constexpr bool kMasked = !std::is_same<Mask, SeeAll>::value;
   float2 acc0[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   float2 acc1[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  const float2 sc2 = make_float2(sl2, sl2), n0 = make_float2(-mr0, -mr0), n1 = make_float2(-mr1, -mr1);
+  const float2 sa = make_float2(sl2.x, sl2.x), sb = make_float2(sl2.y, sl2.y);
+  const float2 n0 = make_float2(-mr0, -mr0), n1 = make_float2(-mr1, -mr1);
 #pragma unroll
   for (int j = j0; j < j0 + 8; ++j) {
-    const float2 x = fma2(make_float2(v[4 * j], v[4 * j + 1]), sc2, n0);
-    const float2 y = fma2(make_float2(v[4 * j + 2], v[4 * j + 3]), sc2, n1);
+    const float2 x = fma2(make_float2(v[4 * j], v[4 * j + 1]), sa, n0);
+    const float2 y = fma2(make_float2(v[4 * j + 2], v[4 * j + 3]), sb, n1);
     float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y), p2 = fast_exp2(y.x), p3 = fast_exp2(y.y);
     if constexpr (kMasked) {
       p0 = mask.see0(8 * j) ? p0 : 0.f;
@@ -558,6 +563,18 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* src, bool take) {
   return v;
 }
 
+// two scale codes at src + OFF, or zeros (see load_codes)
+template <int OFF>
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* src, bool take) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b16 x;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 x, 0;\n\t"
+      "@p ld.global.nc.u16 x, [%1 + %3];\n\tcvt.u32.u16 %0, x;\n\t}"
+      : "=r"(v)
+      : "l"(src), "r"((int)take), "n"(OFF));
+  return v;
+}
+
 // A producer warp over an FP8 cache: of every tile, warps 0..3 take the keys 32 w .. 32 w + 31 of K (a lane 16 of a
 // row's 128 codes), warps 4..7 the same keys of V (a lane the 16 tokens of a group at one dimension).  A warp alone
 // on its scheduler takes some six cycles an instruction, hence eight warps and few instructions a vector; a group's
@@ -688,6 +705,146 @@ __device__ __forceinline__ void fp8_producer(const PrefillParams& p, int w, int 
   }
 }
 
+// A producer warp over a 4-bit cache: of every tile, warps 0..3 take the keys 32 w .. 32 w + 31 of K, warps 4..7 those of V;
+// a group is 16 keys, which lie in one block whatever its size (a multiple of 16).  A lane takes 16 bytes of a row (32
+// dimensions, two of its groups of 16) at a time with their two scales; a code times its scale is exact in fp16.  V lies
+// like K, tokens as rows, and P V takes it like the 16-bit caches' tiles.
+template <typename Item, bool kV>
+__device__ __forceinline__ void fp4_producer(const PrefillParams& p, int w, int lane, int idx0, int idx_step,
+                                             int n_items, uint8_t* ring, uint64_t* bar, uint64_t* freed,
+                                             volatile int* abort_flag) {
+  constexpr int kGroups = 2, kVecs = 2;  // groups of 16 keys of a warp and tile; 8-row vectors of a group
+  const int B = p.block_size;
+  // The lane's place in a vector of 8 rows: eight lanes whose stores go together hold four neighbouring rows of one
+  // 64-column half, which the swizzle puts into different banks.
+  const int c = (lane & 1) + 2 * ((lane >> 3) & 1), row = ((lane >> 1) & 3) + 4 * (lane >> 4);
+  const uint8_t* cache = static_cast<const uint8_t*>(kV ? p.v_cache : p.k_cache);
+  const int code_at = row * kFp4RowBytes + 16 * c, scale_at = kFp4CodeBytes + row * kFp4RowScales + 2 * c;
+  int at[kGroups];  // of its first 16 bytes in the tile: the four go to at ^ 16 k, the group's second vector 8 rows on
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g)
+    at[g] = (c >> 1) * kHalf + (int)swz128(16 * (kGroups * w + g) + row, 4 * (c & 1));
+  int tg = 0;
+  bool ok = true;
+  for (int idx = idx0; ok && idx < n_items; idx += idx_step) {
+    Item it;
+    if (!pf_item(p, idx, it, false)) {
+      idx += pf_skip(p, idx, idx_step, it, false);
+      continue;
+    }
+    const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
+    // lane l < 2: the table entry of the tile's group 2 w + l, INT_MIN if it has none, and its tile in the block
+    auto fetch = [&](int kt, int& entry, int& part) {
+      entry = INT_MIN;
+      part = 0;
+      if (lane < kGroups && kt < it.key_tiles) {
+        const int pos = key_pos(it, (first_tile(it) + kt) * kTile + 16 * (kGroups * w + lane)), bi = pos / B;
+        part = (pos - bi * B) / kFp4Tokens;
+        if (bi < it.nblocks_seq && block_seen(it, bi * B, B)) entry = __ldg(table + bi);
+      }
+    };
+    uint4 raw[kGroups * kVecs];
+    uint32_t scales[kGroups * kVecs];
+    auto load = [&](int entry, int part, int g) {
+      const int e = __shfl_sync(0xffffffffu, entry, g), t = __shfl_sync(0xffffffffu, part, g);
+      const bool in_pool = e >= 0 && e < p.num_blocks;
+      if (!kV && lane == 0 && e != INT_MIN && !in_pool) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+      const uint8_t* src =
+          cache + (((size_t)(in_pool ? e : 0) * p.num_kv_heads + it.hkv) * (B / kFp4Tokens) + t) * kFp4TileBytes;
+      raw[2 * g] = load_codes<0>(src + code_at, in_pool);
+      raw[2 * g + 1] = load_codes<8 * kFp4RowBytes>(src + code_at, in_pool);
+      scales[2 * g] = load_scales<0>(src + scale_at, in_pool);
+      scales[2 * g + 1] = load_scales<8 * kFp4RowScales>(src + scale_at, in_pool);
+    };
+    int entry, part, entry_next, part_next;
+    fetch(0, entry, part);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) load(entry, part, g);
+    fetch(1, entry_next, part_next);
+    for (int t = 0; t < it.key_tiles; ++t, ++tg) {
+      entry = entry_next;
+      part = part_next;
+      fetch(t + 2, entry_next, part_next);
+      if (tg >= 2) ok = __all_sync(0xffffffffu, wait_bar(&freed[(tg - 2) % kSBufs], ((tg - 2) / kSBufs) & 1, abort_flag));
+      if (!ok) break;
+      uint8_t* st = ring + (tg & 1) * 2 * kHalf;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        uint32_t sc[kVecs] = {fp4_scales_to_half(scales[2 * g]), fp4_scales_to_half(scales[2 * g + 1])};
+        if constexpr (kV) {
+          // scales of tokens that no query of the chunk sees may be NaN: zeros (every code is finite)
+          const int pos = key_pos(it, (first_tile(it) + t) * kTile + 16 * (kGroups * w + g));
+          if (!(pos + 16 <= it.L && block_whole(it, pos, 16))) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+              const int mine = pos + row + 8 * i;
+              if (!(mine < it.L && block_seen(it, mine, 1))) sc[i] = 0u;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          const uint4 x = raw[2 * g + i];
+          const uint32_t words[4] = {x.x, x.y, x.z, x.w}, s0 = half_dup_lo(sc[i]), s1 = half_dup_hi(sc[i]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint4 y;
+            fp4_to_half(words[k], y.x, y.y, y.z, y.w);
+            const uint32_t s = k < 2 ? s0 : s1;
+            y.x = half_mul(y.x, s), y.y = half_mul(y.y, s), y.z = half_mul(y.z, s), y.w = half_mul(y.w, s);
+            *reinterpret_cast<uint4*>(st + (at[g] ^ (16 * k)) + 8 * 128 * i) = y;
+          }
+        }
+        if (t + 1 < it.key_tiles) load(entry, part, g);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic writes -> tensor-core reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[tg & 1]);
+    }
+  }
+}
+
+// bf16 queries over a 4-bit cache: two warps turn each item's Q tile, in place, into fp16 after dividing every row by the
+// power of two that brings its largest element into [1, 2); the softmax multiplies the row's scores by it again.  What
+// lies more than 2^-14 below a row's largest element loses bits, by at most 2^-25 of the largest.  So the whole kernel
+// runs on fp16, with one MMA for P V where bf16 weights take two.
+constexpr int kConvertWarps = 2, kConvertWarp0 = kSoftmaxWarps + 2;
+template <typename Item>
+__device__ __forceinline__ void convert_queries(uint8_t* smem, uint8_t* qbuf, const Item* items, int w, int lane,
+                                                uint64_t* bar_qs, uint64_t* bar_qc, volatile int* abort_flag) {
+  const int sub = lane >> 3, chunk = lane & 7;
+  for (int no = 0;; ++no) {
+    if (!__all_sync(0xffffffffu, wait_bar(bar_qs, no & 1, abort_flag))) return;
+    if (items[no & 1].s < 0) return;
+    uint8_t* q = qbuf + (no & 1) * 2 * kHalf;
+    float* unit = reinterpret_cast<float*>(smem + kUnitOff) + (no & 1) * kTile;
+#pragma unroll 2
+    for (int r = 4 * w + sub; r < kTile; r += 4 * kConvertWarps) {
+      uint4* at[2] = {reinterpret_cast<uint4*>(q + r * 128 + chunk * 16),
+                      reinterpret_cast<uint4*>(q + kHalf + r * 128 + chunk * 16)};
+      const uint4 a = *at[0], b = *at[1];
+      uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        mx = fmaxf(mx, fmaxf(fabsf(Mma<__nv_bfloat16>::lo(x[i])), fabsf(Mma<__nv_bfloat16>::hi(x[i]))));
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      float up, down;
+      row_power(mx, up, down);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = Mma<__half>::pack(Mma<__nv_bfloat16>::lo(x[i]) * down, Mma<__nv_bfloat16>::hi(x[i]) * down);
+      *at[0] = make_uint4(x[0], x[1], x[2], x[3]);
+      *at[1] = make_uint4(x[4], x[5], x[6], x[7]);
+      if (chunk == 0) unit[r] = up;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic writes -> tensor-core reads
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_qc);
+  }
+}
+
 // Split items (few items, long windows): the CTAs of a cluster each left the unnormalised rows of their share of
 // the keys, then (reference maximum in log2 units, sum), kPartRow floats a row; each now merges its share of the
 // rows through distributed shared memory.  Every thread of the cluster comes here once.
@@ -728,6 +885,9 @@ __device__ __forceinline__ void split_merge(const PrefillParams& p, const float*
   cluster_sync_all();  // no CTA leaves while another reads its rows
 }
 
+// What the cache holds: the kernel's type T, E4M3 codes, or 4-bit rows (T fp16, queries and outputs in fp16 or bf16).
+enum class PfCache { kSame, kFp8, kFp4, kFp4Bf16 };
+
 // kWindow: see the file comment; kSplit: windowed, a cluster of p.split CTAs an item; kMixed: windowed, see pf_skip
 enum class PfForm { kPlain, kWindow, kSplit, kMixed };
 
@@ -736,14 +896,18 @@ enum class PfForm { kPlain, kWindow, kSplit, kMixed };
 // key tiles so far), so the next item's Q, K/V copies and first S MMAs overlap this item's last
 // P V and epilogue.
 // D: head size (64: windowed forms)
-template <typename T, PfForm kForm, bool kFp8, int D>
-__global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
+template <typename T, PfForm kForm, PfCache kCache, int D>
+__global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                       const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_out,
                       const PrefillParams p) {
   constexpr bool kWindow = kForm != PfForm::kPlain, kSplit = kForm == PfForm::kSplit;
+  constexpr bool kFp8 = kCache == PfCache::kFp8, kFp4 = kCache == PfCache::kFp4 || kCache == PfCache::kFp4Bf16;
+  constexpr bool kCoded = kFp8 || kFp4;                        // the producers convert
+  constexpr bool kConvertQ = kCache == PfCache::kFp4Bf16;      // bf16 queries become fp16 in shared memory
+  using TRow = std::conditional_t<kConvertQ, __nv_bfloat16, T>;  // of q and out
   constexpr int kHalves = D / 64;  // 64-column halves of a row
-  static_assert(D == 128 || (D == 64 && kWindow && !kFp8), "head size");
+  static_assert(D == 128 || (D == 64 && kWindow && !kCoded), "head size");
   using Item = std::conditional_t<
       kSplit, PfSplitItem,
       std::conditional_t<kForm == PfForm::kMixed, PfMixedItem, std::conditional_t<kWindow, PfWindowItem, PfItem>>>;
@@ -769,6 +933,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
   uint64_t* bar_ofree = bar_q + 15; // the item's epilogue has read O (one phase per item)
   uint64_t* bar_qs = bar_q + 16;    // item k published and its Q tile in shared memory (phase k)
   uint64_t* bar_staged = bar_q + 17; // the item's output tile written to the stage (or stored) (phase per item)
+  uint64_t* bar_qc = bar_q + 18;     // item k's Q tile converted (phase k; bf16 queries over a 4-bit cache)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kBarOff + 192);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 200);
   Item* items = reinterpret_cast<Item*>(smem + kBarOff + 256);  // [2] published items (s < 0: none left)
@@ -783,8 +948,8 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     mbar_init(bar_q, kSoftmaxWarps);
     for (int b = 0; b < 2; ++b) {
       // each copy slot arrives once per tile (with its bytes, or none); FP8: each producer warp
-      mbar_init(&bar_k[b], kFp8 ? kFp8Producers / 2 : slots);
-      mbar_init(&bar_v[b], kFp8 ? kFp8Producers / 2 : slots + kHalves);  // + each V producer's partial-block / zero-fill arrival
+      mbar_init(&bar_k[b], kCoded ? kFp8Producers / 2 : slots);
+      mbar_init(&bar_v[b], kCoded ? kFp8Producers / 2 : slots + kHalves);  // + each V producer's partial-block / zero-fill arrival
     }
     for (int b = 0; b < kSBufs; ++b) {
       mbar_init(&bar_s[b], 1);
@@ -795,6 +960,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     mbar_init(bar_ofree, kSoftmaxWarps);
     mbar_init(bar_qs, 1);
     mbar_init(bar_staged, kSoftmaxWarps);
+    if constexpr (kConvertQ) mbar_init(bar_qc, kConvertWarps);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -813,18 +979,27 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
   };
 
-  if (kFp8 && warp >= kFp8LoadWarp0) {
-    // =================================================================== producers over an FP8 cache
-    if constexpr (kFp8) {
+  if (kCoded && warp >= kFp8LoadWarp0) {
+    // =================================================================== producers over an FP8 or a 4-bit cache
+    if constexpr (kCoded) {
       regs_dec<kFp8LoadRegs>();
       const int w = warp - kFp8LoadWarp0;
-      if (w < kFp8Producers / 2)
-        fp8_producer<Item, false>(p, w, lane, idx0, idx_step, n_items, smem + kKOff, bar_k, bar_s, abort_flag);
-      else
-        fp8_producer<Item, true>(p, w - kFp8Producers / 2, lane, idx0, idx_step, n_items, smem + kVOff, bar_v, bar_o,
-                                 abort_flag);
+      const bool is_k = w < kFp8Producers / 2;
+      if constexpr (kFp4) {
+        if (is_k)
+          fp4_producer<Item, false>(p, w, lane, idx0, idx_step, n_items, smem + kKOff, bar_k, bar_s, abort_flag);
+        else
+          fp4_producer<Item, true>(p, w - kFp8Producers / 2, lane, idx0, idx_step, n_items, smem + kVOff, bar_v, bar_o,
+                                   abort_flag);
+      } else {
+        if (is_k)
+          fp8_producer<Item, false>(p, w, lane, idx0, idx_step, n_items, smem + kKOff, bar_k, bar_s, abort_flag);
+        else
+          fp8_producer<Item, true>(p, w - kFp8Producers / 2, lane, idx0, idx_step, n_items, smem + kVOff, bar_v, bar_o,
+                                   abort_flag);
+      }
     }
-  } else if (!kFp8 && warp >= kLoadWarp0) {
+  } else if (!kCoded && warp >= kLoadWarp0) {
     // =================================================================== producers: one half of K or V tiles
     const bool is_v = warp >= kLoadWarp0 + 2;
     const int half = (warp - kLoadWarp0) & 1;  // columns 64 half .. 64 half + 63
@@ -908,7 +1083,11 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       }
     }
   } else if (warp >= kSoftmaxWarps) {
-    if constexpr (kFp8) regs_dec<kFp8IssueRegs>();
+    if constexpr (kCoded) regs_dec<kFp8IssueRegs>();
+    if constexpr (kConvertQ) {
+      if (warp >= kConvertWarp0)
+        convert_queries(smem, qbuf, items, warp - kConvertWarp0, lane, bar_qs, bar_qc, abort_flag);
+    }
     if (warp == kSWarp && lane == 0) {
       // ================================================================= S = Q K^T issuer
       const uint32_t id_s = idesc<T>(0, kTile);
@@ -942,7 +1121,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       int idx = publish(idx0, 0, it);
       while (ok && idx < n_items) {
         // Q of this item in its buffer (this thread publishes the barrier's next phase: exact)
-        ok = wait_bar_spin(bar_qs, item_no & 1, abort_flag);
+        ok = wait_bar_spin(kConvertQ ? bar_qc : bar_qs, item_no & 1, abort_flag);
         if (!ok) break;
         Item nx;
         int idx_next = n_items;
@@ -1050,7 +1229,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     __syncwarp();
   } else {
     // =================================================================== softmax warps
-    if constexpr (kFp8) regs_inc<kFp8SoftmaxRegs>();
+    if constexpr (kCoded) regs_inc<kFp8SoftmaxRegs>();
     // Warp w owns the 16 query rows (tensor-memory lanes) 32 (w % 4) + 16 (w / 4) .. + 15 of the tile,
     // all 128 key columns: thread t holds rows r0 = base + t / 4 and r1 = r0 + 8, keys 8j + 2 (t % 4)
     // and + 1 (j = 0..15), so a row's maximum and sum take two shuffles among its four threads.
@@ -1058,6 +1237,8 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     const uint32_t half_base = (uint32_t)(q4 * 32 + hh * 16) << 16;  // first lane of this warp's rows
     const int r0 = q4 * 32 + hh * 16 + (lane >> 2), r1 = r0 + 8;
     const float sl2 = p.scale_log2;
+    // (bf16 queries over a 4-bit cache: each row's scale times the power of two that its queries were divided by)
+    [[maybe_unused]] float sr0 = sl2, sr1 = sl2;
     // every warp arrives on bar_q once it has read the published item
     auto take_item = [&]() {
       __syncwarp();
@@ -1068,6 +1249,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     int lim0 = 0, lim1 = 0;                                    // last key each row sees
     Item it = {};
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // reference maxima (log2 units), partial sums
+    auto row_scale = [&]() { return kConvertQ ? make_float2(sr0, sr1) : make_float2(sl2, sl2); };
     // key tile kt of the current item (this CTA's tile tg)
     auto tile = [&](int kt) {
       const int buf = tg % kSBufs;
@@ -1098,7 +1280,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
 #pragma unroll
         for (int j0 = 0; j0 < 16; j0 += 8) {
           uint32_t hi[16], lo[16];
-          make_p<T>(v, j0, sl2, m0, m1, SeeAll{}, hi, lo, n0, n1);
+          make_p<T>(v, j0, row_scale(), m0, m1, SeeAll{}, hi, lo, n0, n1);
           tmem_st16x128_x8(s_addr + 4 * j0, hi);
           if constexpr (split_p<T>()) tmem_st16x128_x8(s_addr + 64 + 4 * j0, lo);
         }
@@ -1130,7 +1312,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
           u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, 1));
           u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, 2));
           u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, 2));
-          if (__any_sync(0xffffffffu, u0 * sl2 > m0 + kRescaleThreshold || u1 * sl2 > m1 + kRescaleThreshold)) {
+          if (__any_sync(0xffffffffu, u0 * row_scale().x > m0 + kRescaleThreshold || u1 * row_scale().y > m1 + kRescaleThreshold)) {
             a0 = b0 = a1 = b1 = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -1150,7 +1332,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
         a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
         a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
-        const float mx0 = a0 * sl2, mx1 = a1 * sl2;  // scale > 0
+        const float mx0 = a0 * row_scale().x, mx1 = a1 * row_scale().y;  // scale > 0
         const bool upd0 = mx0 > m0 + kRescaleThreshold, upd1 = mx1 > m1 + kRescaleThreshold;
         const float al0 = upd0 ? fast_exp2(m0 - mx0) : 1.f, al1 = upd1 ? fast_exp2(m1 - mx1) : 1.f;
         if (__any_sync(0xffffffffu, upd0 || upd1) && kt > 0 && ok) {
@@ -1185,9 +1367,9 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
           // (window: a row may have seen no key yet; its scores are all -inf, its weights 0)
           const float z0 = kWindow && m0 == -INFINITY ? 0.f : m0, z1 = kWindow && m1 == -INFINITY ? 0.f : m1;
           if (!kMask || unmasked)
-            make_p<T>(v, j0, sl2, z0, z1, SeeAll{}, hi, lo, l0, l1);
+            make_p<T>(v, j0, row_scale(), z0, z1, SeeAll{}, hi, lo, l0, l1);
           else
-            make_p<T>(v, j0, sl2, z0, z1, mask, hi, lo, l0, l1);
+            make_p<T>(v, j0, row_scale(), z0, z1, mask, hi, lo, l0, l1);
           tmem_st16x128_x8(s_addr + 4 * j0, hi);
           if constexpr (split_p<T>()) tmem_st16x128_x8(s_addr + 64 + 4 * j0, lo);
         }
@@ -1233,7 +1415,13 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       if (lane == 0) mbar_arrive(&bar_p[buf]);
       ++tg;
     };
-    auto start_item = [&](const Item& x) {
+    auto start_item = [&](const Item& x, [[maybe_unused]] int no) {
+      if constexpr (kConvertQ) {  // (before the next item may be published: the barrier's next phase needs that)
+        ok = warp_wait(bar_qc, no & 1);
+        const float* unit = reinterpret_cast<const float*>(smem + kUnitOff) + (no & 1) * kTile;
+        // (never 0: a masked score is -inf times it)
+        sr0 = fmaxf(sl2 * unit[r0], FLT_MIN), sr1 = fmaxf(sl2 * unit[r1], FLT_MIN);
+      }
       take_item();
       lim0 = min(x.pos0 + (kWindow ? r0 >> p.pack_log2 : r0), x.L - 1) - key_shift(x);
       lim1 = min(x.pos0 + (kWindow ? r1 >> p.pack_log2 : r1), x.L - 1) - key_shift(x);
@@ -1244,7 +1432,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     // the first item and its first tile
     ok = warp_wait(bar_qs, 0);
     it = items[0];
-    if (ok && it.s >= 0) start_item(it);
+    if (ok && it.s >= 0) start_item(it, 0);
     // After a failure (a wait gave up) every warp leaves at the next wait: no warp waits for another
     // softmax warp, and the other roles stop at their next wait too.
     while (ok && it.s >= 0) {
@@ -1264,13 +1452,13 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       auto out_row = [&](int r) {
         const size_t query = (size_t)orow0 + (kWindow ? r >> p.pack_log2 : r);
         const int head = kWindow ? oh + (r & ((1 << p.pack_log2) - 1)) : oh;
-        return reinterpret_cast<T*>(p.out) + (query * p.num_q_heads + head) * D;
+        return reinterpret_cast<TRow*>(p.out) + (query * p.num_q_heads + head) * D;
       };
       const int rows = it.rows;
       [[maybe_unused]] const float pm0 = m0, pm1 = m1;  // split: this item's reference maxima
       ok = warp_wait(bar_qs, (item_no + 1) & 1);
       it = items[(item_no + 1) & 1];
-      if (ok && it.s >= 0) start_item(it);
+      if (ok && it.s >= 0) start_item(it, item_no + 1);
       // ---- epilogue: out = O / l for this warp's 16 rows, from the 16x256b layout (thread: rows r0, r1,
       //      columns 8j + 2 (t % 4) and + 1)
       if (ok) ok = warp_wait(bar_done, item_no & 1);
@@ -1302,7 +1490,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         ++item_no;
         continue;
       }
-      const float unit = kFp8 ? p.v_scale : 1.f;
+      const float unit = kCoded ? p.v_scale : 1.f;
       const float inv0 = s0 > 0.f ? unit / s0 : 0.f, inv1 = s1 > 0.f ? unit / s1 : 0.f;
       if constexpr (kStagedOut<T>) {
         // The tile goes to the stage, in the 128-byte-swizzled layout of the output's tensor map (row r's
@@ -1313,9 +1501,9 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         for (int j = 0; j < D / 8; ++j) {
           uint8_t* col = stage + (j >> 3) * kHalf + 4 * c4;
           *reinterpret_cast<uint32_t*>(col + swz128(r0, j & 7)) =
-              Mma<T>::pack(o[4 * j] * inv0, o[4 * j + 1] * inv0);
+              Mma<TRow>::pack(o[4 * j] * inv0, o[4 * j + 1] * inv0);
           *reinterpret_cast<uint32_t*>(col + swz128(r1, j & 7)) =
-              Mma<T>::pack(o[4 * j + 2] * inv1, o[4 * j + 3] * inv1);
+              Mma<TRow>::pack(o[4 * j + 2] * inv1, o[4 * j + 3] * inv1);
         }
         if (rows == kTile) {
           // a full tile: the P V issuer stores it once every softmax warp has written its rows
@@ -1343,7 +1531,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
         // transpose within the quad (two xor-shuffle steps per group of 4 j) gives thread c the 16 bytes
         // of columns 8j .. 8j + 7 for j = 4g + c, so a store writes 16 bytes per thread and 64
         // contiguous bytes per row and quad.
-        T *out0 = out_row(r0), *out1 = out_row(r1);
+        TRow *out0 = out_row(r0), *out1 = out_row(r1);
         const bool hi2 = (c4 >> 1) != 0, odd = (c4 & 1) != 0;
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
@@ -1379,7 +1567,7 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
     // a wait expired (the flag is stable: every thread has left its loop): record it, and let the
     // copies and MMAs this CTA started finish, each wait bounded, before its memory is released
     if (threadIdx.x == 0) report_error(p.err_flag, PA_DEVERR_TIMEOUT);
-    if (!kFp8 && warp >= kLoadWarp0 && lane == 0) {  // copies still landing
+    if (!kCoded && warp >= kLoadWarp0 && lane == 0) {  // copies still landing
       uint64_t* ring_bar = warp >= kLoadWarp0 + 2 ? bar_v : bar_k;
       for (int t = max(0, n_issued - 2); t < n_issued; ++t) drain_wait(&ring_bar[t & 1], (t >> 1) & 1);
     }
@@ -1393,59 +1581,68 @@ __global__ void __launch_bounds__(kFp8 ? kFp8Threads : kThreads, 1)
       for (int t = max(0, n_o - kSBufs); t < n_o; ++t) drain_wait(&bar_o[t % kSBufs], (t / kSBufs) & 1);
     __syncthreads();
   }
-  if constexpr (kSplit) split_merge<T, D>(p, reinterpret_cast<const float*>(smem + kKOff), idx0);
+  if constexpr (kSplit) split_merge<TRow, D>(p, reinterpret_cast<const float*>(smem + kKOff), idx0);
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 // one CTA per SM (the kernel holds all of tensor memory and most of shared memory), at most one per item
-template <typename T, PfForm kForm, bool kFp8 = false, int D = 128>
+template <typename T, PfForm kForm, PfCache kCache = PfCache::kSame, int D = 128>
 static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                   const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
   const long long items = (long long)p.num_seqs * (p.num_q_heads >> p.pack_log2) * p.q_tiles;
   if (items == 0) return cudaSuccess;
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  constexpr int kBytes = kCache == PfCache::kFp4Bf16 ? kSmemBytesConvert : kSmemBytes;
+  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // split: one cluster an item
   const unsigned grid = (unsigned)(p.split > 1 ? items * p.split : items < sms ? items : sms);
-  auto kernel = prefill_tc_kernel<T, kForm, kFp8, D>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  constexpr bool kCoded = kCache != PfCache::kSame;
+  auto kernel = prefill_tc_kernel<T, kForm, kCache, D>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  if constexpr (kFp8) {
+  if constexpr (kCoded) {
     static std::atomic<bool> known;
     e = require_registers(reinterpret_cast<const void*>(kernel), kFp8LaunchRegs, known);
     if (e != cudaSuccess) return e;
   }
-  return launch_cluster(kernel, dim3(grid), dim3(kFp8 ? kFp8Threads : kThreads), kSmemBytes, p.split, false, stream, tk,
+  return launch_cluster(kernel, dim3(grid), dim3(kCoded ? kFp8Threads : kThreads), kBytes, p.split, false, stream, tk,
                         tv, tq, to, p);
 }
 
-template <typename T, bool kFp8, int D>
+template <typename T, PfCache kCache, int D>
 static cudaError_t launch_window(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                  const CUtensorMap& to, const PrefillParams& p, bool mixed, cudaStream_t stream) {
-  return p.split > 1 ? launch_prefill<T, PfForm::kSplit, kFp8, D>(tk, tv, tq, to, p, stream)
-         : mixed     ? launch_prefill<T, PfForm::kMixed, kFp8, D>(tk, tv, tq, to, p, stream)
-                     : launch_prefill<T, PfForm::kWindow, kFp8, D>(tk, tv, tq, to, p, stream);
+  return p.split > 1 ? launch_prefill<T, PfForm::kSplit, kCache, D>(tk, tv, tq, to, p, stream)
+         : mixed     ? launch_prefill<T, PfForm::kMixed, kCache, D>(tk, tv, tq, to, p, stream)
+                     : launch_prefill<T, PfForm::kWindow, kCache, D>(tk, tv, tq, to, p, stream);
 }
 
 cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                               const CUtensorMap& to, const PrefillParams& p, bool mixed, cudaStream_t stream) {
   const bool window = p.window > 0;
   if (p.head_size == 64) {
-    if (dtype == PA_F16 && window) return launch_window<__half, false, 64>(tk, tv, tq, to, p, mixed, stream);
-    if (dtype == PA_BF16 && window) return launch_window<__nv_bfloat16, false, 64>(tk, tv, tq, to, p, mixed, stream);
+    if (dtype == PA_F16 && window) return launch_window<__half, PfCache::kSame, 64>(tk, tv, tq, to, p, mixed, stream);
+    if (dtype == PA_BF16 && window) return launch_window<__nv_bfloat16, PfCache::kSame, 64>(tk, tv, tq, to, p, mixed, stream);
     return cudaErrorInvalidValue;
   }
   if (dtype == PA_F16)
-    return window ? launch_window<__half, false, 128>(tk, tv, tq, to, p, mixed, stream)
+    return window ? launch_window<__half, PfCache::kSame, 128>(tk, tv, tq, to, p, mixed, stream)
                   : launch_prefill<__half, PfForm::kPlain>(tk, tv, tq, to, p, stream);
   if (dtype == PA_BF16)
-    return window ? launch_window<__nv_bfloat16, false, 128>(tk, tv, tq, to, p, mixed, stream)
+    return window ? launch_window<__nv_bfloat16, PfCache::kSame, 128>(tk, tv, tq, to, p, mixed, stream)
                   : launch_prefill<__nv_bfloat16, PfForm::kPlain>(tk, tv, tq, to, p, stream);
-  if (dtype == PA_FP8_E4M3 && window) return launch_window<__half, true, 128>(tk, tv, tq, to, p, mixed, stream);
+  if (dtype == PA_FP8_E4M3 && window) return launch_window<__half, PfCache::kFp8, 128>(tk, tv, tq, to, p, mixed, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prefill_fp4(int row_dtype, const CUtensorMap& tq, const CUtensorMap& to, const PrefillParams& p,
+                               bool mixed, cudaStream_t stream) {
+  if (row_dtype == PA_F16) return launch_window<__half, PfCache::kFp4, 128>(tq, tq, tq, to, p, mixed, stream);
+  if (row_dtype == PA_BF16) return launch_window<__half, PfCache::kFp4Bf16, 128>(tq, tq, tq, to, p, mixed, stream);
   return cudaErrorInvalidValue;
 }
 

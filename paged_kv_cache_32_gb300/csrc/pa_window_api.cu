@@ -168,8 +168,10 @@ int pack_log2(int G) {
   return k;
 }
 
-// 16-bit and FP8 caches whose blocks fit the 128-key tiles run on the tensor-core tile kernel
-bool tile_kernel_takes(const pa_cache_desc* c) { return c->dtype != PA_F32 && 128 % c->block_size == 0; }
+// 16-bit and FP8 caches whose blocks fit the 128-key tiles run on the tensor-core tile kernel, and every 4-bit cache
+bool tile_kernel_takes(const pa_cache_desc* c) {
+  return c->dtype == PA_FP4_E2M1 || (c->dtype != PA_F32 && 128 % c->block_size == 0);
+}
 
 // CTAs that share an item's key tiles: as many as leave each SM at most one, with four tiles or more each
 int tile_split(long long items, long long max_keys) {
@@ -209,14 +211,17 @@ long long tile_items(const pa::WindowParams& w, int pack) {
   return w.num_seqs * q_tiles * (w.num_q_heads >> pack);
 }
 
-int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack, cudaStream_t stream) {
+int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack, cudaStream_t stream,
+                 int32_t row_dtype = PA_F16) {
   const long long items = tile_items(w, pack);
   CUtensorMap tk, tv, tq, to;
-  const bool fp8 = cache->dtype == PA_FP8_E4M3;  // read by plain loads
-  if ((!fp8 && (!encode_cache_map(&tk, w.k_cache, cache, cache->block_size) ||
+  const bool fp8 = cache->dtype == PA_FP8_E4M3, fp4 = cache->dtype == PA_FP4_E2M1;  // read by plain loads
+  pa_cache_desc rows = *cache;
+  if (fp4) rows.dtype = row_dtype;
+  if ((!fp8 && !fp4 && (!encode_cache_map(&tk, w.k_cache, cache, cache->block_size) ||
                 !encode_cache_map(&tv, w.v_cache, cache, cache->block_size))) ||
-      !encode_query_map(&tq, w.q, cache, w.num_q_heads, w.num_query_tokens, 1 << pack) ||
-      !encode_query_map(&to, w.out, cache, w.num_q_heads, w.num_query_tokens, 1 << pack))
+      !encode_query_map(&tq, w.q, &rows, w.num_q_heads, w.num_query_tokens, 1 << pack) ||
+      !encode_query_map(&to, w.out, &rows, w.num_q_heads, w.num_query_tokens, 1 << pack))
     return PA_ERR_CUDA;
   pa::PrefillParams p = {};
   p.out = w.out;
@@ -245,8 +250,18 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   const bool mixed =
       mixes(items, ((long long)w.num_query_tokens / (128 >> pack) + w.num_seqs) * (w.num_q_heads >> pack));
   p.split = tile_split(items, std::min((long long)w.max_blocks * w.block_size, (long long)w.window + w.sinks + 128));
+  if (fp4)
+    return pa::launch_prefill_fp4(row_dtype, tq, to, p, mixed, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   if (fp8) tk = tv = tq;
   return pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, mixed, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int launch_chunk(const pa_cache_desc* cache, pa::WindowParams& p, cudaStream_t stream, int32_t row_dtype = PA_F16) {
+  const int pack = pack_log2(p.num_q_heads / p.num_kv_heads);
+  // (the tile kernel counts its items in int32, with room for one grid stride past the end; the rows kernels' slots fit)
+  if (tile_kernel_takes(cache) && tile_items(p, pack) <= kInt32Max - 4096 && tiles_faster(cache, p, pack))
+    return launch_tiles(cache, p, pack, stream, row_dtype);
+  return launch_rows(cache, p, stream, row_dtype);
 }
 
 pa::WindowParams base_params(const pa_cache_desc* cache, void* out, const void* q, const void* k_cache,
@@ -283,6 +298,10 @@ namespace pa {
 
 int fp4_rows(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, cudaStream_t stream) {
   return launch_rows(cache, p, stream, row_dtype);
+}
+
+int fp4_chunk(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, cudaStream_t stream) {
+  return launch_chunk(cache, p, stream, row_dtype);
 }
 
 }  // namespace pa
@@ -353,11 +372,7 @@ int pa_prefill_window(void* out, const void* q, const void* k_cache, const void*
   p.query_start = query_start;
   p.num_query_tokens = num_query_tokens;
   p.max_query_len = std::min(max_query_len, num_query_tokens);  // no valid chunk is longer
-  const int pack = pack_log2(num_q_heads / cache->num_kv_heads);
-  // (the tile kernel counts its items in int32, with room for one grid stride past the end; the rows kernels' slots fit)
-  if (tile_kernel_takes(cache) && tile_items(p, pack) <= kInt32Max - 4096 && tiles_faster(cache, p, pack))
-    return launch_tiles(cache, p, pack, static_cast<cudaStream_t>(stream));
-  return launch_rows(cache, p, static_cast<cudaStream_t>(stream));
+  return launch_chunk(cache, p, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
