@@ -26,7 +26,8 @@ PA_DEVERR = {0: "none", 1: "block id out of range", 2: "slot out of range", 3: "
 EXPORTED = ("pa_decode", "pa_decode_ex", "pa_decode_append", "pa_decode_partition_size", "pa_decode_workspace_size",
             "pa_reshape_and_cache", "pa_copy_blocks", "pa_status_string", "pa_version", "pa_decode_noalloc", "pa_prefill",
             "pa_reshape_and_cache_fp8", "pa_rope_frequencies", "pa_rope_and_cache", "pa_decode_window",
-            "pa_prefill_window", "pa_reshape_and_cache_fp4", "pa_read_cache_fp4", "pa_decode_fp4", "pa_prefill_fp4",
+            "pa_prefill_window", "pa_reshape_and_cache_fp4", "pa_read_cache_fp4", "pa_decode_fp4",
+            "pa_decode_fp4_workspace_size", "pa_prefill_fp4",
             "pa_rope_axes_and_cache", "pa_tables_extend", "pa_tables_trim")
 
 
@@ -110,7 +111,9 @@ def lib() -> ctypes.CDLL:
         L.pa_read_cache_fp4.argtypes = L.pa_reshape_and_cache_fp4.argtypes
         L.pa_read_cache_fp4.restype = ctypes.c_int
         L.pa_decode_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, desc_p, i32, f32, i32, i32, f32, f32, vp,
-                                    ctypes.c_uint32, vp, vp]
+                                    ctypes.c_uint32, vp, sz, vp, vp]
+        L.pa_decode_fp4_workspace_size.argtypes = []
+        L.pa_decode_fp4_workspace_size.restype = sz
         L.pa_decode_fp4.restype = ctypes.c_int
         L.pa_prefill_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, desc_p, i32, f32, i32, i32, f32,
                                      f32, vp, vp]
@@ -728,13 +731,29 @@ def _attention_fp4(where, host, out, q, k_cache, v_cache, block_tables, seq_lens
     return dev, code, desc, err, shape, table
 
 
+_fp4_workspace_bytes = 0
+
+
+def _fp4_workspace() -> int:
+    global _fp4_workspace_bytes
+    if not _fp4_workspace_bytes:
+        _fp4_workspace_bytes = int(lib().pa_decode_fp4_workspace_size())
+    return _fp4_workspace_bytes
+
+
+def pa_decode_fp4_workspace_size() -> int:
+    """Bytes of the workspace of pa_decode_fp4, whatever the call's sizes."""
+    return _fp4_workspace()
+
+
 def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, k_scale: float, v_scale: float,
                   window: int | None = None, num_sinks: int = 0, key=None, value=None, err_flag=None, stream=None,
-                  desc: pa_cache_desc | None = None, alibi_slopes=None, test_flags: int = 0) -> None:
+                  desc: pa_cache_desc | None = None, alibi_slopes=None, workspace=None, test_flags: int = 0) -> None:
     """A decode step over a 4-bit cache (see fp4_cache): out[s, h] = softmax(scale * q[s, h] K_s^T) V_s over the last
     ``window`` (None: all) and the first ``num_sinks`` positions.  out, q [num_seqs, num_q_heads, 128] fp16 or bf16;
     ``key`` / ``value`` [num_seqs, num_kv_heads, 128]: each sequence's new token, stored at position seq_lens[s] - 1 as
-    pa_reshape_and_cache_fp4 does and attended in the same launch.  No workspace."""
+    pa_reshape_and_cache_fp4 does and attended in the same call.  ``workspace``: a uint8 device tensor of
+    pa_decode_fp4_workspace_size() bytes, allocated with torch when None; calls that may overlap need one each."""
     where = "pa_decode_fp4"
     dev, code, desc, err, shape, table = _attention_fp4(where, True, out, q, k_cache, v_cache, block_tables, seq_lens,
                                                         err_flag, desc)
@@ -756,11 +775,16 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float
         if alibi_slopes.numel() != shape[1] or not alibi_slopes.is_contiguous():
             raise ValueError(f"{where}: one ALiBi slope per query head")
         slopes = alibi_slopes.data_ptr()
+    if workspace is None:
+        import torch
+        workspace = torch.empty(_fp4_workspace(), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev:
+        raise ValueError(f"{where}: workspace is on {workspace.device}, the caches on cuda:{dev}")
     _launch(lib().pa_decode_fp4, dev, (
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, block_tables.data_ptr(),
         seq_lens.data_ptr(), shape[0], shape[1], table[1], desc, code, float(scale),
         _INT32_MAX if window is None else _int32(window), _int32(num_sinks), float(k_scale), float(v_scale), slopes,
-        int(test_flags), err, _stream_of(dev, stream)), where)
+        int(test_flags), workspace.data_ptr(), workspace.numel() * workspace.element_size(), err, _stream_of(dev, stream)), where)
 
 
 def pa_prefill_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_query_len: int, scale: float,

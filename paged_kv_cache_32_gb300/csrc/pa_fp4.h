@@ -33,8 +33,12 @@ cudaError_t launch_fp4_rope(int row_dtype, bool interleaved, const RopeAxesParam
 // rows attention (see pa_window.h); row_dtype: of q, out and the appended rows
 cudaError_t launch_fp4_rows(int row_dtype, const WindowParams& p, bool slots, cudaStream_t stream);
 
-// a decode step, with the split of a windowed call chosen; a chunk, with its kernel chosen too (a PA_* status)
-int fp4_rows(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, cudaStream_t stream);
+// a decode step whose slabs are dealt out evenly to a grid of kFp4EvenGrid CTAs, in a workspace of fp4_even_workspace() bytes
+constexpr int kFp4EvenGrid = 152 * 4;
+size_t fp4_even_workspace();
+cudaError_t launch_fp4_even(int row_dtype, const WindowParams& p, float* workspace, cudaStream_t stream);
+// a decode step, with its kernel and split chosen (workspace: nullable); a chunk, with its kernel chosen too (a PA_* status)
+int fp4_decode(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, float* workspace, cudaStream_t stream);
 int fp4_chunk(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, cudaStream_t stream);
 
 namespace host {

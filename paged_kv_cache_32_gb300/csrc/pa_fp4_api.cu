@@ -138,11 +138,13 @@ int pa_read_cache_fp4(void* key, void* value, const void* k_cache, const void* v
   return pa::launch_fp4_read(row_dtype, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+size_t pa_decode_fp4_workspace_size(void) { return pa::fp4_even_workspace(); }
+
 int pa_decode_fp4(void* out, const void* q, void* k_cache, void* v_cache, const void* key, const void* value,
                   const int32_t* block_tables, const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads,
                   int32_t max_blocks_per_seq, const pa_cache_desc* cache, int32_t row_dtype, float scale, int32_t window,
                   int32_t num_sinks, float k_scale, float v_scale, const float* alibi_slopes, uint32_t test_flags,
-                  int32_t* err_flag, void* stream) {
+                  void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream) {
   const int rc = check_attention(cache, row_dtype, num_seqs, num_q_heads, max_blocks_per_seq, scale, window, num_sinks,
                                  k_scale, v_scale);
   if (rc != PA_OK) return rc;
@@ -151,10 +153,12 @@ int pa_decode_fp4(void* out, const void* q, void* k_cache, void* v_cache, const 
   if (out == nullptr || q == nullptr || k_cache == nullptr || v_cache == nullptr || seq_lens == nullptr)
     return PA_ERR_NULL_POINTER;
   if (block_tables == nullptr && max_blocks_per_seq > 0) return PA_ERR_NULL_POINTER;
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 16) || !aligned(out, 4) || !aligned(key, 16) ||
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(key, 16) ||
       !aligned(value, 16) || !aligned(seq_lens, 4) || !aligned(block_tables, 4) || !aligned(alibi_slopes, 4))
     return PA_ERR_MISALIGNED;
   if ((int64_t)num_seqs * num_q_heads > kInt32Max) return PA_ERR_TOO_LARGE;
+  if (workspace != nullptr && workspace_bytes < pa::fp4_even_workspace()) return PA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return PA_ERR_MISALIGNED;
   pa::WindowParams p = base_params(cache, out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_q_heads,
                                    max_blocks_per_seq, scale, window, num_sinks, k_scale, v_scale, err_flag);
   p.alibi = alibi_slopes;
@@ -163,7 +167,7 @@ int pa_decode_fp4(void* out, const void* q, void* k_cache, void* v_cache, const 
   p.new_v = value;
   p.k_cache_out = k_cache;
   p.v_cache_out = v_cache;
-  return pa::fp4_rows(cache, row_dtype, p, static_cast<cudaStream_t>(stream));
+  return pa::fp4_decode(cache, row_dtype, p, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 int pa_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,

@@ -48,9 +48,9 @@ def test_write_and_read_refusals(lib, name):
 
 
 def decode(lib, d=desc(), out=FAKE, q=FAKE, k=FAKE, v=FAKE, key=None, value=None, bt=FAKE, sl=FAKE, n=2, hq=4, m=4,
-           rows=pa.PA_BF16, scale=0.1, window=8, sinks=0, ku=0.01, vu=0.01, slopes=None):
+           rows=pa.PA_BF16, scale=0.1, window=8, sinks=0, ku=0.01, vu=0.01, slopes=None, ws=None, ws_bytes=0):
     return lib.pa_decode_fp4(out, q, k, v, key, value, bt, sl, n, hq, m, ctypes.byref(d), rows, scale, window, sinks, ku, vu,
-                             slopes, 0, None, None)
+                             slopes, 0, ws, ws_bytes, None, None)
 
 
 def prefill(lib, d=desc(), out=FAKE, q=FAKE, k=FAKE, v=FAKE, bt=FAKE, sl=FAKE, qs=FAKE, n=2, t=10, hq=4, m=4, most=5,
@@ -69,6 +69,9 @@ def test_attention_refusals(lib):
         assert call(lib, q=FAKE + 8) == 5 and call(lib, v=FAKE + 4) == 5 and call(lib, sl=FAKE + 2) == 5
         assert call(lib, m=1 << 28) == 7
         assert call(lib, n=0, out=None) == 0
+    need = lib.pa_decode_fp4_workspace_size()
+    assert decode(lib, ws=FAKE, ws_bytes=need - 1) == 4 and decode(lib, ws=FAKE + 64, ws_bytes=need) == 5
+    assert decode(lib, out=FAKE + 8) == 5
     assert decode(lib, key=FAKE) == 1 and decode(lib, key=FAKE, value=FAKE + 8) == 5 and decode(lib, slopes=FAKE + 2) == 5
     assert prefill(lib, scale=0.0) == 3 and prefill(lib, t=-1) == 3 and prefill(lib, most=-1) == 3
     assert prefill(lib, qs=None) == 1 and prefill(lib, out=FAKE + 8) == 5 and prefill(lib, t=(1 << 31) - 1, hq=1 << 12) == 7

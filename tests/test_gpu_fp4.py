@@ -222,6 +222,58 @@ def test_decode_few_long_sequences(rows, hkv, append):
         assert torch.equal(s.out, Step(w).decode())
 
 
+@pytest.mark.parametrize("rows,hq,hkv,block_size", [("f16", 8, 8, 16), ("bf16", 24, 2, 32), ("bf16", 7, 1, 48)])
+def test_decode_workspace(pa, rows, hq, hkv, block_size):
+    """Slabs dealt out evenly (no window), empty and bad sequences among them, with a workspace full of NaN and one that a
+    captured call keeps; without a workspace the same to rounding."""
+    import torch
+    rng = np.random.default_rng(hq)
+    lens = [0, 5000, 1, 31, 32, 33, 0, 700] + [int(x) for x in rng.integers(1, 900, 30)] + [0]
+    w = case(rows, lens, [1] * len(lens), hq, hkv, block_size, BIG, 0, seed=4)
+    ref = w.reference()
+    ref[[0, 6, -1]] = 0.0
+    ws = torch.full((pa.pa_decode_fp4_workspace_size(),), 0xFF, dtype=torch.uint8, device="cuda")
+    s, t = Step(w), Step(w)
+    s.decode(workspace=ws)
+    check(s, ref, "even")
+    assert torch.equal(s.out, Step(w).decode())  # the same bits again
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t.decode(workspace=ws)
+    ws.fill_(0xFF)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(t.err.item()) == 0 and torch.equal(s.out, t.out)
+    # a length past the table is reported, the others stay right
+    s = Step(w)
+    s.lens[3] = 10 ** 6
+    s.decode()
+    got = out_f64(s.out)
+    assert int(s.err.item()) == 5 and np.all(got[3] == SENTINEL)
+    ok, err, _ = within_bound(np.delete(got, 3, 0), np.delete(ref, 3, 0), rows)
+    assert ok, err
+    # the C call without one
+    s = Step(w)
+    d = pa.fp4_cache_desc(s.k)
+    status = pa.lib().pa_decode_fp4(s.out.data_ptr(), s.q.data_ptr(), s.k.data_ptr(), s.v.data_ptr(), None, None,
+                                    s.table.data_ptr(), s.lens.data_ptr(), len(lens), hq, w.width, d,
+                                    pa.PA_F16 if rows == "f16" else pa.PA_BF16, w.scale, 2 ** 31 - 1, 0, K_UNIT, V_UNIT, None,
+                                    0, None, 0, s.err.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    check(s, ref, "clusters")
+
+
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 1e-36])
+def test_decode_any_scale(scale):
+    """Negative scales, and those that leave every token the same weight."""
+    for window in (BIG, 50):
+        w = case("bf16", [300, 77, 5], [1, 1, 1], 8, 2, 16, window, 0, seed=3)
+        w.scale = scale
+        s = Step(w)
+        s.decode()
+        check(s, w.reference(), "scale")
+
+
 def test_decode_alibi():
     import torch
     slopes = -(2.0 ** -np.arange(1, 13)).astype(np.float32)
