@@ -714,6 +714,7 @@ __device__ __forceinline__ void fp4_producer(const PrefillParams& p, int w, int 
                                              int n_items, uint8_t* ring, uint64_t* bar, uint64_t* freed,
                                              volatile int* abort_flag) {
   constexpr int kGroups = 2, kVecs = 2;  // groups of 16 keys of a warp and tile; 8-row vectors of a group
+  constexpr int kPrefetchTiles = 4;
   const int B = p.block_size;
   // The lane's place in a vector of 8 rows: eight lanes whose stores go together hold four neighbouring rows of one
   // 64-column half, which the swizzle puts into different banks.
@@ -733,38 +734,56 @@ __device__ __forceinline__ void fp4_producer(const PrefillParams& p, int w, int 
       continue;
     }
     const int32_t* table = p.block_tables + (size_t)it.s * p.max_blocks;
-    // lane l < 2: the table entry of the tile's group 2 w + l, INT_MIN if it has none, and its tile in the block
-    auto fetch = [&](int kt, int& entry, int& part) {
-      entry = INT_MIN;
-      part = 0;
-      if (lane < kGroups && kt < it.key_tiles) {
-        const int pos = key_pos(it, (first_tile(it) + kt) * kTile + 16 * (kGroups * w + lane)), bi = pos / B;
-        part = (pos - bi * B) / kFp4Tokens;
-        if (bi < it.nblocks_seq && block_seen(it, bi * B, B)) entry = __ldg(table + bi);
-      }
+    // Lane 2 j + g: the tile of the cache that group 2 w + g of key tile 16 b + j is (kNone: no query sees it; kBad: of a
+    // block outside the pool); for the present 16 key tiles and the next.
+    constexpr int kNone = -1, kBad = -2, kBatch = 32 / kGroups;
+    auto fetch = [&](int batch) {
+      const int kt = batch * kBatch + lane / kGroups;
+      if (kt >= it.key_tiles) return kNone;
+      const int pos = key_pos(it, (first_tile(it) + kt) * kTile + 16 * (kGroups * w + lane % kGroups)), bi = pos / B;
+      if (bi >= it.nblocks_seq || !block_seen(it, bi * B, B)) return kNone;
+      const int block = __ldg(table + bi);
+      return block >= 0 && block < p.num_blocks
+                 ? (block * p.num_kv_heads + it.hkv) * (B / kFp4Tokens) + (pos - bi * B) / kFp4Tokens
+                 : kBad;
+    };
+    int batch_no = 0, here = fetch(0), ahead = fetch(1);
+    auto tile_of = [&](int kt, int g) {  // kt in the present batch or the next
+      const int x = __shfl_sync(0xffffffffu, here, kGroups * (kt % kBatch) + g);
+      const int y = __shfl_sync(0xffffffffu, ahead, kGroups * (kt % kBatch) + g);
+      return kt / kBatch == batch_no ? x : y;
     };
     uint4 raw[kGroups * kVecs];
     uint32_t scales[kGroups * kVecs];
-    auto load = [&](int entry, int part, int g) {
-      const int e = __shfl_sync(0xffffffffu, entry, g), t = __shfl_sync(0xffffffffu, part, g);
-      const bool in_pool = e >= 0 && e < p.num_blocks;
-      if (!kV && lane == 0 && e != INT_MIN && !in_pool) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
-      const uint8_t* src =
-          cache + (((size_t)(in_pool ? e : 0) * p.num_kv_heads + it.hkv) * (B / kFp4Tokens) + t) * kFp4TileBytes;
-      raw[2 * g] = load_codes<0>(src + code_at, in_pool);
-      raw[2 * g + 1] = load_codes<8 * kFp4RowBytes>(src + code_at, in_pool);
-      scales[2 * g] = load_scales<0>(src + scale_at, in_pool);
-      scales[2 * g + 1] = load_scales<8 * kFp4RowScales>(src + scale_at, in_pool);
+    auto load = [&](int kt, int g) {
+      const int tile = tile_of(kt, g);
+      if (!kV && lane == 0 && tile == kBad) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+      const bool take = tile >= 0;
+      const uint8_t* src = cache + (size_t)(take ? tile : 0) * kFp4TileBytes;
+      raw[2 * g] = load_codes<0>(src + code_at, take);
+      raw[2 * g + 1] = load_codes<8 * kFp4RowBytes>(src + code_at, take);
+      scales[2 * g] = load_scales<0>(src + scale_at, take);
+      scales[2 * g + 1] = load_scales<8 * kFp4RowScales>(src + scale_at, take);
     };
-    int entry, part, entry_next, part_next;
-    fetch(0, entry, part);
+    // the lines of a tile further on into L2 (its registers are loaded one tile ahead, too late for HBM's latency)
+    auto prefetch = [&](int kt) {
+      if (kt >= it.key_tiles) return;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) load(entry, part, g);
-    fetch(1, entry_next, part_next);
+      for (int g = 0; g < kGroups; ++g) {
+        const int tile = tile_of(kt, g);
+        if (tile >= 0 && lane < kFp4TileBytes / 128)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(cache + (size_t)tile * kFp4TileBytes + lane * 128));
+      }
+    };
+    for (int kt = 1; kt < kPrefetchTiles; ++kt) prefetch(kt);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) load(0, g);
     for (int t = 0; t < it.key_tiles; ++t, ++tg) {
-      entry = entry_next;
-      part = part_next;
-      fetch(t + 2, entry_next, part_next);
+      if (t + 1 >= (batch_no + 1) * kBatch) {  // (the next batch's entries are used twelve tiles on)
+        here = ahead;
+        ahead = fetch(++batch_no + 1);
+      }
+      prefetch(t + kPrefetchTiles);
       if (tg >= 2) ok = __all_sync(0xffffffffu, wait_bar(&freed[(tg - 2) % kSBufs], ((tg - 2) / kSBufs) & 1, abort_flag));
       if (!ok) break;
       uint8_t* st = ring + (tg & 1) * 2 * kHalf;
@@ -795,7 +814,7 @@ __device__ __forceinline__ void fp4_producer(const PrefillParams& p, int w, int 
             *reinterpret_cast<uint4*>(st + (at[g] ^ (16 * k)) + 8 * 128 * i) = y;
           }
         }
-        if (t + 1 < it.key_tiles) load(entry, part, g);
+        if (t + 1 < it.key_tiles) load(t + 1, g);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic writes -> tensor-core reads
       __syncwarp();

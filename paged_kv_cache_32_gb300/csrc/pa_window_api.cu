@@ -173,10 +173,14 @@ bool tile_kernel_takes(const pa_cache_desc* c) {
   return c->dtype == PA_FP4_E2M1 || (c->dtype != PA_F32 && 128 % c->block_size == 0);
 }
 
-// CTAs that share an item's key tiles: as many as leave each SM at most one, with four tiles or more each
-int tile_split(long long items, long long max_keys) {
+// CTAs that share an item's key tiles: as many as leave each SM at most one, with four tiles or more each.  Over a 4-bit
+// cache up to two an SM, with eight tiles or more: its tiles take longer to convert, so that the longest of unequal items
+// is what a call waits for (16 sequences of 5 queries over 2500 to 20000 tokens, 64 / 8 heads: 236 us, with two 147, four
+// 155; equal lengths the same).
+int tile_split(long long items, long long max_keys, bool fp4) {
   int c = 1;
   while (c < kMaxCluster && items * c * 2 <= kSms && max_keys / (128 * 2 * c) >= 4) c *= 2;
+  while (fp4 && c < kMaxCluster && items * c * 2 <= 2 * kSms && max_keys / (128 * 2 * c) >= 8) c *= 2;
   return c;
 }
 
@@ -186,22 +190,27 @@ int tile_split(long long items, long long max_keys) {
 //  * rows: 6 us and the longer of 1 us for `rate` keys of an eight-row group over all, and 0.85 us for each slab of 16
 //    keys (FP8: 1.3 us for 32) of the warp with most;
 //  * tiles: 5 us and, for each item that an SM gets, 1 us and `per_tile` a key tile.
+// Over a 4-bit cache fitted apart, to 250 chunks of 1 to 64 queries (1 to 64 sequences, 300 to 20000 keys): 1 % lost on
+// average, and up to a half (12 us for 18) for five queries over 300 keys.
 // E.g. 32 sequences, 64 / 8 heads, 4096 keys, bf16: 2 queries each 95 us on rows and 104 on tiles, 5 queries 204 and
 // 104; 8 sequences of 5 queries: 70 and 35; one of 3 with 300 keys: 7 and 10.5.
 bool tiles_faster(const pa_cache_desc* cache, pa::WindowParams p, int pack) {
-  const bool fp8 = cache->dtype == PA_FP8_E4M3;
+  const bool fp8 = cache->dtype == PA_FP8_E4M3, fp4 = cache->dtype == PA_FP4_E2M1;
   const int G = p.num_q_heads / p.num_kv_heads, queries = 128 >> pack;
   const double kv = (double)p.num_seqs * p.num_kv_heads;
   const double keys = std::min((double)p.max_blocks * p.block_size, (double)p.window + p.sinks + queries);
   const double groups = kv * ceil((double)p.max_query_len * G / 8);
   spread(cache->dtype, (long long)std::min(groups, 1e9), (long long)keys, p);
-  const double slabs = ceil(keys / (fp8 ? 32.0 : 16.0) / (p.warps * p.cluster));
+  const double slabs = ceil(keys / (fp8 || fp4 ? 32.0 : 16.0) / (p.warps * p.cluster));
   const bool narrow = cache->head_size == 64;
-  const double rate = fp8 ? 35000.0 : narrow ? 26000.0 : 30000.0, per_tile = narrow ? 1.6 : 1.3;
-  const double rows_us = 6.0 + std::max(groups * keys / rate, slabs * (fp8 ? 1.3 : 0.85));
-  const double items = kv * ceil((double)p.max_query_len / queries) * (G >> pack), share = items / kSms;
-  const double tiles = ceil(keys / 128.0) / tile_split((long long)std::min(items, 1e9), (long long)keys);
-  const double tile_us = 5.0 + std::max(1.0, 0.5 * (share + ceil(share))) * (1.0 + per_tile * tiles);
+  const double rate = fp4 ? 32500.0 : fp8 ? 35000.0 : narrow ? 26000.0 : 30000.0;
+  const double per_tile = fp4 ? 1.4 : narrow ? 1.6 : 1.3;
+  const double rows_us = (fp4 ? 6.5 : 6.0) + std::max(groups * keys / rate, slabs * (fp4 ? 1.2 : fp8 ? 1.3 : 0.85));
+  const double items = kv * ceil((double)p.max_query_len / queries) * (G >> pack);
+  const int split = tile_split((long long)std::min(items, 1e9), (long long)keys, fp4);
+  const double share = items * split / kSms, tiles = ceil(keys / 128.0) / split;
+  const double tile_us =
+      (fp4 ? 6.0 : 5.0) + std::max(1.0, 0.5 * (share + ceil(share))) * ((fp4 ? 4.0 : 1.0) + per_tile * tiles);
   return tile_us < rows_us;
 }
 
@@ -249,7 +258,7 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   p.max_query_len = w.max_query_len;
   const bool mixed =
       mixes(items, ((long long)w.num_query_tokens / (128 >> pack) + w.num_seqs) * (w.num_q_heads >> pack));
-  p.split = tile_split(items, std::min((long long)w.max_blocks * w.block_size, (long long)w.window + w.sinks + 128));
+  p.split = tile_split(items, std::min((long long)w.max_blocks * w.block_size, (long long)w.window + w.sinks + 128), fp4);
   if (fp4)
     return pa::launch_prefill_fp4(row_dtype, tq, to, p, mixed, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   if (fp8) tk = tv = tq;
