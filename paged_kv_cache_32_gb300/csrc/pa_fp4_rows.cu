@@ -580,7 +580,7 @@ __device__ __forceinline__ void write_rows(const WindowParams& p, const RowsItem
 // Warps of a CTA, slabs of a ring, CTAs of an SM: 16 warps of 118 registers.  96 sequences of up to 16384 tokens, 64 / 8
 // heads: 138 us, with three CTAs 150, five (96 registers, spills) 151, two of eight warps 157, slabs of 64 tokens 159.
 constexpr int kEvenWarps = 4, kEvenStages = 2, kEvenResident = 4;
-constexpr int kEvenMinSlabs = 4 * kEvenWarps;  // of a CTA: fewer CTAs take part in small calls
+constexpr int kEvenMinSlabs = kEvenWarps;  // of a CTA: fewer CTAs take part in small calls
 
 template <typename T>
 __global__ void __launch_bounds__(kEvenWarps * 32, kEvenResident) fp4_even_kernel(const WindowParams p, float* workspace) {

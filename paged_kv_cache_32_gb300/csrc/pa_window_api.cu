@@ -305,13 +305,21 @@ pa::WindowParams base_params(const pa_cache_desc* cache, void* out, const void* 
 
 namespace pa {
 
-// With a workspace, slabs are dealt out evenly; but a window shorter than half of what the table holds makes the items
-// nearly equal, and those run as well without a second kernel, one cluster each: 64 sequences of up to 8192 tokens, 32 / 32
-// heads, window 4000: 191 us, dealt out 194; 96 of up to 16384 without a window, 64 / 8 heads: 205 and 138.  (ALiBi: only
-// the clusters' kernel.)
+// With a workspace, are the slabs dealt out evenly?  Where an item is long and there are many of them: 128 items of 4096
+// tokens 31 us in clusters and 27 dealt out, of 20000 134 and 76 (contexts of 1250 to 20000: 116 and 45); 32 of 4096 10.8
+// and 14.4, of 20000 27 both; one of 80000 38 and 18; 1024 of 1000 45 and 49.  Not where a window shorter than half of what
+// the table holds makes items nearly equal and lets many start far from their sequence's: those run as well in one
+// launch.  (The lengths themselves are on the device: short ones in a wide table cost a dealt out call 9 to 20 us for 6 to
+// 14.)  ALiBi: only the clusters' kernel.
+bool deal_evenly(const pa_cache_desc* cache, const WindowParams& p) {
+  const long long cap = (long long)p.max_blocks * cache->block_size, reach = (long long)p.window + p.sinks;
+  const long long keys = std::min(cap, reach), group = p.num_q_heads / p.num_kv_heads;
+  const long long items = (long long)p.num_seqs * p.num_kv_heads * ((group + 7) / 8);
+  return p.alibi == nullptr && 2 * reach >= cap && (keys >= 32768 || (keys >= 2048 && items * keys >= 300000));
+}
+
 int fp4_decode(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, float* workspace, cudaStream_t stream) {
-  const bool equal = 2 * ((long long)p.window + p.sinks) < (long long)p.max_blocks * p.block_size;
-  if (workspace == nullptr || p.alibi != nullptr || equal) return launch_rows(cache, p, stream, row_dtype);
+  if (workspace == nullptr || !deal_evenly(cache, p)) return launch_rows(cache, p, stream, row_dtype);
   return launch_fp4_even(row_dtype, p, workspace, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

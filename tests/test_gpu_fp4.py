@@ -229,7 +229,8 @@ def test_decode_workspace(pa, rows, hq, hkv, block_size):
     import torch
     rng = np.random.default_rng(hq)
     lens = [0, 5000, 1, 31, 32, 33, 0, 700] + [int(x) for x in rng.integers(1, 900, 30)] + [0]
-    w = case(rows, lens, [1] * len(lens), hq, hkv, block_size, BIG, 0, seed=4)
+    # (a table of 40000 tokens: the slabs are dealt out by what it holds)
+    w = case(rows, lens, [1] * len(lens), hq, hkv, block_size, BIG, 0, seed=4, slack_blocks=35000 // block_size)
     ref = w.reference()
     ref[[0, 6, -1]] = 0.0
     ws = torch.full((pa.pa_decode_fp4_workspace_size(),), 0xFF, dtype=torch.uint8, device="cuda")
