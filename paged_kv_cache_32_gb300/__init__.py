@@ -814,14 +814,18 @@ def _tables(where, block_tables, seq_lens, held_blocks, free_blocks, num_free, w
     """The checks of both calls: (device, address of err_flag, num_seqs, max_blocks_per_seq)."""
     import torch
     dev, i32 = block_tables.get_device(), torch.int32
-    if dev < 0:
-        raise ValueError(f"{where}: the tables must be CUDA tensors")
-    for t, name in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (held_blocks, "held_blocks"),
-                    (free_blocks, "free_blocks"), (num_free, "num_free"), (wanted, "new_tokens / keep_lens")):
-        if t.dtype is not i32 or t.get_device() != dev:
+    if not (dev >= 0 and block_tables.dtype is i32 and seq_lens.dtype is i32 and held_blocks.dtype is i32 and
+            free_blocks.dtype is i32 and num_free.dtype is i32 and wanted.dtype is i32 and seq_lens.get_device() == dev and
+            held_blocks.get_device() == dev and free_blocks.get_device() == dev and num_free.get_device() == dev and
+            wanted.get_device() == dev and block_tables.is_contiguous() and seq_lens.is_contiguous() and
+            held_blocks.is_contiguous() and free_blocks.is_contiguous() and wanted.is_contiguous()):
+        if dev < 0:
+            raise ValueError(f"{where}: the tables must be CUDA tensors")
+        for t, name in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (held_blocks, "held_blocks"),
+                        (free_blocks, "free_blocks"), (num_free, "num_free"), (wanted, "new_tokens / keep_lens")):
             _refuse(where, dev, False, (t, name, i32))
-        if not t.is_contiguous():
-            raise ValueError(f"{where}: {name} must be contiguous")
+            if not t.is_contiguous():
+                raise ValueError(f"{where}: {name} must be contiguous")
     if block_tables.dim() != 2 or num_free.numel() != 1:
         raise ValueError(f"{where}: block_tables must be [num_seqs, max_blocks_per_seq], num_free one number")
     n, width = block_tables.shape

@@ -3,8 +3,8 @@
 //
 // A group is 16 neighbouring elements x of a row: s = e4m3(max |x| / (6 unit)), codes e2m1(x * (1 / (s unit))), every
 // step one fp32 operation, so that the bytes are the same whoever writes them (the append inside a decode step, too).
-// Eight elements, 16 bytes of a row, are one thread's: a group's maximum takes one shuffle, a row 16 threads.
-// Bound by HBM: 256 bytes read and 72 written a row.
+// A group, 32 bytes of a row, is one thread's, a row 8 threads'.
+// Bound by HBM: 256 bytes read and 72 written a row (the read back: the other way round).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -18,112 +18,183 @@
 namespace pa {
 namespace {
 
-constexpr int kRowThreads = kFp4D / 8;  // threads of a row
+constexpr int kRowThreads = kFp4D / 16;  // threads of a row
 constexpr int kThreads = 256;
 constexpr int kRows = kThreads / kRowThreads;  // rows that a CTA takes at a time
 
+struct Group16 {  // 16 elements in 16 bits
+  uint4 a, b;
+};
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  f[0] = Mma<T>::lo(v.x), f[1] = Mma<T>::hi(v.x), f[2] = Mma<T>::lo(v.y), f[3] = Mma<T>::hi(v.y);
-  f[4] = Mma<T>::lo(v.z), f[5] = Mma<T>::hi(v.z), f[6] = Mma<T>::lo(v.w), f[7] = Mma<T>::hi(v.w);
+__device__ __forceinline__ void unpack(const Group16& v, float (&f)[16]) {
+  const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[2 * i] = Mma<T>::lo(w[i]), f[2 * i + 1] = Mma<T>::hi(w[i]);
 }
 template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(Mma<T>::pack(f[0], f[1]), Mma<T>::pack(f[2], f[3]), Mma<T>::pack(f[4], f[5]),
-                    Mma<T>::pack(f[6], f[7]));
+__device__ __forceinline__ Group16 pack(const float (&f)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = Mma<T>::pack(f[2 * i], f[2 * i + 1]);
+  return {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
+}
+__device__ __forceinline__ Group16 load_group(const void* src) {
+  const uint4* x = static_cast<const uint4*>(src);
+  return {__ldg(x), __ldg(x + 1)};
+}
+__device__ __forceinline__ void store_group(void* dst, const Group16& v) {
+  static_cast<uint4*>(dst)[0] = v.a;
+  static_cast<uint4*>(dst)[1] = v.b;
 }
 
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Thread j (0 .. 15) of a row, all 32 lanes of the warp together: elements 8 j .. to their place in the tile at `tile`
-// (nullptr: the row is not written), row r of it.
-__device__ __forceinline__ void store_row(uint8_t* tile, int r, int j, const float (&f)[8], float unit, float unit6) {
+// Thread j (0 .. 7) of a row, all 32 lanes of the warp together: group j to its place in the tile at `tile` (nullptr: the
+// row is not written), row r of it.
+__device__ __forceinline__ void store_row(uint8_t* tile, int r, int j, const float (&f)[16], float unit) {
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  const uint32_t scale = fp4_scale_code(amax, unit6);
-  const uint32_t codes = fp4_codes8(f, fp4_inverse(scale, unit));
-  // the scales of four groups (eight threads) into one word
-  uint32_t s = scale | __shfl_down_sync(0xffffffffu, scale, 2) << 8;
-  s |= __shfl_down_sync(0xffffffffu, s, 4) << 16;
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+  const uint32_t scale = fp4_scale_code(amax, __fmul_rn(6.f, unit));
+  const float inv = fp4_inverse(scale, unit);
+  const float lo[8] = {f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]};
+  const float hi[8] = {f[8], f[9], f[10], f[11], f[12], f[13], f[14], f[15]};
+  const uint2 codes = make_uint2(fp4_codes8(lo, inv), fp4_codes8(hi, inv));
+  // the scales of four groups into one word
+  uint32_t s = scale | __shfl_down_sync(0xffffffffu, scale, 1) << 8;
+  s |= __shfl_down_sync(0xffffffffu, s, 2) << 16;
   if (tile == nullptr) return;
-  *reinterpret_cast<uint32_t*>(tile + r * kFp4RowBytes + 4 * j) = codes;
-  if (j % 8 == 0) *reinterpret_cast<uint32_t*>(tile + kFp4CodeBytes + r * kFp4RowScales + j / 2) = s;
+  *reinterpret_cast<uint2*>(tile + r * kFp4RowBytes + 8 * j) = codes;
+  if (j % 4 == 0) *reinterpret_cast<uint32_t*>(tile + kFp4CodeBytes + r * kFp4RowScales + j) = s;
 }
 
 // the block and offset of a token's slot; false: padding, or outside the pool (reported if `report`)
 template <typename P>
-__device__ __forceinline__ bool find_slot(const P& p, long long slot, bool report, long long& block, int& off) {
+__device__ __forceinline__ bool find_slot(const P& p, long long slot, bool report, int& block, int& off) {
   if (slot < 0) return false;
-  block = slot / p.block_size;
-  off = (int)(slot - block * p.block_size);
-  if (block < p.num_blocks) return true;
+  if (slot < (long long)p.num_blocks * p.block_size) {  // (a pool's rows are counted in int32)
+    block = (int)slot / p.block_size;
+    off = (int)slot - block * p.block_size;
+    return true;
+  }
   if (report) report_error(p.err_flag, PA_DEVERR_SLOT);
   return false;
 }
 
+// Rows of a thread, kRows of the CTA apart: their loads are in flight together.  A prompt's 320016 rows written and read
+// back: 44 us (24 + 20, 4.3 and 5.2 TB/s), with four 47; one 16-byte vector a thread, four rows 64 (36 + 28), one row 83.
+// A decode step's few rows go to as many CTAs as there are (64 tokens, 8 heads: 1.7 us each).
+constexpr int kBatch = 2;
+
+// Row `row` of the tokens' keys and values: token, head, which.  (At most 2^32 - 2 rows.)
+struct RowAt {
+  unsigned t;
+  int h;
+  bool is_v;
+};
+__device__ __forceinline__ RowAt row_at(const Fp4Rows& p, unsigned row) {
+  const unsigned per_token = 2u * (unsigned)p.num_kv_heads, t = row / per_token, h2 = row - t * per_token;
+  const bool is_v = h2 >= (unsigned)p.num_kv_heads;
+  return {t, (int)(is_v ? h2 - p.num_kv_heads : h2), is_v};
+}
 template <typename T>
+__device__ __forceinline__ T* row_ptr(const Fp4Rows& p, const RowAt& r, int j) {
+  return static_cast<T*>(r.is_v ? p.value : p.key) + (long long)r.t * (r.is_v ? p.value_stride : p.key_stride) +
+         (size_t)r.h * kFp4D + 16 * j;
+}
+
+template <typename T, int R>
 __global__ void __launch_bounds__(kThreads) fp4_write_kernel(const Fp4Rows p) {
   griddep_wait();
   griddep_launch_dependents();
-  const long long row = (long long)blockIdx.x * kRows + threadIdx.x / kRowThreads;
-  const int j = threadIdx.x % kRowThreads, per_token = 2 * p.num_kv_heads;
-  const long long t = row / per_token;
-  const int h2 = (int)(row - t * per_token), h = h2 % p.num_kv_heads;
-  const bool is_v = h2 >= p.num_kv_heads;
-  uint8_t* tile = nullptr;
-  int off = 0;
-  float f[8] = {};
-  if (t < p.num_tokens) {
-    long long block;
-    if (find_slot(p, p.slot_mapping[t], h2 == 0 && j == 0, block, off)) {
-      const T* src = static_cast<const T*>(is_v ? p.value : p.key) + t * (is_v ? p.value_stride : p.key_stride) +
-                     (size_t)h * kFp4D + 8 * j;
-      unpack8<T>(*reinterpret_cast<const uint4*>(src), f);
-      tile = (is_v ? p.v_cache : p.k_cache) + fp4_tile(block, p.num_kv_heads, h, p.block_size, off);
+  const unsigned rows = 2u * (unsigned)p.num_kv_heads * (unsigned)p.num_tokens;
+  const unsigned first = blockIdx.x * (unsigned)(kRows * R) + threadIdx.x / kRowThreads;
+  const int j = threadIdx.x % kRowThreads;
+  RowAt at[R];
+  Group16 x[R];
+  long long slot[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const unsigned row = first + i * kRows;
+    x[i] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    slot[i] = -1;
+    at[i] = {0, 0, false};
+    if (row < rows) {
+      at[i] = row_at(p, row);
+      slot[i] = __ldg(p.slot_mapping + at[i].t);
+      x[i] = load_group(row_ptr<T>(p, at[i], j));
     }
   }
-  const float unit = is_v ? p.v_scale : p.k_scale;
-  store_row(tile, off % kFp4Tokens, j, f, unit, __fmul_rn(6.f, unit));
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    uint8_t* tile = nullptr;
+    int block, off = 0;
+    if (find_slot(p, slot[i], !at[i].is_v && at[i].h == 0 && j == 0, block, off))
+      tile = (at[i].is_v ? p.v_cache : p.k_cache) + fp4_tile(block, p.num_kv_heads, at[i].h, p.block_size, off);
+    float f[16];
+    unpack<T>(x[i], f);
+    store_row(tile, off % kFp4Tokens, j, f, at[i].is_v ? p.v_scale : p.k_scale);
+  }
 }
 
 // Rows back in 16 bits: each is the fp32 product e2m1 * scale * unit, rounded once.
-template <typename T>
+template <typename T, int R>
 __global__ void __launch_bounds__(kThreads) fp4_read_kernel(const Fp4Rows p) {
   griddep_wait();
   griddep_launch_dependents();
-  const long long row = (long long)blockIdx.x * kRows + threadIdx.x / kRowThreads;
-  const int j = threadIdx.x % kRowThreads, per_token = 2 * p.num_kv_heads;
-  const long long t = row / per_token;
-  if (t >= p.num_tokens) return;
-  const int h2 = (int)(row - t * per_token), h = h2 % p.num_kv_heads;
-  const bool is_v = h2 >= p.num_kv_heads;
-  long long block;
-  int off;
-  if (!find_slot(p, p.slot_mapping[t], h2 == 0 && j == 0, block, off)) return;
-  const uint8_t* tile =
-      (is_v ? p.v_cache : p.k_cache) + fp4_tile(block, p.num_kv_heads, h, p.block_size, off);
-  const int r = off % kFp4Tokens;
-  const uint32_t codes = *reinterpret_cast<const uint32_t*>(tile + r * kFp4RowBytes + 4 * j);
-  const uint32_t s2 = fp4_scales_to_half(tile[kFp4CodeBytes + r * kFp4RowScales + j / 2]);
-  uint32_t x[4];
-  fp4_to_half(codes, x[0], x[1], x[2], x[3]);
-  const float unit = is_v ? p.v_scale : p.k_scale;
-  float f[8];
+  const unsigned rows = 2u * (unsigned)p.num_kv_heads * (unsigned)p.num_tokens;
+  const unsigned first = blockIdx.x * (unsigned)(kRows * R) + threadIdx.x / kRowThreads;
+  const int j = threadIdx.x % kRowThreads;
+  RowAt at[R];
+  long long slot[R];
+  uint2 codes[R];
+  uint32_t scale[R];
+  bool real[R];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t y = half_mul(x[i], half_dup_lo(s2));
-    f[2 * i] = Mma<__half>::lo(y) * unit;
-    f[2 * i + 1] = Mma<__half>::hi(y) * unit;
+  for (int i = 0; i < R; ++i) {
+    const unsigned row = first + i * kRows;
+    at[i] = {0, 0, false};
+    slot[i] = -1;
+    if (row < rows) {
+      at[i] = row_at(p, row);
+      slot[i] = __ldg(p.slot_mapping + at[i].t);
+    }
   }
-  T* dst = static_cast<T*>(is_v ? p.value : p.key) + t * (is_v ? p.value_stride : p.key_stride) + (size_t)h * kFp4D + 8 * j;
-  *reinterpret_cast<uint4*>(dst) = pack8<T>(f);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    int block, off;
+    codes[i] = make_uint2(0, 0);
+    scale[i] = 0;
+    real[i] = find_slot(p, slot[i], !at[i].is_v && at[i].h == 0 && j == 0, block, off);
+    if (real[i]) {
+      const uint8_t* tile = (at[i].is_v ? p.v_cache : p.k_cache) + fp4_tile(block, p.num_kv_heads, at[i].h, p.block_size, off);
+      const int r = off % kFp4Tokens;
+      codes[i] = *reinterpret_cast<const uint2*>(tile + r * kFp4RowBytes + 8 * j);
+      scale[i] = tile[kFp4CodeBytes + r * kFp4RowScales + j];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (!real[i]) continue;
+    const uint32_t s2 = half_dup_lo(fp4_scales_to_half(scale[i]));
+    uint32_t x[8];
+    fp4_to_half(codes[i].x, x[0], x[1], x[2], x[3]);
+    fp4_to_half(codes[i].y, x[4], x[5], x[6], x[7]);
+    const float unit = at[i].is_v ? p.v_scale : p.k_scale;
+    float f[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t y = half_mul(x[k], s2);
+      f[2 * k] = Mma<__half>::lo(y) * unit;
+      f[2 * k + 1] = Mma<__half>::hi(y) * unit;
+    }
+    store_group(row_ptr<T>(p, at[i], j), pack<T>(f));
+  }
 }
 
 // Rotary positions with the write.  A CTA takes one token: its first threads work out the pairs' angles, then its rows
-// (query heads, keys, values) go by 16 at a time.  A turned row is rounded to T first, then held in 4 bits, so that the
+// (query heads, keys, values) go by 32 at a time.  A turned row is rounded to T first, then held in 4 bits, so that the
 // cache is what the append makes of the same rows in T.
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) fp4_rope_kernel(const RopeAxesParams p) {
@@ -132,8 +203,7 @@ __global__ void __launch_bounds__(kThreads) fp4_rope_kernel(const RopeAxesParams
   const int t = blockIdx.x, half = p.rotary_dim / 2;
   griddep_wait();
   griddep_launch_dependents();
-  long long block;
-  int off;
+  int block, off;
   if (!find_slot(p, p.slot_mapping[t], threadIdx.x == 0, block, off)) return;
   if (threadIdx.x < half)
     cs[threadIdx.x] = turn_of(turn_fraction(p.inv_freq[threadIdx.x]),
@@ -145,20 +215,21 @@ __global__ void __launch_bounds__(kThreads) fp4_rope_kernel(const RopeAxesParams
     const int row = first + w;
     const bool real = row < per_token, is_q = row < p.num_q_heads, is_v = row >= p.num_q_heads + p.num_kv_heads;
     const int h = is_q ? row : (row - p.num_q_heads) % p.num_kv_heads;
-    float f[8] = {};
+    float f[16] = {};
     if (real) {
       const T* src = is_q ? static_cast<const T*>(p.q) + t * p.q_stride
                           : is_v ? static_cast<const T*>(p.value) + t * p.value_stride
                                  : static_cast<const T*>(p.key) + t * p.key_stride;
-      const uint4 x = *reinterpret_cast<const uint4*>(src + (size_t)h * kFp4D + 8 * j);
-      unpack8<T>(x, f);
-      *reinterpret_cast<uint4*>(&rows[w][8 * j]) = x;
+      const uint4* at = reinterpret_cast<const uint4*>(src + (size_t)h * kFp4D + 16 * j);
+      const Group16 x = {at[0], at[1]};  // (not through the read-only path: q_out may be q)
+      unpack<T>(x, f);
+      store_group(&rows[w][16 * j], x);
     }
     __syncwarp();  // a row belongs to one warp
     if (real && !is_v) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = 8 * j + i;
+      for (int i = 0; i < 16; ++i) {
+        const int e = 16 * j + i;
         if (e < p.rotary_dim) {
           const bool second = INTERLEAVED ? e & 1 : e >= half;
           const int pair = INTERLEAVED ? e / 2 : second ? e - half : e;
@@ -169,25 +240,29 @@ __global__ void __launch_bounds__(kThreads) fp4_rope_kernel(const RopeAxesParams
         }
       }
     }
-    const uint4 y = pack8<T>(f);
-    if (real && is_q)
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + t * p.q_out_stride + (size_t)h * kFp4D + 8 * j) = y;
-    unpack8<T>(y, f);
+    const Group16 y = pack<T>(f);
+    if (real && is_q) store_group(static_cast<T*>(p.q_out) + t * p.q_out_stride + (size_t)h * kFp4D + 16 * j, y);
+    unpack<T>(y, f);
     uint8_t* tile = real && !is_q ? static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) +
                                         fp4_tile(block, p.num_kv_heads, h, p.block_size, off)
                                   : nullptr;
-    const float unit = is_v ? p.v_scale : p.k_scale;
-    store_row(tile, off % kFp4Tokens, j, f, unit, __fmul_rn(6.f, unit));
+    store_row(tile, off % kFp4Tokens, j, f, is_v ? p.v_scale : p.k_scale);
     __syncwarp();  // the row has been read before the next one takes its place
   }
+}
+
+template <typename T, int R>
+cudaError_t launch_batch(bool read, const Fp4Rows& p, long long rows, cudaStream_t stream) {
+  const dim3 grid((unsigned)((rows + kRows * R - 1) / (kRows * R)));
+  return read ? launch_dependent(fp4_read_kernel<T, R>, grid, dim3(kThreads), 0, stream, p)
+              : launch_dependent(fp4_write_kernel<T, R>, grid, dim3(kThreads), 0, stream, p);
 }
 
 template <typename T>
 cudaError_t launch_rows_of(bool read, const Fp4Rows& p, cudaStream_t stream) {
   const long long rows = 2ll * p.num_kv_heads * p.num_tokens;
-  const dim3 grid((unsigned)((rows + kRows - 1) / kRows));
-  return read ? launch_dependent(fp4_read_kernel<T>, grid, dim3(kThreads), 0, stream, p)
-              : launch_dependent(fp4_write_kernel<T>, grid, dim3(kThreads), 0, stream, p);
+  return rows < 152ll * 8 * kRows * kBatch ? launch_batch<T, 1>(read, p, rows, stream)
+                                           : launch_batch<T, kBatch>(read, p, rows, stream);
 }
 
 }  // namespace

@@ -24,7 +24,10 @@ using namespace pa::host;
 namespace pa {
 namespace {
 
-constexpr int kThreads = 512;
+// Threads of a CTA: a step's few requests take one small CTA (64 requests of 5 tokens: 3.6 us a call, of 1024 threads 5).
+constexpr int kSmall = 256, kLarge = 1024;
+constexpr int kKept = 4;              // requests of a thread whose numbers it keeps between the two passes over them
+constexpr int kAhead = 4;             // rows of a thread whose loads are in flight together
 constexpr int kMaxSeqs = 16384;      // whose sums fit shared memory
 constexpr int kMaxTablesCluster = 8;
 
@@ -71,18 +74,33 @@ struct Sums {
 };
 
 // Called by all threads.  rows_of, blocks_of (nullable): [N + 1], the sums over the requests before each one.
-template <bool kTrim>
+template <bool kTrim, int kThreads>
 __device__ __forceinline__ Sums add_up(const TablesParams& p, long long* scratch, int* rows_of, int* blocks_of) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int run = (p.num_seqs + kThreads - 1) / kThreads;
   const int begin = min(p.num_seqs, run * (int)threadIdx.x), end = min(p.num_seqs, begin + run);
   long long rows = 0, blocks = 0;
   bool bad = false;
-  for (int s = begin; s < end; ++s) {
-    const Request r = request<kTrim>(p, s);
-    bad = bad || r.bad;
-    rows += r.bad ? 0 : r.wanted;
-    blocks += r.blocks;
+  int row[kKept] = {}, block[kKept] = {};
+  if (run <= kKept) {
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      if (begin + i < end) {
+        const Request r = request<kTrim>(p, begin + i);
+        bad = bad || r.bad;
+        row[i] = r.bad ? 0 : r.wanted;
+        block[i] = r.blocks;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) rows += row[i], blocks += block[i];
+  } else {
+    for (int s = begin; s < end; ++s) {
+      const Request r = request<kTrim>(p, s);
+      bad = bad || r.bad;
+      rows += r.bad ? 0 : r.wanted;
+      blocks += r.blocks;
+    }
   }
   long long rows_to = rows, blocks_to = blocks;
 #pragma unroll
@@ -91,24 +109,44 @@ __device__ __forceinline__ Sums add_up(const TablesParams& p, long long* scratch
     if (lane >= off) rows_to += x, blocks_to += y;
   }
   if (lane == 31) scratch[2 * warp] = rows_to, scratch[2 * warp + 1] = blocks_to;
-  bad = __syncthreads_or(bad);
   Sums sums = {0, 0, *p.num_free, false};
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) rows_to += scratch[2 * w], blocks_to += scratch[2 * w + 1];
-    sums.rows += scratch[2 * w];
-    sums.blocks += scratch[2 * w + 1];
+  bad = __syncthreads_or(bad);
+  // the warps' sums, added up by the first one: scratch[2 w] becomes what lies before warp w, the last two the totals
+  constexpr int kWarps = kThreads / 32;
+  if (warp == 0) {
+    const long long r = lane < kWarps ? scratch[2 * lane] : 0, b = lane < kWarps ? scratch[2 * lane + 1] : 0;
+    long long x = r, y = b;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, x, off), v = __shfl_up_sync(0xffffffffu, y, off);
+      if (lane >= off) x += u, y += v;
+    }
+    if (lane < kWarps) scratch[2 * lane] = x - r, scratch[2 * lane + 1] = y - b;
+    if (lane == 31) scratch[2 * kWarps] = x, scratch[2 * kWarps + 1] = y;
   }
+  __syncthreads();
+  rows_to += scratch[2 * warp], blocks_to += scratch[2 * warp + 1];
+  sums.rows = scratch[2 * kWarps], sums.blocks = scratch[2 * kWarps + 1];
   const bool state = !bad && sums.free >= 0 && sums.free <= p.num_blocks;
   sums.ok = state && (kTrim ? sums.free + sums.blocks <= p.num_blocks
                             : sums.blocks <= sums.free && sums.rows <= p.num_rows);
   if (sums.ok && blocks_of != nullptr) {
     int q = (int)(rows_to - rows), b = (int)(blocks_to - blocks);
-    for (int s = begin; s < end; ++s) {
-      const Request r = request<kTrim>(p, s);
+    auto put = [&](int s, int r, int n) {
       if (rows_of != nullptr) rows_of[s] = q;
       blocks_of[s] = b;
-      q += r.wanted;
-      b += r.blocks;
+      q += r;
+      b += n;
+    };
+    if (run <= kKept) {
+#pragma unroll
+      for (int i = 0; i < kKept; ++i)
+        if (begin + i < end) put(begin + i, row[i], block[i]);
+    } else {
+      for (int s = begin; s < end; ++s) {
+        const Request r = request<kTrim>(p, s);
+        put(s, r.wanted, r.blocks);
+      }
     }
     if (threadIdx.x == 0) {
       if (rows_of != nullptr) rows_of[p.num_seqs] = (int)sums.rows;
@@ -131,7 +169,7 @@ __device__ __forceinline__ int owner(const int* of, int n, int x) {
 }
 
 // One CTA: the new lengths, or the error.
-template <bool kTrim>
+template <bool kTrim, int kThreads>
 __device__ __forceinline__ void commit(const TablesParams& p, const Sums& sums) {
   if (!sums.ok) {
     if (threadIdx.x == 0) {
@@ -155,96 +193,128 @@ __device__ __forceinline__ void all_read() {
 }
 
 // kAlone: the grid is one cluster, which writes the lengths too (else commit_kernel does).
-template <bool kAlone>
+template <bool kAlone, int kThreads>
 __global__ void __launch_bounds__(kThreads) extend_kernel(const TablesParams p) {
   extern __shared__ int sums_of[];  // rows before each request, then blocks
-  __shared__ long long scratch[2 * kThreads / 32];
+  __shared__ long long scratch[2 * kThreads / 32 + 2];
   int* rows_of = sums_of;
   int* blocks_of = sums_of + p.num_seqs + 1;
   griddep_wait();
-  const Sums sums = add_up<false>(p, scratch, rows_of, blocks_of);
+  const Sums sums = add_up<false, kThreads>(p, scratch, rows_of, blocks_of);
   const int B = p.block_size, total = sums.ok ? (int)sums.rows : 0;
   for (int s = blockIdx.x * kThreads + threadIdx.x; s <= p.num_seqs; s += gridDim.x * kThreads)
     p.query_start[s] = sums.ok ? rows_of[s] : 0;
-  for (long long t = (long long)blockIdx.x * kThreads + threadIdx.x; t < p.num_rows; t += (long long)gridDim.x * kThreads) {
-    long long slot = -1;
-    int pos = 0;
-    if (t < total) {
-      const int s = owner(rows_of, p.num_seqs, (int)t);
-      const int held = p.held[s];
-      pos = p.seq_lens[s] + (int)t - rows_of[s];
-      const int b = pos / B, off = pos - b * B;
-      int32_t* entry = p.block_tables + (long long)s * p.max_blocks + b;
-      int block;
-      if (b < held) {
-        block = *entry;
-      } else {
-        block = p.free_blocks[sums.free - 1 - (blocks_of[s] + b - held)];
-        if (off == 0) *entry = block;  // (a fresh block's first token is new: the blocks held hold the others)
-      }
-      if (block >= 0 && block < p.num_blocks) slot = (long long)block * B + off;
-      else report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+  const long long step = (long long)gridDim.x * kThreads;
+  for (long long t0 = (long long)blockIdx.x * kThreads + threadIdx.x; t0 < p.num_rows; t0 += kAhead * step) {
+    int s[kAhead], held[kAhead], pos[kAhead], block[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const long long t = t0 + i * step;
+      s[i] = t < total ? owner(rows_of, p.num_seqs, (int)t) : -1;
+      held[i] = s[i] >= 0 ? p.held[s[i]] : 0;
+      pos[i] = s[i] >= 0 ? p.seq_lens[s[i]] + (int)t - rows_of[s[i]] : 0;
     }
-    p.slot_mapping[t] = slot;
-    p.positions[t] = pos;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      block[i] = -1;
+      if (s[i] >= 0) {
+        const int b = pos[i] / B;
+        block[i] = b < held[i] ? p.block_tables[(long long)s[i] * p.max_blocks + b]
+                               : p.free_blocks[sums.free - 1 - (blocks_of[s[i]] + b - held[i])];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const long long t = t0 + i * step;
+      if (t >= p.num_rows) break;
+      long long slot = -1;
+      if (s[i] >= 0) {
+        const int b = pos[i] / B, off = pos[i] - b * B;
+        // (a fresh block's first token is new: the blocks held hold the others)
+        if (b >= held[i] && off == 0) p.block_tables[(long long)s[i] * p.max_blocks + b] = block[i];
+        if (block[i] >= 0 && block[i] < p.num_blocks) slot = (long long)block[i] * B + off;
+        else report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+      }
+      p.slot_mapping[t] = slot;
+      p.positions[t] = pos[i];
+    }
   }
   if constexpr (kAlone) {
     all_read();
-    if (blockIdx.x == 0) commit<false>(p, sums);
+    if (blockIdx.x == 0) commit<false, kThreads>(p, sums);
   }
   __threadfence();  // see the file comment
 }
 
-template <bool kAlone>
+template <bool kAlone, int kThreads>
 __global__ void __launch_bounds__(kThreads) trim_kernel(const TablesParams p) {
   extern __shared__ int blocks_of[];
-  __shared__ long long scratch[2 * kThreads / 32];
+  __shared__ long long scratch[2 * kThreads / 32 + 2];
   griddep_wait();
-  const Sums sums = add_up<true>(p, scratch, nullptr, blocks_of);
+  const Sums sums = add_up<true, kThreads>(p, scratch, nullptr, blocks_of);
   const int B = p.block_size, total = sums.ok ? (int)sums.blocks : 0;
-  for (int i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
-    const int s = owner(blocks_of, p.num_seqs, i);
-    const int kept = (int)(((long long)p.wanted[s] + B - 1) / B);
-    int32_t* entry = p.block_tables + (long long)s * p.max_blocks + kept + (i - blocks_of[s]);
-    const int block = *entry;
-    if (block < 0 || block >= p.num_blocks) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
-    p.free_blocks[sums.free + total - 1 - i] = block;
-    *entry = -1;
+  const long long step = (long long)gridDim.x * kThreads;
+  for (long long i0 = (long long)blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += kAhead * step) {
+    int32_t* entry[kAhead];
+    int block[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const long long i = i0 + j * step;
+      entry[j] = nullptr;
+      if (i < total) {
+        const int s = owner(blocks_of, p.num_seqs, (int)i);
+        const int kept = (int)(((long long)p.wanted[s] + B - 1) / B);
+        entry[j] = p.block_tables + (long long)s * p.max_blocks + kept + (i - blocks_of[s]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) block[j] = entry[j] != nullptr ? *entry[j] : 0;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (entry[j] == nullptr) break;
+      if (block[j] < 0 || block[j] >= p.num_blocks) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
+      p.free_blocks[sums.free + total - 1 - (i0 + j * step)] = block[j];
+      *entry[j] = -1;
+    }
   }
   if constexpr (kAlone) {
     all_read();
-    if (blockIdx.x == 0) commit<true>(p, sums);
+    if (blockIdx.x == 0) commit<true, kThreads>(p, sums);
   }
   __threadfence();
 }
 
 template <bool kTrim>
-__global__ void __launch_bounds__(kThreads) commit_kernel(const TablesParams p) {
-  __shared__ long long scratch[2 * kThreads / 32];
+__global__ void __launch_bounds__(kLarge) commit_kernel(const TablesParams p) {
+  constexpr int kThreads = kLarge;
+  __shared__ long long scratch[2 * kThreads / 32 + 2];
   griddep_wait();
-  const Sums sums = add_up<kTrim>(p, scratch, nullptr, nullptr);
-  commit<kTrim>(p, sums);
+  const Sums sums = add_up<kTrim, kThreads>(p, scratch, nullptr, nullptr);
+  commit<kTrim, kThreads>(p, sums);
   __threadfence();
 }
 
-// work: rows (extend), or blocks that a call may release (trim), at most
 template <bool kTrim>
-cudaError_t launch(const TablesParams& p, long long work, cudaStream_t stream) {
+cudaError_t launch(const TablesParams& p, cudaStream_t stream) {
   const size_t smem = (size_t)(p.num_seqs + 1) * sizeof(int) * (kTrim ? 1 : 2);
-  auto alone = kTrim ? trim_kernel<true> : extend_kernel<true>;
-  auto grid = kTrim ? trim_kernel<false> : extend_kernel<false>;
-  const long long ctas = std::max(1ll, (work + 4 * kThreads - 1) / (4 * kThreads));
-  const bool one = kTrim || ctas <= kMaxTablesCluster;
-  cudaError_t e = cudaFuncSetAttribute(one ? alone : grid, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  if (one) {
-    int cluster = 1;
-    while (cluster < kMaxTablesCluster && cluster < ctas) cluster *= 2;
-    return launch_cluster(alone, dim3((unsigned)cluster), dim3(kThreads), smem, cluster, true, stream, p);
+  const long long ctas = std::max(1ll, ((long long)p.num_rows + kAhead * kLarge - 1) / (kAhead * kLarge));
+  auto run = [&](void (*kernel)(TablesParams), int grid, int threads, int cluster, size_t bytes) {
+    cudaError_t e = cudaSuccess;
+    if (bytes > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return e != cudaSuccess ? e : launch_cluster(kernel, dim3((unsigned)grid), dim3(threads), bytes, cluster, true, stream, p);
+  };
+  // (few requests release few blocks, as a rule: one CTA; many at once take a millisecond's fraction there, too)
+  if (p.num_seqs <= kSmall && ctas == 1)
+    return run(kTrim ? trim_kernel<true, kSmall> : extend_kernel<true, kSmall>, 1, kSmall, 1, smem);
+  if (kTrim || ctas <= kMaxTablesCluster) {
+    int cluster = kTrim ? kMaxTablesCluster : 1;
+    while (cluster < ctas) cluster *= 2;
+    return run(kTrim ? trim_kernel<true, kLarge> : extend_kernel<true, kLarge>, cluster, kLarge, cluster, smem);
   }
-  e = launch_cluster(grid, dim3((unsigned)std::min(ctas, 304ll)), dim3(kThreads), smem, 1, true, stream, p);
-  if (e != cudaSuccess) return e;
-  return launch_cluster(commit_kernel<kTrim>, dim3(1), dim3(kThreads), 0, 1, true, stream, p);
+  if constexpr (!kTrim) {
+    const cudaError_t e = run(extend_kernel<false, kLarge>, (int)std::min(ctas, 152ll), kLarge, 1, smem);
+    return e != cudaSuccess ? e : run(commit_kernel<false>, 1, kLarge, 1, 0);
+  }
 }
 
 // Checks that both calls share.
@@ -281,7 +351,7 @@ int pa_tables_extend(int32_t* block_tables, int32_t* seq_lens, int32_t* held_blo
   if (query_start == nullptr || (num_rows > 0 && (slot_mapping == nullptr || positions == nullptr)))
     return PA_ERR_NULL_POINTER;
   if (!aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(query_start, 4)) return PA_ERR_MISALIGNED;
-  return pa::launch<false>(p, num_rows, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return pa::launch<false>(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 int pa_tables_trim(int32_t* block_tables, int32_t* seq_lens, int32_t* held_blocks, int32_t* free_blocks,
@@ -301,8 +371,7 @@ int pa_tables_trim(int32_t* block_tables, int32_t* seq_lens, int32_t* held_block
   p.err_flag = err_flag;
   const int rc = pa::check_tables(p);
   if (rc != PA_OK || num_seqs == 0) return rc;
-  const long long work = std::min((long long)num_blocks, (long long)num_seqs * max_blocks_per_seq);
-  return pa::launch<true>(p, work, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return pa::launch<true>(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // extern "C"
