@@ -563,15 +563,19 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* src, bool take) {
   return v;
 }
 
-// two scale codes at src + OFF, or zeros (see load_codes)
+// 16 bytes, or two scale codes, at src + OFF; volatile as load_codes
 template <int OFF>
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* src, bool take) {
-  uint32_t v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b16 x;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 x, 0;\n\t"
-      "@p ld.global.nc.u16 x, [%1 + %3];\n\tcvt.u32.u16 %0, x;\n\t}"
-      : "=r"(v)
-      : "l"(src), "r"((int)take), "n"(OFF));
+__device__ __forceinline__ uint4 load_row(const uint8_t* src) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(src), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* src) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1 + %2];" : "=h"(v) : "l"(src), "n"(OFF));
   return v;
 }
 
@@ -749,21 +753,23 @@ __device__ __forceinline__ void fp4_producer(const PrefillParams& p, int w, int 
     };
     int batch_no = 0, here = fetch(0), ahead = fetch(1);
     auto tile_of = [&](int kt, int g) {  // kt in the present batch or the next
-      const int x = __shfl_sync(0xffffffffu, here, kGroups * (kt % kBatch) + g);
-      const int y = __shfl_sync(0xffffffffu, ahead, kGroups * (kt % kBatch) + g);
-      return kt / kBatch == batch_no ? x : y;
+      return __shfl_sync(0xffffffffu, kt < (batch_no + 1) * kBatch ? here : ahead, (kGroups * kt + g) & 31);
     };
     uint4 raw[kGroups * kVecs];
     uint32_t scales[kGroups * kVecs];
     auto load = [&](int kt, int g) {
       const int tile = tile_of(kt, g);
       if (!kV && lane == 0 && tile == kBad) report_error(p.err_flag, PA_DEVERR_BLOCK_ID);
-      const bool take = tile >= 0;
-      const uint8_t* src = cache + (size_t)(take ? tile : 0) * kFp4TileBytes;
-      raw[2 * g] = load_codes<0>(src + code_at, take);
-      raw[2 * g + 1] = load_codes<8 * kFp4RowBytes>(src + code_at, take);
-      scales[2 * g] = load_scales<0>(src + scale_at, take);
-      scales[2 * g + 1] = load_scales<8 * kFp4RowScales>(src + scale_at, take);
+      if (tile >= 0) {
+        const uint8_t* src = cache + (size_t)tile * kFp4TileBytes;
+        raw[2 * g] = load_row<0>(src + code_at);
+        raw[2 * g + 1] = load_row<8 * kFp4RowBytes>(src + code_at);
+        scales[2 * g] = load_scales<0>(src + scale_at);
+        scales[2 * g + 1] = load_scales<8 * kFp4RowScales>(src + scale_at);
+      } else {
+        raw[2 * g] = raw[2 * g + 1] = make_uint4(0, 0, 0, 0);
+        scales[2 * g] = scales[2 * g + 1] = 0u;
+      }
     };
     // the lines of a tile further on into L2 (its registers are loaded one tile ahead, too late for HBM's latency)
     auto prefetch = [&](int kt) {
