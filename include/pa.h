@@ -500,10 +500,10 @@ int pa_read_cache_fp4(void* key, void* value, const void* k_cache, const void* v
  *   key, value   pa_decode_fp4: both NULL, or each sequence's new token of row_dtype, [num_seqs][num_kv_heads][128],
  *                stored at position seq_lens[s] - 1 in the bytes that pa_reshape_and_cache_fp4 writes, and attended
  *   alibi_slopes, test_flags  as in pa_decode_options (NULL, 0 in normal use)
- *   workspace    pa_decode_fp4: NULL, or device scratch of pa_decode_fp4_workspace_size() bytes (a few MB whatever the
- *                sizes), 256-byte aligned, with which contexts of very different lengths keep every SM busy to the end
- *                (two launches then).  Its contents on entry do not matter.  Calls that may overlap, and graphs that
- *                may be replayed at once, need one each.
+ *   workspace    pa_decode_fp4: NULL, or device scratch of pa_decode_fp4_workspace_size(...) bytes, 256-byte aligned, with
+ *                which long contexts of very different lengths keep every SM busy to the end (two launches then).  That
+ *                size is a few MB, or 0 where these arguments use none (and for invalid ones).  Its contents on entry
+ *                do not matter.  Calls that may overlap, and graphs that may be replayed at once, need one each.
  *   Softmax weights enter the value product as one fp16 term.  A bf16 query row goes in as fp16 over a power of two:
  *   what lies more than 2^-14 below its largest element loses bits, by at most 2^-25 of the largest.
  */
@@ -512,7 +512,8 @@ int pa_decode_fp4(void* out, const void* q, void* k_cache, void* v_cache, const 
                   int32_t max_blocks_per_seq, const pa_cache_desc* cache, int32_t row_dtype, float scale, int32_t window,
                   int32_t num_sinks, float k_scale, float v_scale, const float* alibi_slopes, uint32_t test_flags,
                   void* workspace, size_t workspace_bytes, int32_t* err_flag, void* stream);
-size_t pa_decode_fp4_workspace_size(void);
+size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                    const pa_cache_desc* cache, int32_t window, int32_t num_sinks);
 int pa_prefill_fp4(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                    const int32_t* seq_lens, const int32_t* query_start, int32_t num_seqs, int32_t num_query_tokens,
                    int32_t num_q_heads, int32_t max_blocks_per_seq, int32_t max_query_len, const pa_cache_desc* cache,

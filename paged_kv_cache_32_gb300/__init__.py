@@ -112,7 +112,7 @@ def lib() -> ctypes.CDLL:
         L.pa_read_cache_fp4.restype = ctypes.c_int
         L.pa_decode_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, desc_p, i32, f32, i32, i32, f32, f32, vp,
                                     ctypes.c_uint32, vp, sz, vp, vp]
-        L.pa_decode_fp4_workspace_size.argtypes = []
+        L.pa_decode_fp4_workspace_size.argtypes = [i32, i32, i32, desc_p, i32, i32]
         L.pa_decode_fp4_workspace_size.restype = sz
         L.pa_decode_fp4.restype = ctypes.c_int
         L.pa_prefill_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, desc_p, i32, f32, i32, i32, f32,
@@ -731,19 +731,14 @@ def _attention_fp4(where, host, out, q, k_cache, v_cache, block_tables, seq_lens
     return dev, code, desc, err, shape, table
 
 
-_fp4_workspace_bytes = 0
+_FP4_WORKSPACE: dict = {}  # sizes of a call -> bytes
 
 
-def _fp4_workspace() -> int:
-    global _fp4_workspace_bytes
-    if not _fp4_workspace_bytes:
-        _fp4_workspace_bytes = int(lib().pa_decode_fp4_workspace_size())
-    return _fp4_workspace_bytes
-
-
-def pa_decode_fp4_workspace_size() -> int:
-    """Bytes of the workspace of pa_decode_fp4, whatever the call's sizes."""
-    return _fp4_workspace()
+def pa_decode_fp4_workspace_size(num_seqs: int, num_q_heads: int, max_blocks_per_seq: int, desc: pa_cache_desc,
+                                 window: int | None = None, num_sinks: int = 0) -> int:
+    """Bytes of the workspace that pa_decode_fp4 uses for these sizes (0: none)."""
+    return int(lib().pa_decode_fp4_workspace_size(_int32(num_seqs), _int32(num_q_heads), _int32(max_blocks_per_seq), desc,
+                                                  _INT32_MAX if window is None else _int32(window), _int32(num_sinks)))
 
 
 def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, k_scale: float, v_scale: float,
@@ -753,7 +748,7 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float
     ``window`` (None: all) and the first ``num_sinks`` positions.  out, q [num_seqs, num_q_heads, 128] fp16 or bf16;
     ``key`` / ``value`` [num_seqs, num_kv_heads, 128]: each sequence's new token, stored at position seq_lens[s] - 1 as
     pa_reshape_and_cache_fp4 does and attended in the same call.  ``workspace``: a uint8 device tensor of
-    pa_decode_fp4_workspace_size() bytes, allocated with torch when None; calls that may overlap need one each."""
+    pa_decode_fp4_workspace_size(...) bytes, allocated with torch when None; calls that may overlap need one each."""
     where = "pa_decode_fp4"
     dev, code, desc, err, shape, table = _attention_fp4(where, True, out, q, k_cache, v_cache, block_tables, seq_lens,
                                                         err_flag, desc)
@@ -775,16 +770,27 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float
         if alibi_slopes.numel() != shape[1] or not alibi_slopes.is_contiguous():
             raise ValueError(f"{where}: one ALiBi slope per query head")
         slopes = alibi_slopes.data_ptr()
+    ws = None
+    ws_bytes = 0
     if workspace is None:
-        import torch
-        workspace = torch.empty(_fp4_workspace(), dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev:
-        raise ValueError(f"{where}: workspace is on {workspace.device}, the caches on cuda:{dev}")
+        sizes = (shape[0], shape[1], table[1], desc.num_kv_heads, desc.block_size, window, num_sinks)
+        need = _FP4_WORKSPACE.get(sizes)
+        if need is None:
+            if len(_FP4_WORKSPACE) > 4096:
+                _FP4_WORKSPACE.clear()
+            need = _FP4_WORKSPACE[sizes] = pa_decode_fp4_workspace_size(shape[0], shape[1], table[1], desc, window, num_sinks)
+        if need:
+            import torch
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace must be contiguous, on cuda:{dev}")
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _launch(lib().pa_decode_fp4, dev, (
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, block_tables.data_ptr(),
         seq_lens.data_ptr(), shape[0], shape[1], table[1], desc, code, float(scale),
         _INT32_MAX if window is None else _int32(window), _int32(num_sinks), float(k_scale), float(v_scale), slopes,
-        int(test_flags), workspace.data_ptr(), workspace.numel() * workspace.element_size(), err, _stream_of(dev, stream)), where)
+        int(test_flags), ws, ws_bytes, err, _stream_of(dev, stream)), where)
 
 
 def pa_prefill_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, query_start, max_query_len: int, scale: float,

@@ -37,6 +37,8 @@ cudaError_t launch_fp4_rows(int row_dtype, const WindowParams& p, bool slots, cu
 constexpr int kFp4EvenGrid = 152 * 4;
 size_t fp4_even_workspace();
 cudaError_t launch_fp4_even(int row_dtype, const WindowParams& p, float* workspace, cudaStream_t stream);
+// does a decode step use such a workspace?
+bool fp4_deals_evenly(const pa_cache_desc* cache, const WindowParams& p);
 // a decode step, with its kernel and split chosen (workspace: nullable); a chunk, with its kernel chosen too (a PA_* status)
 int fp4_decode(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, float* workspace, cudaStream_t stream);
 int fp4_chunk(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, cudaStream_t stream);

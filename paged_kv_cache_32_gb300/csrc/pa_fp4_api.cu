@@ -138,7 +138,19 @@ int pa_read_cache_fp4(void* key, void* value, const void* k_cache, const void* v
   return pa::launch_fp4_read(row_dtype, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-size_t pa_decode_fp4_workspace_size(void) { return pa::fp4_even_workspace(); }
+size_t pa_decode_fp4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                    const pa_cache_desc* cache, int32_t window, int32_t num_sinks) {
+  if (check_attention(cache, PA_F16, num_seqs, num_q_heads, max_blocks_per_seq, 1.f, window, num_sinks, 1.f, 1.f) != PA_OK)
+    return 0;
+  pa::WindowParams p = {};
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.max_blocks = max_blocks_per_seq;
+  p.window = window;
+  p.sinks = num_sinks;
+  return pa::fp4_deals_evenly(cache, p) ? pa::fp4_even_workspace() : 0;
+}
 
 int pa_decode_fp4(void* out, const void* q, void* k_cache, void* v_cache, const void* key, const void* value,
                   const int32_t* block_tables, const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads,
@@ -157,7 +169,6 @@ int pa_decode_fp4(void* out, const void* q, void* k_cache, void* v_cache, const 
       !aligned(value, 16) || !aligned(seq_lens, 4) || !aligned(block_tables, 4) || !aligned(alibi_slopes, 4))
     return PA_ERR_MISALIGNED;
   if ((int64_t)num_seqs * num_q_heads > kInt32Max) return PA_ERR_TOO_LARGE;
-  if (workspace != nullptr && workspace_bytes < pa::fp4_even_workspace()) return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return PA_ERR_MISALIGNED;
   pa::WindowParams p = base_params(cache, out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs, num_q_heads,
                                    max_blocks_per_seq, scale, window, num_sinks, k_scale, v_scale, err_flag);
@@ -167,6 +178,8 @@ int pa_decode_fp4(void* out, const void* q, void* k_cache, void* v_cache, const 
   p.new_v = value;
   p.k_cache_out = k_cache;
   p.v_cache_out = v_cache;
+  if (workspace != nullptr && pa::fp4_deals_evenly(cache, p) && workspace_bytes < pa::fp4_even_workspace())
+    return PA_ERR_WORKSPACE;
   return pa::fp4_decode(cache, row_dtype, p, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
 }
 

@@ -311,7 +311,7 @@ namespace pa {
 // the table holds makes items nearly equal and lets many start far from their sequence's: those run as well in one
 // launch.  (The lengths themselves are on the device: short ones in a wide table cost a dealt out call 9 to 20 us for 6 to
 // 14.)  ALiBi: only the clusters' kernel.
-bool deal_evenly(const pa_cache_desc* cache, const WindowParams& p) {
+bool fp4_deals_evenly(const pa_cache_desc* cache, const WindowParams& p) {
   const long long cap = (long long)p.max_blocks * cache->block_size, reach = (long long)p.window + p.sinks;
   const long long keys = std::min(cap, reach), group = p.num_q_heads / p.num_kv_heads;
   const long long items = (long long)p.num_seqs * p.num_kv_heads * ((group + 7) / 8);
@@ -319,7 +319,7 @@ bool deal_evenly(const pa_cache_desc* cache, const WindowParams& p) {
 }
 
 int fp4_decode(const pa_cache_desc* cache, int32_t row_dtype, WindowParams& p, float* workspace, cudaStream_t stream) {
-  if (workspace == nullptr || !deal_evenly(cache, p)) return launch_rows(cache, p, stream, row_dtype);
+  if (workspace == nullptr || !fp4_deals_evenly(cache, p)) return launch_rows(cache, p, stream, row_dtype);
   return launch_fp4_even(row_dtype, p, workspace, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -69,8 +69,14 @@ def test_attention_refusals(lib):
         assert call(lib, q=FAKE + 8) == 5 and call(lib, v=FAKE + 4) == 5 and call(lib, sl=FAKE + 2) == 5
         assert call(lib, m=1 << 28) == 7
         assert call(lib, n=0, out=None) == 0
-    need = lib.pa_decode_fp4_workspace_size()
-    assert decode(lib, ws=FAKE, ws_bytes=need - 1) == 4 and decode(lib, ws=FAKE + 64, ws_bytes=need) == 5
+    big = desc(bs=64)
+    need = pa.pa_decode_fp4_workspace_size(2, 4, 1000, big)
+    assert need > 0 and need == pa.pa_decode_fp4_workspace_size(100, 4, 700, big, window=30000)
+    assert pa.pa_decode_fp4_workspace_size(2, 4, 4, big) == 0                  # short contexts
+    assert pa.pa_decode_fp4_workspace_size(100, 4, 1000, big, window=4096) == 0  # items of nearly one length
+    assert pa.pa_decode_fp4_workspace_size(2, 3, 1000, big) == 0 and pa.pa_decode_fp4_workspace_size(2, 4, 1000, desc(bs=8)) == 0
+    assert decode(lib, big, m=1000, window=2 ** 31 - 1, ws=FAKE, ws_bytes=need - 1) == 4
+    assert decode(lib, big, m=1000, window=2 ** 31 - 1, ws=FAKE + 64, ws_bytes=need) == 5
     assert decode(lib, out=FAKE + 8) == 5
     assert decode(lib, key=FAKE) == 1 and decode(lib, key=FAKE, value=FAKE + 8) == 5 and decode(lib, slopes=FAKE + 2) == 5
     assert prefill(lib, scale=0.0) == 3 and prefill(lib, t=-1) == 3 and prefill(lib, most=-1) == 3

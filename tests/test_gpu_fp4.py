@@ -233,7 +233,10 @@ def test_decode_workspace(pa, rows, hq, hkv, block_size):
     w = case(rows, lens, [1] * len(lens), hq, hkv, block_size, BIG, 0, seed=4, slack_blocks=35000 // block_size)
     ref = w.reference()
     ref[[0, 6, -1]] = 0.0
-    ws = torch.full((pa.pa_decode_fp4_workspace_size(),), 0xFF, dtype=torch.uint8, device="cuda")
+    need = pa.pa_decode_fp4_workspace_size(len(lens), hq, w.width, pa.pa_cache_desc(w.num_blocks, block_size, hkv, 128,
+                                                                                    pa.PA_FP4_E2M1))
+    assert need > 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     s, t = Step(w), Step(w)
     s.decode(workspace=ws)
     check(s, ref, "even")
