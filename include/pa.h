@@ -559,7 +559,8 @@ int pa_rope_axes_and_cache(void* q_out, void* k_cache, void* v_cache, const void
  *   All or nothing: a request whose numbers do not fit (a negative one, more tokens than its table or than its blocks
  *   hold, more kept than there are, more rows than num_rows, a stack that does not fit) gives PA_DEVERR_TABLES, too few
  *   free blocks PA_DEVERR_NO_BLOCKS, and nothing of the state changes; extend then writes padding rows and zeros in
- *   query_start.  A block outside the pool gives PA_DEVERR_BLOCK_ID; its tokens' rows are padding.
+ *   query_start.  A block outside the pool gives PA_DEVERR_BLOCK_ID: extend's rows for it are padding,
+ *   trim puts it back on the stack as it is.
  *   num_seqs <= 16384.  The arrays do not overlap.  Two calls on one state are ordered by the caller, on one stream.
  */
 int pa_tables_extend(int32_t* block_tables, int32_t* seq_lens, int32_t* held_blocks, const int32_t* free_blocks,

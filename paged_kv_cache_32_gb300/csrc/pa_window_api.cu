@@ -259,8 +259,11 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   const bool mixed =
       mixes(items, ((long long)w.num_query_tokens / (128 >> pack) + w.num_seqs) * (w.num_q_heads >> pack));
   p.split = tile_split(items, std::min((long long)w.max_blocks * w.block_size, (long long)w.window + w.sinks + 128), fp4);
-  if (fp4)
+  if (fp4) {
+    // (a masked score is -inf times the scale, which must not vanish; bf16 queries: times their row's, in the kernel)
+    if (row_dtype == PA_F16) p.scale_log2 = std::max(p.scale_log2, 1.17549435e-38f);
     return pa::launch_prefill_fp4(row_dtype, tq, to, p, mixed, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
   if (fp8) tk = tv = tq;
   return pa::launch_prefill_tc(cache->dtype, tk, tv, tq, to, p, mixed, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

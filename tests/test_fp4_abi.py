@@ -90,6 +90,11 @@ def test_other_calls_refuse_the_type(lib):
     assert lib.pa_prefill(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, 10, 4, 4, 5, d, 0.1, None, None) == 2
     assert lib.pa_reshape_and_cache(FAKE, FAKE, FAKE, FAKE, FAKE, 2, d, None, None) == 2
     assert lib.pa_reshape_and_cache_fp8(FAKE, FAKE, FAKE, FAKE, FAKE, 2, d, 1.0, 1.0, None, None) == 2
+    assert lib.pa_decode_window(FAKE, FAKE, FAKE, FAKE, None, None, FAKE, FAKE, 2, 4, 4, d, 0.1, 8, 0, None, None, None) == 2
+    assert lib.pa_prefill_window(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, 10, 4, 4, 5, d, 0.1, 8, 0, 1.0, 1.0, None,
+                                 None) == 2
+    assert lib.pa_rope_and_cache(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 512, 512, 256, 256, FAKE, FAKE, FAKE, 4, 4, 128, 0, 1.0, d,
+                                 1.0, 1.0, None, None) == 2
     assert lib.pa_copy_blocks(FAKE, FAKE, FAKE, -1, d, None, None) == 3
     assert lib.pa_copy_blocks(FAKE, FAKE, FAKE, 2, ctypes.byref(desc(bs=8)), None, None) == 2
 

@@ -248,6 +248,14 @@ def test_decode_workspace(pa, rows, hq, hkv, block_size):
     graph.replay()
     torch.cuda.synchronize()
     assert int(t.err.item()) == 0 and torch.equal(s.out, t.out)
+    # a bounded wait that runs out is reported, and the workspace is as good as before
+    t = Step(w)
+    t.decode(workspace=ws, test_flags=pa.PA_DECODE_TEST_EXPIRE_FIRST_WAIT)
+    torch.cuda.synchronize()
+    assert int(t.err.item()) == 4
+    t = Step(w)
+    t.decode(workspace=ws)
+    assert int(t.err.item()) == 0 and torch.equal(s.out, t.out)
     # a length past the table is reported, the others stay right
     s = Step(w)
     s.lens[3] = 10 ** 6
@@ -433,6 +441,36 @@ def test_prefill_bad_block():
     got, ref = out_f64(s.out), w.reference()
     assert int(s.err.item()) == 1
     assert within_bound(got[:140], ref[:140], "f16")[0] and within_bound(got[200:], ref[200:], "f16")[0]
+
+
+@pytest.mark.parametrize("rows", ["f16", "bf16"])
+@pytest.mark.parametrize("chunk", [3, 200])
+def test_prefill_scales_and_nan(rows, chunk):
+    """A scale that leaves every visible token the same weight; a NaN query is a NaN row and no other."""
+    w = case(rows, [300, 260], [chunk, chunk], 8, 2, 16, 150, 3, seed=3)
+    w.scale = 1e-36
+    s = Step(w)
+    s.prefill()
+    check(s, w.reference(), "tiny scale")
+    w = case(rows, [300, 260], [chunk, chunk], 8, 2, 16, BIG, 0, seed=5)
+    s = Step(w)
+    s.q[chunk + 1, 5, 99] = float("nan")
+    s.prefill()
+    got, ref = out_f64(s.out), w.reference()
+    assert int(s.err.item()) == 0 and np.isnan(got[chunk + 1, 5]).all()
+    got[chunk + 1, 5] = ref[chunk + 1, 5]
+    assert within_bound(got, ref, rows)[0]
+
+
+@pytest.mark.parametrize("power", [-100, 90])
+def test_prefill_bf16_queries_of_any_size(power):
+    w = case("bf16", [300, 177], [150, 130], 8, 2, 16, BIG, 0, seed=3)
+    ref = w.reference()
+    w.q = W.to_storage(O.to_f64(w.q, "bf16") * 2.0 ** power, "bf16")
+    w.scale *= 2.0 ** -power
+    s = Step(w)
+    s.prefill()
+    check(s, ref, "scaled queries")
 
 
 # ---------------------------------------------------------------- streams and graphs
