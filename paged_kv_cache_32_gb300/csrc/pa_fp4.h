@@ -27,8 +27,8 @@ struct Fp4Rows {
 };
 cudaError_t launch_fp4_write(int row_dtype, const Fp4Rows& p, cudaStream_t stream);
 cudaError_t launch_fp4_read(int row_dtype, const Fp4Rows& p, cudaStream_t stream);
-// rotary positions with the write (p.positions: one row of num_tokens for each axis)
-cudaError_t launch_fp4_rope(int row_dtype, bool interleaved, const RopeAxesParams& p, cudaStream_t stream);
+// rotary positions with the write, where the halves of the turned elements are no multiple of a group
+cudaError_t launch_fp4_rope_cut(int row_dtype, const RopeAxesParams& p, cudaStream_t stream);
 
 // rows attention (see pa_window.h); row_dtype: of q, out and the appended rows
 cudaError_t launch_fp4_rows(int row_dtype, const WindowParams& p, bool slots, cudaStream_t stream);

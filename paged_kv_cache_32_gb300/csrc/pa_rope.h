@@ -33,5 +33,7 @@ struct RopeAxesParams : RopeParams {
 // dtype: the cache's (fp16 queries, keys and values for an FP8 cache)
 cudaError_t launch_rope(int dtype, bool interleaved, const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_rope_axes(int dtype, bool interleaved, const RopeAxesParams& p, cudaStream_t stream);
+// caches held in 4 bits; row_dtype: of queries, keys and values
+cudaError_t launch_rope_fp4(int row_dtype, bool interleaved, const RopeAxesParams& p, cudaStream_t stream);
 
 }  // namespace pa

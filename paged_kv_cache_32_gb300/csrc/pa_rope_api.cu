@@ -200,7 +200,7 @@ int pa_rope_axes_and_cache(void* q_out, void* k_cache, void* v_cache, const void
   if (done || rc != PA_OK) return rc;
   p.num_axes = num_axes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t err = fp4 ? pa::launch_fp4_rope(row_dtype, interleaved != 0, p, st)
+  const cudaError_t err = fp4 ? pa::launch_rope_fp4(row_dtype, interleaved != 0, p, st)
                               : pa::launch_rope_axes(cache->dtype, interleaved != 0, p, st);
   return err == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -91,7 +91,9 @@ def test_one_axis_is_rope(pa, dtype):
 
 @pytest.mark.parametrize("rows", ["f16", "bf16"])
 @pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("rotary,tokens,hq,hkv", [(128, 70, 8, 2), (36, 5, 7, 1), (2, 300, 0, 3), (64, 1000, 17, 4)])
+@pytest.mark.parametrize("rotary,tokens,hq,hkv", [(128, 70, 8, 2), (36, 5, 7, 1), (2, 300, 0, 3), (64, 1000, 17, 4),
+                                                  (96, 33, 4, 1), (112, 700, 3, 5), (126, 9, 0, 2), (32, 2500, 6, 2),
+                                                  (16, 1301, 1, 16), (128, 1, 64, 8)])
 def test_rope_fp4(pa, rows, interleaved, rotary, tokens, hq, hkv):
     """Over a 4-bit cache: the queries of the same call over a 16-bit cache, and its keys held in 4 bits."""
     import torch
