@@ -175,12 +175,22 @@ bool tile_kernel_takes(const pa_cache_desc* c) {
 
 // CTAs that share an item's key tiles: as many as leave each SM at most one, with four tiles or more each.  Over a 4-bit
 // cache up to two an SM, with eight tiles or more: its tiles take longer to convert, so that the longest of unequal items
-// is what a call waits for (16 sequences of 5 queries over 2500 to 20000 tokens, 64 / 8 heads: 236 us, with two 147, four
-// 155; equal lengths the same).
-int tile_split(long long items, long long max_keys, bool fp4) {
+// is what a call waits for (they start with the longest, too).  With more items than that, two an item if all at the
+// longest take no longer so than undivided: by 6 us and 1.32 a key tile for every item of an SM, and 12 us and 0.66 a
+// tile for every half, measured; or up to 15 % longer where sequences may differ, where it gains most.  (Every CTA ranks
+// the sequences: not past 512.)  5 queries each, 64 / 8 heads, 20 / 40 / 64 / 100 sequences of unequal lengths up to
+// 20000: 155 / 255 / 375 / 581 us (undivided 290 / 368 / 539 / 762), all of 8000: 157 / 261 / 369 / 580 (177 / 268 / 365 /
+// 545); one chunk of 700 over 30000, 32 / 8 heads: 451 (576).
+int tile_split(long long items, long long max_keys, bool fp4, int seqs) {
   int c = 1;
   while (c < kMaxCluster && items * c * 2 <= kSms && max_keys / (128 * 2 * c) >= 4) c *= 2;
   while (fp4 && c < kMaxCluster && items * c * 2 <= 2 * kSms && max_keys / (128 * 2 * c) >= 8) c *= 2;
+  if (fp4 && c == 1 && items > kSms && items <= 6 * kSms && seqs <= 512) {
+    const double tiles = ceil(max_keys / 128.0);
+    const double whole = ceil(items / (double)kSms) * (6.0 + 1.32 * tiles);
+    const double halves = ceil(2 * items / (double)kSms) * (12.0 + 0.66 * tiles);
+    if (halves <= (seqs > 1 ? 1.15 : 1.0) * whole) c = 2;
+  }
   return c;
 }
 
@@ -207,7 +217,7 @@ bool tiles_faster(const pa_cache_desc* cache, pa::WindowParams p, int pack) {
   const double per_tile = fp4 ? 1.4 : narrow ? 1.6 : 1.3;
   const double rows_us = (fp4 ? 6.5 : 6.0) + std::max(groups * keys / rate, slabs * (fp4 ? 1.2 : fp8 ? 1.3 : 0.85));
   const double items = kv * ceil((double)p.max_query_len / queries) * (G >> pack);
-  const int split = tile_split((long long)std::min(items, 1e9), (long long)keys, fp4);
+  const int split = tile_split((long long)std::min(items, 1e9), (long long)keys, fp4, p.num_seqs);
   const double share = items * split / kSms, tiles = ceil(keys / 128.0) / split;
   const double tile_us =
       (fp4 ? 6.0 : 5.0) + std::max(1.0, 0.5 * (share + ceil(share))) * ((fp4 ? 4.0 : 1.0) + per_tile * tiles);
@@ -258,7 +268,10 @@ int launch_tiles(const pa_cache_desc* cache, const pa::WindowParams& w, int pack
   p.max_query_len = w.max_query_len;
   const bool mixed =
       mixes(items, ((long long)w.num_query_tokens / (128 >> pack) + w.num_seqs) * (w.num_q_heads >> pack));
-  p.split = tile_split(items, std::min((long long)w.max_blocks * w.block_size, (long long)w.window + w.sinks + 128), fp4);
+  // (a split item of a sequence that lacks it still takes a cluster: not where many do)
+  p.split = tile_split(mixed && items > kSms ? kInt32Max : items,
+                       std::min((long long)w.max_blocks * w.block_size, (long long)w.window + w.sinks + 128), fp4,
+                       w.num_seqs);
   if (fp4) {
     // (a masked score is -inf times the scale, which must not vanish; bf16 queries: times their row's, in the kernel)
     if (row_dtype == PA_F16) p.scale_log2 = std::max(p.scale_log2, 1.17549435e-38f);

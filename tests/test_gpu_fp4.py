@@ -401,6 +401,32 @@ def test_prefill_few_long_items(rows, block_size, window, sinks, lens, chunks):
 
 
 @pytest.mark.parametrize("rows", ["f16", "bf16"])
+@pytest.mark.parametrize("seqs,window,sinks", [(24, BIG, 0), (24, 9000, 5), (40, BIG, 0), (40, 8000, 0)])
+def test_prefill_unequal_sequences(rows, seqs, window, sinks):
+    """More divided items than SMs, of equal and unequal lengths, in a table wide enough for 10000 tokens; the second
+    sequence has no queries, the last one is inconsistent."""
+    import torch
+    rng = np.random.default_rng(seqs)
+    chunks = [int(x) for x in rng.integers(1, 25, seqs)]
+    lens = [24 + int(x) for x in rng.integers(0, 700, seqs)]
+    lens[3:9] = [300] * 6
+    lens[seqs - 2] = 1500
+    chunks[1], chunks[-1], lens[-1] = 0, 9, 40
+    w = case(rows, lens, chunks, 16, 4, 16, window, sinks, seed=seqs)
+    ref = w.reference()
+    s = Step(w)
+    s.table = torch.cat([s.table, torch.full((seqs, 625 - s.table.shape[1]), -3, dtype=torch.int32, device="cuda")], 1)
+    s.prefill(max_query_len=24)
+    check(s, ref, "unequal sequences")
+    bad = Step(w)
+    bad.table = s.table
+    bad.lens[-1] = 8  # fewer than its queries
+    bad.prefill(max_query_len=24)
+    assert int(bad.err.item()) == 5 and torch.equal(bad.out[:-9], s.out[:-9])
+    assert torch.all(bad.out[-9:] == SENTINEL)
+
+
+@pytest.mark.parametrize("rows", ["f16", "bf16"])
 def test_prefill_mixed_batch(rows):
     """One prompt among many single tokens (more items in the grid than exist)."""
     rng = np.random.default_rng(2)
