@@ -46,6 +46,8 @@ bool encode_query_map(CUtensorMap* map, const void* base, const pa_cache_desc* c
 cudaError_t launch_prefill_tc(int dtype, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                               const CUtensorMap& to, const PrefillParams& p, bool mixed,
                               cudaStream_t stream);
+// sequences that the tile kernel over a 4-bit cache deals out with the longest first
+constexpr int kDealMaxSeqs = 96;
 // over a 4-bit cache, windowed form; row_dtype: of q and out
 cudaError_t launch_prefill_fp4(int row_dtype, const CUtensorMap& tq, const CUtensorMap& to, const PrefillParams& p,
                                bool mixed, cudaStream_t stream);

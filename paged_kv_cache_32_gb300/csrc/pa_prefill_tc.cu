@@ -93,6 +93,12 @@
 //    themselves.  Values lie in the cache with a dimension's 16 tokens side by
 //    side, so the value tile is V^T, rows of 64 keys, and P V takes it like S
 //    takes K.
+//  * 4-bit caches (kFp4, kFp4Bf16): the same with codes times scales, exact in fp16,
+//    values with tokens as rows; bf16 queries become fp16 in shared memory.  Up to 96
+//    sequences' items are dealt out evenly (PfDealtItem): one chunk of 2048 over 4856
+//    tokens, 32 / 8 heads, fp16 156 us (824 TFLOP/s; in order 166); 8 of 200-900 over
+//    770-4100, W = 1500, bf16 147 (in order 180).  Neither conversion, loads nor
+//    softmax alone bounds them; they share the issue slots.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -125,8 +131,12 @@ constexpr int kBarOff = 14 * kHalf;   // barriers, flags, the published work ite
 constexpr int kPlaceOff = 204;        // in the barrier region: the sequence whose item a split CTA takes
 constexpr int kSmsOfGb300 = 152;
 constexpr int kUnitOff = kBarOff + 512;  // the power of two of each query row of two items (bf16 queries, 4-bit cache)
+constexpr int kDealOff = kUnitOff + 2 * kTile * 4;  // the sequences in the order in which their items are dealt out
+constexpr int kDealBytes = 512;  // (kDealMaxSeqs times an int and a byte)
 constexpr int kSmemBytes = kBarOff + 512 + 1024;
 constexpr int kSmemBytesConvert = kSmemBytes + 2 * kTile * 4;
+constexpr int kSmemBytesDeal = kDealOff + kDealBytes + 1024;
+static_assert(5 * kDealMaxSeqs <= kDealBytes, "the dealt sequences' region");
 constexpr int kSBufs = 3;             // S buffers in tensor memory (columns 128 b .. 128 b + 127)
 constexpr uint32_t kOCol = 384;       // tensor-memory column of O
 constexpr int kSoftmaxWarps = 8;
@@ -464,25 +474,11 @@ struct PfWindowItem : PfItem {
   int lo_chunk, s_chunk;  // what some query of the chunk sees: [0, s_chunk) and from lo_chunk on
 };
 
-__device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfWindowItem& it, bool report) {
-  const int groups = p.num_q_heads >> p.pack_log2, per_tile = kTile >> p.pack_log2;
-  const int per_seq = p.q_tiles * groups;
-  it.s = idx / per_seq;
-  const int rem = idx % per_seq;
-  const int qt = p.q_tiles - 1 - rem / groups;
-  it.h = (rem % groups) << p.pack_log2;
-  it.q0 = __ldg(p.query_start + it.s);
-  it.n = __ldg(p.query_start + it.s + 1) - it.q0;
-  it.L = __ldg(p.seq_lens + it.s);
+// the rows and keys of the item's tile
+__device__ __forceinline__ void pf_keys(const PrefillParams& p, PfWindowItem& it) {
   const int B = p.block_size;
-  if (pf_bad_chunk(p, it)) {
-    if (report && qt == 0 && it.h == 0) report_error(p.err_flag, PA_DEVERR_QUERY);
-    return false;
-  }
-  it.tile0 = qt * per_tile;
-  if (it.tile0 >= it.n) return false;
   it.hkv = it.h / (p.num_q_heads / p.num_kv_heads);
-  const int queries = min(per_tile, it.n - it.tile0);
+  const int queries = min(kTile >> p.pack_log2, it.n - it.tile0);
   it.rows = queries << p.pack_log2;
   it.pos0 = it.L - it.n + it.tile0;
   it.nblocks_seq = (it.L + B - 1) / B;
@@ -494,6 +490,25 @@ __device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfWindo
   it.shift = (win_block - sink_blocks) * B;
   const int blocks = sink_blocks + max(0, last / B + 1 - win_block);
   it.key_tiles = (blocks * B + kTile - 1) / kTile;
+}
+
+__device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfWindowItem& it, bool report) {
+  const int groups = p.num_q_heads >> p.pack_log2, per_tile = kTile >> p.pack_log2;
+  const int per_seq = p.q_tiles * groups;
+  it.s = idx / per_seq;
+  const int rem = idx % per_seq;
+  const int qt = p.q_tiles - 1 - rem / groups;
+  it.h = (rem % groups) << p.pack_log2;
+  it.q0 = __ldg(p.query_start + it.s);
+  it.n = __ldg(p.query_start + it.s + 1) - it.q0;
+  it.L = __ldg(p.seq_lens + it.s);
+  if (pf_bad_chunk(p, it)) {
+    if (report && qt == 0 && it.h == 0) report_error(p.err_flag, PA_DEVERR_QUERY);
+    return false;
+  }
+  it.tile0 = qt * per_tile;
+  if (it.tile0 >= it.n) return false;
+  pf_keys(p, it);
   return true;
 }
 
@@ -531,6 +546,66 @@ __device__ __forceinline__ int pf_skip(const PrefillParams& p, int idx, int step
     report_error(p.err_flag, PA_DEVERR_QUERY);
   const int empty = it.s * per_seq + (p.q_tiles - tiles) * groups - idx;  // items from idx on without queries
   return (empty - 1) / step * step;
+}
+// Dealt items: those with queries only, of the longest sequences first, there and back over the CTAs (0 .. g - 1, then
+// g - 1 .. 0), which evens out items that grow shorter.  deal_sequences leaves the sequences in that order, each with the
+// number of items up to its last.
+struct PfDealtItem : PfWindowItem {};
+extern __shared__ uint8_t smem_raw[];
+__device__ __forceinline__ uint8_t* smem_base() {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+}
+// (every thread, before the CTA's first barrier)
+__device__ __forceinline__ void deal_sequences(const PrefillParams& p) {
+  int* ends = reinterpret_cast<int*>(smem_base() + kDealOff);
+  uint8_t* ids = smem_base() + kDealOff + 4 * kDealMaxSeqs;
+  const int groups = p.num_q_heads >> p.pack_log2;
+  auto items_of = [&](int s, int& len, bool report) {
+    PfItem it;
+    it.q0 = __ldg(p.query_start + s);
+    it.n = __ldg(p.query_start + s + 1) - it.q0;
+    it.L = len = __ldg(p.seq_lens + s);
+    if (!pf_bad_chunk(p, it)) return ((it.n + (kTile >> p.pack_log2) - 1) >> (7 - p.pack_log2)) * groups;
+    if (report) report_error(p.err_flag, PA_DEVERR_QUERY);
+    return 0;
+  };
+  for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x) {
+    int mine, place = 0, end = items_of(i, mine, blockIdx.x == 0);
+#pragma unroll 4
+    for (int j = 0; j < p.num_seqs; ++j) {
+      int other;
+      const int n = items_of(j, other, false);
+      if (other > mine || (other == mine && j < i)) ++place, end += n;
+    }
+    ends[place] = end;
+    ids[place] = (uint8_t)i;
+  }
+}
+__device__ __forceinline__ bool pf_item(const PrefillParams& p, int idx, PfDealtItem& it, bool) {
+  const int* ends = reinterpret_cast<const int*>(smem_base() + kDealOff);
+  const int g = gridDim.x, round = idx / g, first = round * g, pos = round & 1 ? first + (g - 1 - (idx - first)) : idx;
+  int lo = 0, hi = p.num_seqs;  // the first sequence whose items end past pos
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > pos)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  if (lo == p.num_seqs) return false;
+  const int rem = pos - (lo > 0 ? ends[lo - 1] : 0), groups = p.num_q_heads >> p.pack_log2;
+  it.s = (smem_base() + kDealOff + 4 * kDealMaxSeqs)[lo];
+  it.h = (rem % groups) << p.pack_log2;
+  it.q0 = __ldg(p.query_start + it.s);
+  it.n = __ldg(p.query_start + it.s + 1) - it.q0;
+  it.L = __ldg(p.seq_lens + it.s);
+  it.tile0 = (((it.n + (kTile >> p.pack_log2) - 1) >> (7 - p.pack_log2)) - 1 - rem / groups) * (kTile >> p.pack_log2);
+  pf_keys(p, it);
+  return true;
+}
+// past the last item: so is the rest of the walk
+__device__ __forceinline__ int pf_skip(const PrefillParams& p, int idx, int, const PfDealtItem&, bool) {
+  return max(0, p.num_seqs * (p.num_q_heads >> p.pack_log2) * p.q_tiles - idx);
 }
 __device__ __forceinline__ int first_tile(const PfItem&) { return 0; }
 __device__ __forceinline__ int first_tile(const PfSplitItem& it) { return it.first; }
@@ -915,8 +990,9 @@ __device__ __forceinline__ void split_merge(const PrefillParams& p, const float*
 // What the cache holds: the kernel's type T, E4M3 codes, or 4-bit rows (T fp16, queries and outputs in fp16 or bf16).
 enum class PfCache { kSame, kFp8, kFp4, kFp4Bf16 };
 
-// kWindow: see the file comment; kSplit: windowed, a cluster of p.split CTAs an item; kMixed: windowed, see pf_skip
-enum class PfForm { kPlain, kWindow, kSplit, kMixed };
+// kWindow: see the file comment; kSplit: windowed, a cluster of p.split CTAs an item; kMixed: windowed, see pf_skip;
+// kDealt: windowed, see PfDealtItem
+enum class PfForm { kPlain, kWindow, kSplit, kMixed, kDealt };
 
 // Persistent: each CTA takes items blockIdx.x, blockIdx.x + gridDim.x, ...  Every role walks the same
 // items; the K/V rings, the S buffers and their barriers run on across items (tg counts this CTA's
@@ -937,17 +1013,20 @@ __global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThre
   static_assert(D == 128 || (D == 64 && kWindow && !kCoded), "head size");
   using Item = std::conditional_t<
       kSplit, PfSplitItem,
-      std::conditional_t<kForm == PfForm::kMixed, PfMixedItem, std::conditional_t<kWindow, PfWindowItem, PfItem>>>;
+      std::conditional_t<kForm == PfForm::kMixed, PfMixedItem,
+                         std::conditional_t<kForm == PfForm::kDealt, PfDealtItem,
+                                            std::conditional_t<kWindow, PfWindowItem, PfItem>>>>;
   // split: the CTAs of a cluster take the same items
   int idx0 = kSplit ? blockIdx.x / (unsigned)p.split : blockIdx.x;
   const int idx_step = kSplit ? gridDim.x / (unsigned)p.split : gridDim.x;
-  const int n_items = p.num_seqs * (kWindow ? p.num_q_heads >> p.pack_log2 : p.num_q_heads) * p.q_tiles;
+  int n_items = p.num_seqs * (kWindow ? p.num_q_heads >> p.pack_log2 : p.num_q_heads) * p.q_tiles;
+  // (a CTA's place in the last round may be one that comes back to an earlier item)
+  if constexpr (kForm == PfForm::kDealt) n_items = (int)((n_items + gridDim.x - 1) / gridDim.x * gridDim.x);
   const int B = p.block_size;
   const int blocks_per_tile = kTile / B;
   const int slots = kHalves * blocks_per_tile;  // tensor-map copies per tile: one per block and half
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_base();
   // every softmax warp has read item k's publication (phase k; item k + 1 is published only after it, so
   // no softmax warp can find bar_qs two phases on)
   uint64_t* bar_q = reinterpret_cast<uint64_t*>(smem + kBarOff);
@@ -993,6 +1072,7 @@ __global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThre
   }
   // Split items that outnumber the SMs start with those of the longest sequences (ties: the first), so that what starts
   // last is short.  (16 sequences of 5 queries over 3000 to 19600 tokens, 64 / 8 heads: 113 us, in their own order 134.)
+  if constexpr (kForm == PfForm::kDealt) deal_sequences(p);
   if constexpr (kSplit && kFp4) {
     if (gridDim.x > (unsigned)kSmsOfGb300) {
       const int per_seq = n_items / p.num_seqs, place = idx0 / per_seq;
@@ -1642,7 +1722,9 @@ static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, 
                                   const CUtensorMap& to, const PrefillParams& p, cudaStream_t stream) {
   const long long items = (long long)p.num_seqs * (p.num_q_heads >> p.pack_log2) * p.q_tiles;
   if (items == 0) return cudaSuccess;
-  constexpr int kBytes = kCache == PfCache::kFp4Bf16 ? kSmemBytesConvert : kSmemBytes;
+  constexpr int kBytes = kForm == PfForm::kDealt       ? kSmemBytesDeal
+                         : kCache == PfCache::kFp4Bf16 ? kSmemBytesConvert
+                                                       : kSmemBytes;
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1666,6 +1748,11 @@ static cudaError_t launch_prefill(const CUtensorMap& tk, const CUtensorMap& tv, 
 template <typename T, PfCache kCache, int D>
 static cudaError_t launch_window(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                  const CUtensorMap& to, const PrefillParams& p, bool mixed, cudaStream_t stream) {
+  // (a walk of one item a CTA has nothing to even out)
+  if constexpr (kCache == PfCache::kFp4 || kCache == PfCache::kFp4Bf16)
+    if (p.split == 1 && p.num_seqs <= kDealMaxSeqs &&
+        (long long)p.num_seqs * (p.num_q_heads >> p.pack_log2) * p.q_tiles > kSmsOfGb300)
+      return launch_prefill<T, PfForm::kDealt, kCache, D>(tk, tv, tq, to, p, stream);
   return p.split > 1 ? launch_prefill<T, PfForm::kSplit, kCache, D>(tk, tv, tq, to, p, stream)
          : mixed     ? launch_prefill<T, PfForm::kMixed, kCache, D>(tk, tv, tq, to, p, stream)
                      : launch_prefill<T, PfForm::kWindow, kCache, D>(tk, tv, tq, to, p, stream);

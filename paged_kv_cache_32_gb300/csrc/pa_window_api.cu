@@ -175,12 +175,12 @@ bool tile_kernel_takes(const pa_cache_desc* c) {
 
 // CTAs that share an item's key tiles: as many as leave each SM at most one, with four tiles or more each.  Over a 4-bit
 // cache up to two an SM, with eight tiles or more: its tiles take longer to convert, so that the longest of unequal items
-// is what a call waits for (they start with the longest, too).  With more items than that, two an item if all at the
-// longest take no longer so than undivided: by 6 us and 1.32 a key tile for every item of an SM, and 12 us and 0.66 a
-// tile for every half, measured; or up to 15 % longer where sequences may differ, where it gains most.  (Every CTA ranks
-// the sequences: not past 512.)  5 queries each, 64 / 8 heads, 20 / 40 / 64 / 100 sequences of unequal lengths up to
-// 20000: 155 / 255 / 375 / 581 us (undivided 290 / 368 / 539 / 762), all of 8000: 157 / 261 / 369 / 580 (177 / 268 / 365 /
-// 545); one chunk of 700 over 30000, 32 / 8 heads: 451 (576).
+// is what a call waits for (they start with the longest, too).  With more items than that, two an item if that takes less
+// time with all at the longest, by 6 us and 1.32 a key tile for every item of an SM and 12 us and 0.66 a tile for every
+// half: by 7 % or more where whole items are dealt out with the longest first, or, with more sequences, by -15 %, since
+// whole ones then come in any order.  (Every CTA ranks the sequences: not past 512.)  5 queries each, 64 / 8 heads, 20 /
+// 40 / 64 / 100 sequences of unequal lengths up to 20000, in halves: 155 / 255 / 375 / 581 us, dealt out 211 / 284 / 342
+// / -, in order 290 / 368 / 539 / 762; one chunk of 700 over 30000, 32 / 8 heads: 451 in halves, 560 dealt out.
 int tile_split(long long items, long long max_keys, bool fp4, int seqs) {
   int c = 1;
   while (c < kMaxCluster && items * c * 2 <= kSms && max_keys / (128 * 2 * c) >= 4) c *= 2;
@@ -189,7 +189,7 @@ int tile_split(long long items, long long max_keys, bool fp4, int seqs) {
     const double tiles = ceil(max_keys / 128.0);
     const double whole = ceil(items / (double)kSms) * (6.0 + 1.32 * tiles);
     const double halves = ceil(2 * items / (double)kSms) * (12.0 + 0.66 * tiles);
-    if (halves <= (seqs > 1 ? 1.15 : 1.0) * whole) c = 2;
+    if (halves <= (seqs <= pa::kDealMaxSeqs ? 0.93 : 1.15) * whole) c = 2;
   }
   return c;
 }

@@ -427,6 +427,28 @@ def test_prefill_unequal_sequences(rows, seqs, window, sinks):
 
 
 @pytest.mark.parametrize("rows", ["f16", "bf16"])
+@pytest.mark.parametrize("seqs,most,window,sinks", [(1, 1300, BIG, 0), (2, 700, 90, 2), (20, 60, BIG, 0), (39, 24, 500, 4),
+                                                    (77, 33, BIG, 0), (96, 40, 30, 0), (97, 40, BIG, 0)])
+def test_prefill_more_items_than_sms(rows, seqs, most, window, sinks):
+    """Whole and partial rounds of items, sequences without queries and one that is inconsistent among them."""
+    import torch
+    rng = np.random.default_rng(seqs)
+    chunks = [most] + [int(x) for x in rng.integers(0, most + 1, seqs - 1)]
+    lens = [c + int(x) for c, x in zip(chunks, rng.integers(0, 400, seqs))]
+    w = case(rows, lens, chunks, 16, 4, 16, window, sinks, seed=seqs)
+    s = Step(w)
+    s.prefill()
+    check(s, w.reference(), "many items")
+    assert not torch.any(s.out == SENTINEL)
+    start, n = w.query_start(), seqs - 1
+    bad = Step(w)
+    bad.lens[n] = -1
+    bad.prefill()
+    assert int(bad.err.item()) == 5 and torch.equal(bad.out[:start[n]], s.out[:start[n]])
+    assert torch.all(bad.out[start[n]:] == SENTINEL)
+
+
+@pytest.mark.parametrize("rows", ["f16", "bf16"])
 def test_prefill_mixed_batch(rows):
     """One prompt among many single tokens (more items in the grid than exist)."""
     rng = np.random.default_rng(2)
