@@ -460,6 +460,18 @@ def test_prefill_mixed_batch(rows):
     check(s, w.reference(), "mixed batch")
 
 
+@pytest.mark.parametrize("rows", ["f16", "bf16"])
+def test_prefill_prompt_among_single_tokens(rows):
+    """As above, with few enough sequences that their items are dealt out: far more places than items."""
+    rng = np.random.default_rng(3)
+    chunks = [1] * 60 + [900] + [1] * 35
+    lens = [c + int(x) for c, x in zip(chunks, rng.integers(0, 300, 96))]
+    w = case(rows, lens, chunks, 16, 4, 32, BIG, 0, seed=12)
+    s = Step(w)
+    s.prefill()
+    check(s, w.reference(), "a prompt among single tokens")
+
+
 def test_prefill_rows_and_bad_chunks():
     """Rows that no chunk owns keep what they held; an inconsistent chunk is reported and skipped."""
     import torch
