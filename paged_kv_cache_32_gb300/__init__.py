@@ -229,7 +229,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, pa
     need = pa_decode_workspace_size(num_seqs, num_q_heads, max_blocks, desc, partition_size)
     if workspace is None and need > 0:
         import torch
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=k_cache.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(seq_lens), num_seqs,
             num_q_heads, max_blocks, ctypes.byref(desc), float(scale), int(partition_size), _ptr(workspace), ws_bytes,
@@ -259,7 +259,7 @@ def pa_decode_append(out, q, k_cache, v_cache, key, value, block_tables, seq_len
     need = pa_decode_workspace_size(num_seqs, num_q_heads, max_blocks, desc, partition_size)
     if workspace is None and need > 0:
         import torch
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=k_cache.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     opts = None
     if alibi_slopes is not None or k_scale is not None or v_scale is not None:
@@ -781,7 +781,7 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float
             need = _FP4_WORKSPACE[sizes] = pa_decode_fp4_workspace_size(shape[0], shape[1], table[1], desc, window, num_sinks)
         if need:
             import torch
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=k_cache.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous, on cuda:{dev}")
     if workspace is not None:
