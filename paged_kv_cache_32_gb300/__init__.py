@@ -187,6 +187,20 @@ def _stream(stream) -> int | None:
     return int(getattr(stream, "cuda_stream", stream))
 
 
+def _workspace(need: int, device, stream):
+    """``need`` bytes on ``device`` for a call on ``stream`` (None: torch's current one), taken from that stream's memory:
+    they go back when the call returns, and only what runs there afterwards gets them again."""
+    import torch
+    if stream is not None:
+        handle = int(getattr(stream, "cuda_stream", stream))
+        if handle != torch._C._cuda_getCurrentRawStream(device.index):
+            own = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else \
+                torch.cuda.default_stream(device)  # (0, 1: handles of the default stream)
+            with torch.cuda.stream(own):
+                return torch.empty(need, dtype=torch.uint8, device=device)
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
 def _check(status: int, where: str) -> None:
     if status != PA_OK:
         raise PaError(status, where)
@@ -215,7 +229,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, pa
     out, q: [num_seqs, num_q_heads, head_size] (cache dtype); block_tables: int32
     [num_seqs, max_blocks_per_seq]; seq_lens: int32 [num_seqs].  ``workspace`` is a
     uint8 device tensor of at least pa_decode_workspace_size(...) bytes; when None
-    and one is needed, it is allocated with torch.  ``alibi_slopes``: optional
+    and one is needed, it is allocated with torch, on the call's stream.  ``alibi_slopes``: optional
     float32 device tensor [num_q_heads] (calls pa_decode_ex).  ``k_scale`` /
     ``v_scale``: dequantisation scales of an FP8 cache (q and out are fp16 then).
     ``test_flags``: 0, or PA_DECODE_TEST_EXPIRE_FIRST_WAIT in tests of the bounded waits.
@@ -228,8 +242,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float, pa
     max_blocks = int(block_tables.shape[1]) if block_tables.dim() == 2 else 0
     need = pa_decode_workspace_size(num_seqs, num_q_heads, max_blocks, desc, partition_size)
     if workspace is None and need > 0:
-        import torch
-        workspace = torch.empty(need, dtype=torch.uint8, device=k_cache.device)
+        workspace = _workspace(need, k_cache.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(seq_lens), num_seqs,
             num_q_heads, max_blocks, ctypes.byref(desc), float(scale), int(partition_size), _ptr(workspace), ws_bytes,
@@ -258,8 +271,7 @@ def pa_decode_append(out, q, k_cache, v_cache, key, value, block_tables, seq_len
     max_blocks = int(block_tables.shape[1]) if block_tables.dim() == 2 else 0
     need = pa_decode_workspace_size(num_seqs, num_q_heads, max_blocks, desc, partition_size)
     if workspace is None and need > 0:
-        import torch
-        workspace = torch.empty(need, dtype=torch.uint8, device=k_cache.device)
+        workspace = _workspace(need, k_cache.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     opts = None
     if alibi_slopes is not None or k_scale is not None or v_scale is not None:
@@ -748,7 +760,8 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float
     ``window`` (None: all) and the first ``num_sinks`` positions.  out, q [num_seqs, num_q_heads, 128] fp16 or bf16;
     ``key`` / ``value`` [num_seqs, num_kv_heads, 128]: each sequence's new token, stored at position seq_lens[s] - 1 as
     pa_reshape_and_cache_fp4 does and attended in the same call.  ``workspace``: a uint8 device tensor of
-    pa_decode_fp4_workspace_size(...) bytes, allocated with torch when None; calls that may overlap need one each."""
+    pa_decode_fp4_workspace_size(...) bytes, allocated with torch on the call's stream when None; calls that may overlap
+    need one each."""
     where = "pa_decode_fp4"
     dev, code, desc, err, shape, table = _attention_fp4(where, True, out, q, k_cache, v_cache, block_tables, seq_lens,
                                                         err_flag, desc)
@@ -780,8 +793,7 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float
                 _FP4_WORKSPACE.clear()
             need = _FP4_WORKSPACE[sizes] = pa_decode_fp4_workspace_size(shape[0], shape[1], table[1], desc, window, num_sinks)
         if need:
-            import torch
-            workspace = torch.empty(need, dtype=torch.uint8, device=k_cache.device)
+            workspace = _workspace(need, k_cache.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous, on cuda:{dev}")
     if workspace is not None:

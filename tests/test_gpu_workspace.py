@@ -1,4 +1,4 @@
-"""Decode calls that take their own workspace: queries in pinned host memory (needs a GB300)."""
+"""Decode calls that take their own workspace: queries in pinned host memory, several streams (needs a GB300)."""
 import numpy as np
 import pytest
 
@@ -79,3 +79,60 @@ def test_decode_with_host_queries(pa, append):
     assert int(s.err.item()) == 0
     ok, err, ratio = within_bound(out_f64(out), oracle_step(w)[2], "f16")
     assert ok, f"max abs err {err}, worst err/bound {ratio}"
+
+
+def busy(torch, stream, us=3000):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(us * 2000))
+
+
+@pytest.mark.parametrize("form", ["object", "handle"])
+def test_fp4_decode_on_streams_of_its_own(pa, form):
+    """Two calls on two streams that are not torch's current one, at once, and tensors made on the current one meanwhile:
+    each call's scratch is its own."""
+    import torch
+    steps, streams = [Fp4(pa, 3), Fp4(pa, 4)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for st in streams:
+            busy(torch, st)
+        for s, st in zip(steps, streams):
+            s.run(stream=st if form == "object" else st.cuda_stream)
+            junk = [torch.full((s.need,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        for s in steps:
+            s.check()
+            s.out.zero_()
+        del junk
+
+
+def test_decode_on_a_stream_of_its_own(pa):
+    import torch
+    w = W.build_decode("stream_ws", seed=7, dtype="bf16", seq_lens=[3000, 17, 1500], num_q_heads=8, num_kv_heads=2,
+                       head_size=128, block_size=16, pool_factor=1.2, partition_size=512)
+    s, st = GpuStep(w), torch.cuda.Stream()
+    need = pa.pa_decode_workspace_size(3, 8, s.tables.shape[1], s.desc, 512)
+    torch.cuda.synchronize()
+    busy(torch, st)
+    pa.pa_decode(s.out, s.q, s.k, s.v, s.tables, s.lens, w.scale, partition_size=512, err_flag=s.err, stream=st, desc=s.desc)
+    junk = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert int(s.err.item()) == 0 and bool((junk == 0xFF).all())
+    ok, err, ratio = within_bound(out_f64(s.out), oracle_step(w)[2], "bf16")
+    assert ok, f"max abs err {err}, worst err/bound {ratio}"
+
+
+def test_fp4_decode_captured_on_a_stream_of_its_own(pa):
+    """In a capture the scratch comes from the graph's memory; replayed beside other work it is still the graph's."""
+    import torch
+    s, st = Fp4(pa, 5), torch.cuda.Stream()
+    s.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        s.run(stream=st)
+    s.out.zero_()
+    junk = [torch.full((s.need,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    graph.replay()
+    s.check()
+    assert all(bool((x == 0xFF).all()) for x in junk)

@@ -65,3 +65,12 @@ def test_device_is_the_caches(taken, name):
     """Queries may lie in pinned host memory; the kernels' scratch never does."""
     CALLS[name]()
     assert taken == [(CACHE.device, None)]
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("stream,want", [(0x5550, 0x5550), (type("S", (), {"cuda_stream": 0x6660}), 0x6660), (CURRENT, None),
+                                         (None, None), (0, 0), (1, 0), (2, 2)])
+def test_memory_is_the_streams(taken, name, stream, want):
+    """Taken from another stream's memory, it would go to that stream's next tensors while the call still uses it."""
+    CALLS[name](stream=stream)
+    assert taken == [(CACHE.device, want)]
