@@ -785,7 +785,7 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float
         slopes = alibi_slopes.data_ptr()
     ws = None
     ws_bytes = 0
-    if workspace is None:
+    if workspace is None and slopes is None:  # (with ALiBi no call uses one)
         sizes = (shape[0], shape[1], table[1], desc.num_kv_heads, desc.block_size, window, num_sinks)
         need = _FP4_WORKSPACE.get(sizes)
         if need is None:
@@ -794,7 +794,7 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale: float
             need = _FP4_WORKSPACE[sizes] = pa_decode_fp4_workspace_size(shape[0], shape[1], table[1], desc, window, num_sinks)
         if need:
             workspace = _workspace(need, k_cache.device, stream)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
+    elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError(f"{where}: workspace must be contiguous, on cuda:{dev}")
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()

@@ -74,3 +74,10 @@ def test_memory_is_the_streams(taken, name, stream, want):
     """Taken from another stream's memory, it would go to that stream's next tensors while the call still uses it."""
     CALLS[name](stream=stream)
     assert taken == [(CACHE.device, want)]
+
+
+def test_alibi_takes_none(taken, monkeypatch):
+    """ALiBi decode over a 4-bit cache never uses one."""
+    monkeypatch.setattr(pa, "_refuse", lambda *args: None)
+    pa.pa_decode_fp4(Q, Q, CACHE, CACHE, TABLE, LENS, 0.1, 1.0, 1.0, alibi_slopes=torch.zeros(4))
+    assert taken == []
