@@ -513,11 +513,13 @@ def pa_rope_axes_and_cache(q_out, k_cache, v_cache, q, key, value, positions, sl
     """pa_rope_and_cache with positions int32 [axes, num_tokens] along 1 to 4 axes: pair j of a head turns by
     positions[pair_axis[j]] * inv_freq[j].  ``pair_axis``: an axis number for each pair (bytes, or any sequence on the
     host; pa_rope_pair_axes makes one).  Over a 4-bit cache (see fp4_cache) the rows are fp16 or bf16, and ``k_scale`` /
-    ``v_scale`` its units."""
+    ``v_scale`` its units, which such a call needs."""
     where = "pa_rope_axes_and_cache"
     if k_cache.shape[-1] == FP4_TILE_BYTES:
         dev, desc, code = _caches_fp4(k_cache, v_cache, desc, key.dtype, where)
-        rows, k_scale, v_scale = key.dtype, float(k_scale or 1.0), float(v_scale or 1.0)
+        rows = key.dtype
+        if k_scale is None or v_scale is None:
+            raise ValueError(f"{where}: a 4-bit cache needs k_scale and v_scale, its units")
     else:
         dev, desc, rows = _caches(k_cache, v_cache, desc, where)
         code = 0
