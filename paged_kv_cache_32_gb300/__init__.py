@@ -525,7 +525,9 @@ def pa_rope_axes_and_cache(q_out, k_cache, v_cache, q, key, value, positions, sl
         code = 0
     if positions.dim() != 2 or not 1 <= positions.shape[0] <= 4:
         raise ValueError(f"{where}: positions must be [axes, num_tokens], 1 to 4 axes")
-    axes, pairs = positions.shape[0], bytes(pair_axis)
+    axes = positions.shape[0]
+    # (bytes() of a number would be that many zeros, and of an array its memory)
+    pairs = bytes(pair_axis if isinstance(pair_axis, (bytes, bytearray, list, tuple)) else [int(a) for a in pair_axis])
     if len(pairs) != inv_freq.numel():
         raise ValueError(f"{where}: pair_axis must hold {inv_freq.numel()} axis numbers")
     tokens, hq, qp, op, qs, os_, ks, vs, err = _rope(where, dev, desc, rows, q_out, q, key, value, positions, slot_mapping,

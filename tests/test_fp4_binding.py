@@ -38,3 +38,17 @@ def test_rope_over_a_4_bit_cache_needs_its_units(rope, kw):
 def test_rope_passes_units_as_they_are(rope, k_unit, v_unit):
     """No number becomes another one: the C call refuses those that are no unit."""
     assert rope(k_scale=k_unit, v_scale=v_unit)[-4:-2] == (k_unit, v_unit)
+
+
+@pytest.mark.parametrize("given", [bytes([0, 1, 1, 0]), bytearray([0, 1, 1, 0]), [0, 1, 1, 0], (0, 1, 1, 0),
+                                   torch.tensor([0, 1, 1, 0]), torch.tensor([0, 1, 1, 0], dtype=torch.int32).numpy(),
+                                   torch.tensor([0, 1, 1, 0], dtype=torch.uint8).numpy()])
+def test_pair_axis_in_any_form(rope, given):
+    assert rope(given, k_scale=0.1, v_scale=0.1)[12] == bytes([0, 1, 1, 0])
+
+
+@pytest.mark.parametrize("given", [4, [0, 1, 1], torch.zeros(1, dtype=torch.int32).numpy(), [0, 256, 0, 0], [0, -1, 0, 0], None])
+def test_pair_axis_that_is_none(rope, given):
+    """A number is no sequence, and four bytes of one element are not four axes."""
+    with pytest.raises((TypeError, ValueError)):
+        rope(given, k_scale=0.1, v_scale=0.1)
