@@ -551,7 +551,8 @@ int pa_rope_axes_and_cache(void* q_out, void* k_cache, void* v_cache, const void
  *   (from the top of the stack; requests in order, a request's blocks in order), and writes, of the Q_s + j-th row, for
  *   its j-th new token (Q_s: the new tokens of the requests before):
  *     slot_mapping int64 [num_rows], its slot; positions int32 [num_rows], its position;
- *     query_start  int32 [num_seqs + 1], Q_s, and their sum at the end.
+ *     query_start  int32 [num_seqs + 1], Q_s, and their sum at the end (without requests: one 0; with neither requests
+ *     nor rows it may be NULL, or num_free, and the call does nothing).
  *   Rows past the sum get slot -1 (padding) and position 0.
  *   pa_tables_trim keeps the first keep_lens[s] <= seq_lens[s] tokens of request s: the blocks past them go back, their
  *   table entries become -1.  The first request's first such block comes out on top of the stack.  0 ends a request.

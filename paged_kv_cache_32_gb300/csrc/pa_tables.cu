@@ -347,10 +347,12 @@ int pa_tables_extend(int32_t* block_tables, int32_t* seq_lens, int32_t* held_blo
                               query_start,  num_seqs,     num_rows,    max_blocks_per_seq,
                               block_size,   num_blocks,   err_flag};
   const int rc = pa::check_tables(p);
-  if (rc != PA_OK || (num_seqs == 0 && num_rows == 0)) return rc;
+  // (no requests and no rows: only query_start[0] is to be written, if there is a state at all)
+  if (rc != PA_OK || (num_seqs == 0 && num_rows == 0 && (query_start == nullptr || num_free == nullptr))) return rc;
   if (query_start == nullptr || (num_rows > 0 && (slot_mapping == nullptr || positions == nullptr)))
     return PA_ERR_NULL_POINTER;
-  if (!aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(query_start, 4)) return PA_ERR_MISALIGNED;
+  if (!aligned(num_free, 4) || !aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(query_start, 4))
+    return PA_ERR_MISALIGNED;
   return pa::launch<false>(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
