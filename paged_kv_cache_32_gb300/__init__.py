@@ -163,9 +163,11 @@ def _dtype_code(t) -> int:
 def cache_desc(k_cache) -> pa_cache_desc:
     """Descriptor of a [num_blocks, num_kv_heads, block_size, head_size] key-cache tensor
     (uint8 or float8_e4m3fn storage means an FP8 E4M3 cache, whose values are
-    [num_blocks, num_kv_heads, block_size / 16, head_size, 16])."""
+    [num_blocks, num_kv_heads, block_size / 16, head_size, 16]), or of a 4-bit one (see fp4_cache)."""
     if k_cache.dim() != 4:
         raise ValueError("cache must be [num_blocks, num_kv_heads, block_size, head_size]")
+    if k_cache.shape[3] == FP4_TILE_BYTES and k_cache.element_size() == 1:  # (no FP8 cache has such rows)
+        return fp4_cache_desc(k_cache)
     nb, hkv, bs, d = (int(x) for x in k_cache.shape)
     return pa_cache_desc(nb, bs, hkv, d, _dtype_code(k_cache))
 

@@ -52,3 +52,29 @@ def test_pair_axis_that_is_none(rope, given):
     """A number is no sequence, and four bytes of one element are not four axes."""
     with pytest.raises((TypeError, ValueError)):
         rope(given, k_scale=0.1, v_scale=0.1)
+
+
+def test_descriptor_of_a_4_bit_cache():
+    """A cache's own descriptor is the one that pa_copy_blocks takes; those of other caches stay what they were."""
+    k = pa.fp4_cache(5, 2, 48, device="cpu")
+    d = pa.cache_desc(k)
+    assert (d.num_blocks, d.block_size, d.num_kv_heads, d.head_size, d.dtype) == (5, 48, 2, 128, pa.PA_FP4_E2M1)
+    d = pa.cache_desc(torch.zeros(5, 2, 32, 128, dtype=torch.uint8))
+    assert (d.num_blocks, d.block_size, d.num_kv_heads, d.head_size, d.dtype) == (5, 32, 2, 128, pa.PA_FP8_E4M3)
+    d = pa.cache_desc(torch.zeros(1, 1, 1, 1152))
+    assert (d.head_size, d.dtype) == (1152, pa.PA_F32)
+
+
+def test_copy_blocks_knows_a_4_bit_cache(monkeypatch):
+    got = []
+
+    class Library:
+        def pa_copy_blocks(self, *args):
+            d = ctypes.cast(args[4], ctypes.POINTER(pa.pa_cache_desc)).contents
+            got.append((d.block_size, d.dtype))  # (it lives as long as the call)
+            return 0
+
+    monkeypatch.setattr(pa, "lib", Library)
+    k = pa.fp4_cache(5, 2, 48, device="cpu")
+    pa.pa_copy_blocks(k, k, torch.zeros(1, 2, dtype=torch.int32), stream=0)
+    assert got == [(48, pa.PA_FP4_E2M1)]
