@@ -2,7 +2,7 @@
 // pa_window_rows.cuh for the rows, the visible slabs and the split).
 //
 // A code times its group's scale is exact in fp16, so both contractions run on mma.m16n8k16 in fp16 with fp32
-// accumulation; the cache's unit is folded into the softmax scale (keys) and the output (values).  Queries in bf16 go in
+// accumulation; the cache's unit is folded into the softmax scale (keys) and the normalised output (values).  Queries in bf16 go in
 // as fp16 after each row has been scaled by a power of two that brings its largest element into [1, 2): what lies
 // more than 2^-14 below that loses bits, by at most 2^-25 of the largest element.
 //
@@ -446,15 +446,16 @@ struct Fp4Warp {
     return ok;
   }
 
-  // unnormalised O[8 rows][OROW], then (max score in log2 units, sum)[8 rows]
+  // unnormalised O[8 rows][OROW] of the stored numbers, then (max score in log2 units, sum)[8 rows].  The values' unit
+  // comes after the division by the sum: a unit near the largest (2^100) times what a row has added up would be infinite.
   __device__ __forceinline__ void store(float* wo) const {
     const int g = lane >> 2, c = lane & 3;
     float* wml = wo + 8 * S::OROW;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float* at = wo + 16 * g + 2 * i;
-      *reinterpret_cast<float2*>(at + (2 * c) * S::OROW) = make_float2(o[i][0] * p.v_scale, o[i][2] * p.v_scale);
-      *reinterpret_cast<float2*>(at + (2 * c + 1) * S::OROW) = make_float2(o[i][1] * p.v_scale, o[i][3] * p.v_scale);
+      *reinterpret_cast<float2*>(at + (2 * c) * S::OROW) = make_float2(o[i][0], o[i][2]);
+      *reinterpret_cast<float2*>(at + (2 * c + 1) * S::OROW) = make_float2(o[i][1], o[i][3]);
     }
     if (g == 0) {
       wml[(2 * c) * 2] = m_a;
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(RowsFp4Shape<NW, NS>::THREADS) fp4_rows_kernel
   __syncthreads();
   rows_finish<T, S::D, NW, S::OROW, S::RING_BYTES / 4>(p, it, reinterpret_cast<const float*>(smem),
                                                        reinterpret_cast<float*>(smem + S::WT_OFF),
-                                                       reinterpret_cast<float*>(smem + S::MINE_OFF));
+                                                       reinterpret_cast<float*>(smem + S::MINE_OFF), p.v_scale);
 }
 
 // ---------------------------------------------------------------- decode, slabs dealt out evenly
@@ -570,8 +571,8 @@ __device__ __forceinline__ void write_rows(const WindowParams& p, const RowsItem
     } else {
       const float inv = lsum[r] == 0.f ? 0.f : 1.f / lsum[r];
       uint2 y;
-      y.x = Mma<T>::pack(acc.x * inv, acc.y * inv);
-      y.y = Mma<T>::pack(acc.z * inv, acc.w * inv);
+      y.x = Mma<T>::pack(acc.x * inv * p.v_scale, acc.y * inv * p.v_scale);
+      y.y = Mma<T>::pack(acc.z * inv * p.v_scale, acc.w * inv * p.v_scale);
       *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + rows_offset(p, it, r) * D + d) = y;
     }
   }
@@ -792,8 +793,8 @@ __global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const WindowPara
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2 y;
-  y.x = Mma<T>::pack(acc.x * inv, acc.y * inv);
-  y.y = Mma<T>::pack(acc.z * inv, acc.w * inv);
+  y.x = Mma<T>::pack(acc.x * inv * p.v_scale, acc.y * inv * p.v_scale);
+  y.y = Mma<T>::pack(acc.z * inv * p.v_scale, acc.w * inv * p.v_scale);
   T* out = static_cast<T*>(p.out) + ((size_t)rec.s * p.num_q_heads + (size_t)rec.hkv * G + rec.row0 + r) * kFp4D;
   *reinterpret_cast<uint2*>(out + 4 * lane) = y;
 }

@@ -24,3 +24,46 @@ def test_copy_blocks_without_a_descriptor(pa):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     pa.pa_copy_blocks(k, v, torch.tensor([[0, 4], [5, 1]], dtype=torch.int32, device="cuda"), err_flag=err)
     assert int(err.item()) == 0 and torch.equal(k, want[0]) and torch.equal(v, want[1])
+
+
+def lagging_cache(pa, length, low, unit):
+    """One sequence's blocks of 16 in bf16: keys +-6 (the first `low` tokens the negative ones), every value the largest
+    number that a cache of this unit holds.  The scores of queries of ones rise by 7.9 binary orders behind the low tokens,
+    which the running maximum of what starts at the low ones does not follow."""
+    import torch
+    key = torch.full((length, 1, 128), 6.0, dtype=torch.bfloat16, device="cuda")
+    key[:low] = -6.0
+    value = torch.full_like(key, 2688.0 * unit)
+    k, v = (pa.fp4_cache(length // 16, 1, 16) for _ in range(2))
+    pa.pa_reshape_and_cache_fp4(k, v, key, value, torch.arange(length, device="cuda"), 1.0, unit)
+    return k, v, 7.9 / (2 * 128 * 6 * 1.4426950408889634)
+
+
+@pytest.mark.parametrize("power", [100, -100])
+@pytest.mark.parametrize("form,length", [("clusters", 4000), ("even", 40000), ("tiles", 4096)])
+def test_value_unit_at_its_ends(pa, form, length, power):
+    """Values that the rows' type holds come out as they are, however large or small the unit and whatever a row has added
+    up before the division: every value is the same number, a weighted mean of it within 2^-11 for the rounding of the
+    weights, and half a step of bf16."""
+    import torch
+    unit, seqs = 2.0 ** power, 160
+    k, v, scale = lagging_cache(pa, length, 192, unit)
+    table = torch.arange(length // 16, dtype=torch.int32, device="cuda").repeat(seqs, 1)
+    lens = torch.full((seqs,), length, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if form == "tiles":
+        q = torch.ones(300, 8, 128, dtype=torch.bfloat16, device="cuda")
+        out = torch.zeros_like(q)
+        start = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+        pa.pa_prefill_fp4(out, q, k, v, table[:1].contiguous(), lens[:1], start, 300, scale, 1.0, unit, err_flag=err)
+    else:
+        q = torch.ones(seqs, 8, 128, dtype=torch.bfloat16, device="cuda")
+        out = torch.zeros_like(q)
+        need = pa.pa_decode_fp4_workspace_size(seqs, 8, length // 16, pa.fp4_cache_desc(k))
+        assert need > 0
+        kw = dict(alibi_slopes=torch.zeros(8, device="cuda")) if form == "clusters" else {}  # (ALiBi: always in clusters)
+        pa.pa_decode_fp4(out, q, k, v, table, lens, scale, 1.0, unit, err_flag=err, **kw)
+    assert int(err.item()) == 0
+    want = 2688.0 * unit
+    far = (out.double() / want - 1).abs().max().item()
+    assert far <= 2.0 ** -11 + 2.0 ** -8, far
