@@ -504,7 +504,8 @@ int pa_read_cache_fp4(void* key, void* value, const void* k_cache, const void* v
  *                which long contexts of very different lengths keep every SM busy to the end (two launches then).  That
  *                size is a few MB, or 0 where these arguments use none (and for invalid ones).  Its contents on entry
  *                do not matter.  Calls that may overlap, and graphs that may be replayed at once, need one each.
- *   Softmax weights enter the value product as one fp16 term.  A bf16 query row goes in as fp16 over a power of two:
+ *   Softmax weights enter the value product as one fp16 term, off by at most 2^-11 of itself; weights below 2^-32 of the
+ *   row's largest may count as 0.  A bf16 query row goes in as fp16 over a power of two:
  *   what lies more than 2^-14 below its largest element loses bits, by at most 2^-25 of the largest.
  */
 int pa_decode_fp4(void* out, const void* q, void* k_cache, void* v_cache, const void* key, const void* value,

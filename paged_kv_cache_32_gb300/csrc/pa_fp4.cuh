@@ -61,6 +61,14 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float (&x)[8], float inv) {
   return y;
 }
 
+// Softmax weights over these caches enter the value product as one fp16 number each, off by at most 2^-11 of itself
+// (2^-12 on average, in either direction): less than what the output's rounding takes (fp16 2^-11, bf16 2^-8), where a
+// second term would double the product's MMAs.  Their range is what has to be looked after: against a reference maximum
+// that no score exceeds by more than 2^8, plain weights reach down to 2^-25 only, and a long context's many small ones
+// would vanish beside one large (a first token that takes nearly everything: of 2^20 tokens of 2^-25.5 each 2 %).  So they
+// are 2^(7 + s - m), at most 2^15, and what vanishes lies below 2^-32 of the largest; the factor drops out with the sum.
+constexpr float kFp4WeightShift = 7.f;
+
 // A bf16 query row whose largest magnitude is mx becomes fp16 after a multiplication by `down`, a power of two that brings
 // mx into [1, 2) (mx subnormal: below); `up` is its inverse.  1 for a row with an infinity or a NaN.
 __device__ __forceinline__ void row_power(float mx, float& up, float& down) {

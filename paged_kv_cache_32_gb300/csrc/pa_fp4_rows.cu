@@ -160,8 +160,9 @@ __device__ __forceinline__ void fp4_slab(const uint8_t* kst, const uint8_t* vst,
       o[i][3] *= al_b;
     }
   }
-  // a row that has seen no token yet subtracts 0: masked scores (-inf) weigh nothing
-  const float sub_a = !kFull && m_a == -INFINITY ? 0.f : -m_a, sub_b = !kFull && m_b == -INFINITY ? 0.f : -m_b;
+  // weights 2^(shift + s - m); of a row that has seen no token yet scores are masked (-inf) and weigh nothing
+  const float sub_a = !kFull && m_a == -INFINITY ? 0.f : kFp4WeightShift - m_a;
+  const float sub_b = !kFull && m_b == -INFINITY ? 0.f : kFp4WeightShift - m_b;
   // this thread's tokens t0, t1 and those + 8
   const int t0 = c, t1 = (c ^ 1) + 4;
   const uint8_t* vp = vst + 8 * g;

@@ -953,7 +953,8 @@ __device__ __forceinline__ void convert_queries(uint8_t* smem, uint8_t* qbuf, co
 template <int D>
 constexpr int kPartRow = D + 4;
 static_assert(kTile * kPartRow<128> * 4 <= 8 * kHalf, "the rows fit the K and V stages");
-template <typename T, int D>
+// kUnitLast: the values' unit (4-bit caches: down to 2^-100) goes onto the quotient, else onto the sum's inverse.
+template <typename T, int D, bool kUnitLast>
 __device__ __forceinline__ void split_merge(const PrefillParams& p, const float* part, int idx) {
   cluster_sync_all();
   PfWindowItem it;
@@ -975,12 +976,12 @@ __device__ __forceinline__ void split_merge(const PrefillParams& p, const float*
         l = fmaf(w, ld_cluster(row + D + 1, c), l);
         acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
       }
-      const float inv = l > 0.f ? p.v_scale / l : 0.f;
+      const float inv = l > 0.f ? (kUnitLast ? 1.f : p.v_scale) / l : 0.f, unit = kUnitLast ? p.v_scale : 1.f;
       const size_t query = (size_t)it.q0 + it.tile0 + (r >> p.pack_log2);
       const int head = it.h + (r & ((1 << p.pack_log2) - 1));
       uint2 y;
-      y.x = Mma<T>::pack(acc.x * inv, acc.y * inv);
-      y.y = Mma<T>::pack(acc.z * inv, acc.w * inv);
+      y.x = Mma<T>::pack(acc.x * inv * unit, acc.y * inv * unit);
+      y.y = Mma<T>::pack(acc.z * inv * unit, acc.w * inv * unit);
       *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (query * p.num_q_heads + head) * D + col) = y;
     }
   }
@@ -1379,6 +1380,9 @@ __global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThre
     int lim0 = 0, lim1 = 0;                                    // last key each row sees
     Item it = {};
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // reference maxima (log2 units), partial sums
+    // (weights over a 4-bit cache are larger by a power of two, see kFp4WeightShift: the reference maxima lie that much lower)
+    [[maybe_unused]] constexpr float kShift = kFp4 ? kFp4WeightShift : 0.f, kShiftFactor = 128.f;
+    static_assert(kFp4WeightShift == 7.f, "kShiftFactor is 2 to this power");
     auto row_scale = [&]() { return kConvertQ ? make_float2(sr0, sr1) : make_float2(sl2, sl2); };
     // key tile kt of the current item (this CTA's tile tg)
     auto tile = [&](int kt) {
@@ -1414,7 +1418,8 @@ __global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThre
           tmem_st16x128_x8(s_addr + 4 * j0, hi);
           if constexpr (split_p<T>()) tmem_st16x128_x8(s_addr + 64 + 4 * j0, lo);
         }
-        lazy = !__any_sync(0xffffffffu, n0 - l0 > kLazyBound || n1 - l1 > kLazyBound);
+        constexpr float kBound = kFp4 ? kLazyBound * kShiftFactor : kLazyBound;
+        lazy = !__any_sync(0xffffffffu, n0 - l0 > kBound || n1 - l1 > kBound);
         if (lazy) {
           l0 = n0;
           l1 = n1;
@@ -1442,7 +1447,8 @@ __global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThre
           u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, 1));
           u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, 2));
           u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, 2));
-          if (__any_sync(0xffffffffu, u0 * row_scale().x > m0 + kRescaleThreshold || u1 * row_scale().y > m1 + kRescaleThreshold)) {
+          if (__any_sync(0xffffffffu, u0 * row_scale().x > m0 + (kRescaleThreshold + kShift) ||
+                                           u1 * row_scale().y > m1 + (kRescaleThreshold + kShift))) {
             a0 = b0 = a1 = b1 = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -1462,7 +1468,8 @@ __global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThre
         a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
         a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
         a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
-        const float mx0 = a0 * row_scale().x, mx1 = a1 * row_scale().y;  // scale > 0
+        const float mx0 = kFp4 ? fmaf(a0, row_scale().x, -kShift) : a0 * row_scale().x;  // scale > 0
+        const float mx1 = kFp4 ? fmaf(a1, row_scale().y, -kShift) : a1 * row_scale().y;
         const bool upd0 = mx0 > m0 + kRescaleThreshold, upd1 = mx1 > m1 + kRescaleThreshold;
         const float al0 = upd0 ? fast_exp2(m0 - mx0) : 1.f, al1 = upd1 ? fast_exp2(m1 - mx1) : 1.f;
         if (__any_sync(0xffffffffu, upd0 || upd1) && kt > 0 && ok) {
@@ -1620,8 +1627,10 @@ __global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThre
         ++item_no;
         continue;
       }
-      const float unit = kCoded ? p.v_scale : 1.f;
-      const float inv0 = s0 > 0.f ? unit / s0 : 0.f, inv1 = s1 > 0.f ? unit / s1 : 0.f;
+      const float over = kFp8 ? p.v_scale : 1.f;
+      const float inv0 = s0 > 0.f ? over / s0 : 0.f, inv1 = s1 > 0.f ? over / s1 : 0.f;
+      // (4-bit caches: units down to 2^-100, which over a long row's sum would be no ordinary number)
+      const float unit = kFp4 ? p.v_scale : 1.f;
       if constexpr (kStagedOut<T>) {
         // The tile goes to the stage, in the 128-byte-swizzled layout of the output's tensor map (row r's
         // 16-byte chunk k of column half h at h * kHalf + swz128(r, k)).  Thread c of a quad writes bytes
@@ -1631,9 +1640,9 @@ __global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThre
         for (int j = 0; j < D / 8; ++j) {
           uint8_t* col = stage + (j >> 3) * kHalf + 4 * c4;
           *reinterpret_cast<uint32_t*>(col + swz128(r0, j & 7)) =
-              Mma<TRow>::pack(o[4 * j] * inv0, o[4 * j + 1] * inv0);
+              Mma<TRow>::pack(o[4 * j] * inv0 * unit, o[4 * j + 1] * inv0 * unit);
           *reinterpret_cast<uint32_t*>(col + swz128(r1, j & 7)) =
-              Mma<TRow>::pack(o[4 * j + 2] * inv1, o[4 * j + 3] * inv1);
+              Mma<TRow>::pack(o[4 * j + 2] * inv1 * unit, o[4 * j + 3] * inv1 * unit);
         }
         if (rows == kTile) {
           // a full tile: the P V issuer stores it once every softmax warp has written its rows
@@ -1711,7 +1720,7 @@ __global__ void __launch_bounds__(kCache != PfCache::kSame ? kFp8Threads : kThre
       for (int t = max(0, n_o - kSBufs); t < n_o; ++t) drain_wait(&bar_o[t % kSBufs], (t / kSBufs) & 1);
     __syncthreads();
   }
-  if constexpr (kSplit) split_merge<TRow, D>(p, reinterpret_cast<const float*>(smem + kKOff), idx0);
+  if constexpr (kSplit) split_merge<TRow, D, kFp4>(p, reinterpret_cast<const float*>(smem + kKOff), idx0);
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
