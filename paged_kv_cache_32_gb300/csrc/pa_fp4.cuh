@@ -70,7 +70,8 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float (&x)[8], float inv) {
 constexpr float kFp4WeightShift = 7.f;
 
 // A bf16 query row whose largest magnitude is mx becomes fp16 after a multiplication by `down`, a power of two that brings
-// mx into [1, 2) (mx subnormal: below); `up` is its inverse.  1 for a row with an infinity or a NaN.
+// mx into [1, 2) (mx subnormal: below); `up` is its inverse.  1 for a row with an infinity.  (Callers' fmaxf
+// passes over NaNs: they do not choose the power, and stay NaN whatever it is.)
 __device__ __forceinline__ void row_power(float mx, float& up, float& down) {
   const int e = mx < INFINITY ? max((int)(__float_as_uint(mx) >> 23), 1) : 127;
   up = __uint_as_float((uint32_t)e << 23);
