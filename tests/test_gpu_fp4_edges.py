@@ -107,3 +107,135 @@ def test_many_small_weights_beside_a_large_one(pa, rows, form):
     want = (w / (1 + w))[:, None, None]
     far = ((out.cpu().double() - want).abs() / (2.0 ** -11 * 1.25 + want * (2.0 ** -8 + 2.0 ** -6))).max().item()
     assert far <= 1, far
+
+
+FIRST_CALL = """
+import torch
+import paged_kv_cache_32_gb300 as pa
+for rows in (torch.float16, torch.bfloat16):
+    k = torch.randint(0, 112, (2600, 1, 1, 1152), device="cuda", dtype=torch.uint8)
+    table = torch.arange(2600, device="cuda", dtype=torch.int32)[None]
+    lens = torch.tensor([40000], device="cuda", dtype=torch.int32)
+    slots = torch.arange(200, device="cuda")
+    inv, _ = pa.pa_rope_frequencies(128, device="cuda")
+    def chunk(n):
+        q = torch.ones(n, 8, 128, device="cuda", dtype=rows)
+        start = torch.tensor([0, n], device="cuda", dtype=torch.int32)
+        return lambda o: pa.pa_prefill_fp4(o, q, k, k, table, lens, start, n, 0.01, 0.01, 0.01), torch.zeros_like(q)
+    def decode(**kw):
+        q = torch.ones(1, 8, 128, device="cuda", dtype=rows)
+        return lambda o: pa.pa_decode_fp4(o, q, k, k, table, lens, 0.01, 0.01, 0.01, **kw), torch.zeros_like(q)
+    def write(rotary):
+        x = torch.ones(200, 6, 128, device="cuda", dtype=rows)
+        pos = torch.arange(200, device="cuda", dtype=torch.int32)[None].contiguous()
+        c = pa.fp4_cache(20, 1, 16)
+        return lambda o: pa.pa_rope_axes_and_cache(o, c, c.clone(), x[:, :4], x[:, 4:5], x[:, 5:], pos, slots,
+                                                   inv[:rotary // 2].contiguous(), bytes(rotary // 2), k_scale=0.1,
+                                                   v_scale=0.1), x[:, :4].clone()
+    for call, out in (decode(), decode(window=9000), chunk(1), chunk(40), chunk(3000), write(128), write(34)):
+        again = torch.zeros_like(out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(out)
+        graph.replay()
+        call(again)
+        torch.cuda.synchronize()
+        assert torch.equal(out, again) and torch.count_nonzero(out) > 0
+print("same")
+"""
+
+
+def test_first_call_captured():
+    """A process whose first call of each kernel is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("rows", ["f16", "bf16"])
+def test_pool_past_32_bits(pa, rows):
+    """The last blocks of caches of 5.9 GB: every call gives what it gives over the first blocks of small ones."""
+    import torch
+    t = torch.float16 if rows == "f16" else torch.bfloat16
+    nb, hkv, B, used = 40000, 8, 256, 24
+    assert nb * hkv * B // 16 * 1152 > 2 ** 32
+    big = [torch.zeros((nb, hkv, B // 16, 1152), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    small = [pa.fp4_cache(used, hkv, B) for _ in range(2)]
+    shift = nb - used
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(used * B, 4 * hkv, 128, generator=g, device="cuda").to(t)
+    slots = torch.randperm(used * B, generator=g, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    key, value, back = x[:, :hkv], x[:, hkv:2 * hkv], torch.zeros(2, 2, used * B, hkv, 128, dtype=t, device="cuda")
+
+    def same():
+        assert int(err.item()) == 0
+        assert all(torch.equal(b[shift:], s) for b, s in zip(big, small))
+
+    for i, (c, at) in enumerate(((small, slots), (big, slots + shift * B))):
+        pa.pa_reshape_and_cache_fp4(*c, key, value, at, 0.0025, 0.0031, err_flag=err)
+        pa.pa_read_cache_fp4(*back[i], *c, at, 0.0025, 0.0031, err_flag=err)
+    same()
+    assert torch.equal(back[0], back[1]) and bool((back[0] != 0).any())
+    pos = torch.arange(3 * used * B, dtype=torch.int32, device="cuda").view(3, -1)
+    q_out = torch.zeros(2, used * B, 2 * hkv, 128, dtype=t, device="cuda")
+    for rotary in (128, 34):
+        inv, _ = pa.pa_rope_frequencies(rotary, device="cuda")
+        for i, (c, at) in enumerate(((small, slots), (big, slots + shift * B))):
+            pa.pa_rope_axes_and_cache(q_out[i], *c, x[:, 2 * hkv:], key, value, pos, at, inv,
+                                      bytes(j % 3 for j in range(rotary // 2)), err_flag=err, k_scale=0.0025, v_scale=0.0031)
+        same()
+        assert torch.equal(q_out[0], q_out[1])
+    table = torch.randperm(used, generator=g, device="cuda").to(torch.int32).view(2, 12)
+    lens = torch.tensor([12 * B, 2000], dtype=torch.int32, device="cuda")
+    wide = torch.cat([table, torch.full((2, 140), -1, dtype=torch.int32, device="cuda")], 1)
+    for n, tab in ((1, table), (1, wide), (3, table), (700, table)):
+        outs = []
+        for c, add in ((small, 0), (big, shift)):
+            q = q_out[0, :2 * n].contiguous()
+            out, at = torch.zeros_like(q), torch.where(tab >= 0, tab + add, tab)
+            if n == 1:
+                new = [x[:2, j * hkv:(j + 1) * hkv].contiguous() for j in (2, 3)]
+                pa.pa_decode_fp4(out, q, *c, at, lens, 0.09, 0.0025, 0.0031, key=new[0], value=new[1], err_flag=err)
+            else:
+                start = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+                pa.pa_prefill_fp4(out, q, *c, at, lens, start, n, 0.09, 0.0025, 0.0031, err_flag=err)
+            outs.append(out)
+        same()
+        assert torch.equal(*outs) and bool((outs[0] != 0).any())
+    pairs = torch.tensor([[0, 5], [used - 1, 7]], dtype=torch.int32, device="cuda")
+    pa.pa_copy_blocks(*small, pairs, err_flag=err)
+    pa.pa_copy_blocks(*big, pairs + shift, err_flag=err)
+    same()
+    assert not any(bool(b[:shift].any()) for b in big)
+
+
+@pytest.mark.parametrize("rows", ["f16", "bf16"])
+def test_chunk_in_buffers_of_a_capacity(pa, rows):
+    """Single tokens in buffers that could hold prompts, as a captured graph's do: rows past the last are left alone."""
+    import torch
+    t = torch.float16 if rows == "f16" else torch.bfloat16
+    seqs, length, capacity = 120, 300, 60000
+    k, v = (torch.randint(0, 112, (seqs * 19, 2, 1, 1152), device="cuda", dtype=torch.uint8) for _ in range(2))
+    table = torch.arange(seqs * 19, device="cuda", dtype=torch.int32).view(seqs, 19)
+    lens = torch.full((seqs,), length, dtype=torch.int32, device="cuda")
+    q = torch.randn(capacity, 16, 128, device="cuda").to(t)
+    for n in (seqs, 90):
+        start = torch.arange(n + 1, device="cuda", dtype=torch.int32)
+        outs = []
+        for rows_of, most in ((capacity, capacity), (n, 1)):
+            out = torch.full((rows_of, 16, 128), 123.0, dtype=t, device="cuda")
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            pa.pa_prefill_fp4(out, q[:rows_of], k, v, table[:n].contiguous(), lens[:n], start, most, 0.01, 0.01, 0.01,
+                              err_flag=err)
+            assert int(err.item()) == 0
+            outs.append(out.double())
+        # (the two may run on different kernels: each weight rounded once, by 2^-11; the output, by half a step)
+        step = 2.0 ** -11 if rows == "f16" else 2.0 ** -8
+        top = 2688 * 0.01
+        assert bool(((outs[0][:n] - outs[1]).abs() <= 2 * (2.0 ** -11 * top + step * outs[1].abs() + 2.0 ** -14 * top)).all())
+        assert bool((outs[0][n:] == 123.0).all())
