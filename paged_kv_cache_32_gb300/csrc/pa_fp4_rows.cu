@@ -14,9 +14,10 @@
 // Row r of the S tile is token pi(r), so that the transposed P finds thread c's tokens c, (c ^ 1) + 4 and those + 8:
 // rows that are neighbours in the tile lie in different halves of the banks for both products.
 //
-// Bound by instructions more than by HBM: of 16 tokens (2304 bytes, 96 cycles of an SM's share of HBM) 64 conversions and
-// 64 products with scales, which run at half rate on a pipe each, and some 290 instructions in all take an SM's four
-// schedulers at least 73 cycles, with the latencies of 16 warps about 135; the copies alone run at 0.87 of the copy peak.
+// Bound by latencies: of 16 tokens (2304 bytes) an SM's share of HBM takes 96 cycles, and some 290 instructions, 64
+// conversions and 64 products with scales at half rate among them, take its four schedulers at least 73; sixteen warps
+// take about 135, stalled on fixed latencies, the half-rate pipes and one another.  (The copies alone run at 0.87 of the
+// copy peak.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(kThreads) fp4_read_kernel(const Fp4Rows p) {
 // values) go by 32 at a time through shared memory, where a warp turns four rows, a lane a pair, before each thread
 // takes its group.  A turned row is rounded to T first, then held in 4 bits, so that the cache is what the append makes
 // of the same rows in T.  (9001 tokens, 64 / 8 heads, 34 turned elements: 83 us, where 50 would move the bytes; 64
-// tokens: 4.3 us.)
+// tokens: 4.3 us.  Bound by latencies: a CTA has one token's rows in flight, half of the warps fit, and they wait for
+// those loads, for the two barriers a token and for shared memory; HBM 0.46 of its rate, issue slots 0.48.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) fp4_rope_cut_kernel(const RopeAxesParams p) {
   __shared__ float2 cs[kFp4D / 2];

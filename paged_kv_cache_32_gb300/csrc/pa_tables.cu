@@ -303,7 +303,9 @@ cudaError_t launch(const TablesParams& p, cudaStream_t stream) {
     if (bytes > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     return e != cudaSuccess ? e : launch_cluster(kernel, dim3((unsigned)grid), dim3(threads), bytes, cluster, true, stream, p);
   };
-  // (few requests release few blocks, as a rule: one CTA; many at once take a millisecond's fraction there, too)
+  // (few requests release few blocks, as a rule: one CTA, 11 us for one request that ends with 2500 blocks.  Its threads
+  // walk what is released: 64 requests of 2500 blocks each take 0.36 ms there, 256 of them 1.6 ms, and 257, which eight
+  // CTAs of 1024 threads take, 76 us.)
   if (p.num_seqs <= kSmall && ctas == 1)
     return run(kTrim ? trim_kernel<true, kSmall> : extend_kernel<true, kSmall>, 1, kSmall, 1, smem);
   if (kTrim || ctas <= kMaxTablesCluster) {
