@@ -197,9 +197,10 @@ __global__ void __launch_bounds__(kThreads) fp4_read_kernel(const Fp4Rows p) {
 // pa_rope.cu).  A CTA walks tokens; its first threads work out the pairs' angles, then its rows (query heads, keys,
 // values) go by 32 at a time through shared memory, where a warp turns four rows, a lane a pair, before each thread
 // takes its group.  A turned row is rounded to T first, then held in 4 bits, so that the cache is what the append makes
-// of the same rows in T.  (9001 tokens, 64 / 8 heads, 34 turned elements: 83 us, where 50 would move the bytes; 64
-// tokens: 4.3 us.  Bound by latencies: a CTA has one token's rows in flight, half of the warps fit, and they wait for
-// those loads, for the two barriers a token and for shared memory; HBM 0.46 of its rate, issue slots 0.48.)
+// of the rows that the call over a 16-bit cache turns, bit for bit.  (9001 tokens, 64 / 8 heads, 34 turned elements: 83
+// us, where 50 would move the bytes; 64 tokens: 4.3 us.  Bound by latencies: a CTA has one token's rows in flight, half of
+// the warps fit, and they wait for those loads, for the two barriers a token and for shared memory; HBM 0.46 of its rate,
+// issue slots 0.48.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) fp4_rope_cut_kernel(const RopeAxesParams p) {
   __shared__ float2 cs[kFp4D / 2];
@@ -237,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_rope_cut_kernel(const RopeAxe
         const int wi = threadIdx.x / 32 * (32 / kRowThreads) + i;
         if (first + wi < p.num_q_heads + p.num_kv_heads) {
           for (int pair = lane; pair < half; pair += 32) {
-            const float2 c = cs[pair];
-            const float x0 = to_f32(rows[wi][pair]), x1 = to_f32(rows[wi][pair + half]);
-            rows[wi][pair] = from_float<T>(c.x * x0 - c.y * x1);
-            rows[wi][pair + half] = from_float<T>(c.x * x1 + c.y * x0);
+            float x0 = to_f32(rows[wi][pair]), x1 = to_f32(rows[wi][pair + half]);
+            turn_pair(cs[pair], x0, x1);
+            rows[wi][pair] = from_float<T>(x0);
+            rows[wi][pair + half] = from_float<T>(x1);
           }
         }
       }

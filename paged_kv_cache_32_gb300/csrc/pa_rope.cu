@@ -416,8 +416,7 @@ __global__ void __launch_bounds__(kRopeThreads + kMaxHalf, kRopeResident) rope_k
             if (!INTERLEAVED || unit[k] * V + i < half) {
               float& x0 = !INTERLEAVED ? u[i] : 2 * i < V ? u[(2 * i) % V] : w[(2 * i) % V];
               float& x1 = !INTERLEAVED ? w[i] : 2 * i + 1 < V ? u[(2 * i + 1) % V] : w[(2 * i + 1) % V];
-              const float y0 = c[i].x * x0 - c[i].y * x1, y1 = c[i].x * x1 + c[i].y * x0;
-              x0 = y0, x1 = y1;
+              turn_pair(c[i], x0, x1);
             }
           }
         }

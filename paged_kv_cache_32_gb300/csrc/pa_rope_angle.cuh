@@ -22,4 +22,11 @@ __device__ __forceinline__ float2 turn_of(unsigned long long fraction, long long
   return make_float2(c * magnitude, s * magnitude);
 }
 
+// A pair turned by c = (cos, sin).  Which products are rounded is written out: left to the compiler, kernels differ in
+// the last place of some elements, and rows held in 4 bits from the same rows turned over a 16-bit cache.
+__device__ __forceinline__ void turn_pair(float2 c, float& x0, float& x1) {
+  const float y0 = fmaf(c.x, x0, -__fmul_rn(c.y, x1)), y1 = fmaf(c.x, x1, __fmul_rn(c.y, x0));
+  x0 = y0, x1 = y1;
+}
+
 }  // namespace pa
