@@ -239,3 +239,43 @@ def test_chunk_in_buffers_of_a_capacity(pa, rows):
         top = 2688 * 0.01
         assert bool(((outs[0][:n] - outs[1]).abs() <= 2 * (2.0 ** -11 * top + step * outs[1].abs() + 2.0 ** -14 * top)).all())
         assert bool((outs[0][n:] == 123.0).all())
+
+
+@pytest.mark.parametrize("long", [False, True])
+@pytest.mark.parametrize("rows", ["f16", "bf16"])
+def test_step_from_pinned_memory(pa, rows, long):
+    """The step's small arrays in pinned host memory: the bytes and bits of device arrays (long: slabs dealt out evenly)."""
+    import torch
+    t = torch.float16 if rows == "f16" else torch.bfloat16
+
+    def pinned(x):
+        return torch.empty(x.shape, dtype=x.dtype).pin_memory().copy_(x.cpu())
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n, hq, hkv, B, nb = 5, 12, 2, 32, 300
+    x = torch.randn(n, hq + 2 * hkv, 128, generator=g, device="cuda").to(t)
+    table = torch.randperm(nb, generator=g, device="cuda").to(torch.int32).view(n, nb // n)
+    if long:
+        table = torch.cat([table, torch.full((n, 1000), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
+    lens = torch.tensor([1, 700, 33, 1920, 0], dtype=torch.int32, device="cuda")
+    pos = torch.stack([lens, lens // 2, lens // 3])
+    slots = torch.arange(n, device="cuda") * 7 + 3
+    inv, _ = pa.pa_rope_frequencies(128, device="cuda")
+    held = torch.randint(0, 112, (2, nb, hkv, B // 16, 1152), generator=g, device="cuda", dtype=torch.uint8)
+    got = []
+    for move in (lambda a: a, pinned):
+        k, v = held.clone()
+        q, key, value, tab, ln, po, sl, fr = (move(a.contiguous()) for a in (x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], table,
+                                                                         lens, pos, slots, inv))
+        q_out, out = move(torch.zeros_like(x[:, :hq])), move(torch.zeros_like(x[:, :hq]))
+        back = [move(torch.zeros_like(x[:, :hkv])) for _ in range(2)]
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        pa.pa_rope_axes_and_cache(q_out, k, v, q, key, value, po, sl, fr, bytes(j % 3 for j in range(64)), err_flag=err,
+                                  k_scale=0.0025, v_scale=0.0031)
+        pa.pa_reshape_and_cache_fp4(k, v, key, value, move(slots + 1), 0.0025, 0.0031, err_flag=err)
+        pa.pa_decode_fp4(out, q_out, k, v, tab, ln, 0.01, 0.01, 0.01, key=key, value=value, err_flag=err)
+        pa.pa_read_cache_fp4(*back, k, v, sl, 0.0025, 0.0031, err_flag=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        got.append([a.cpu() for a in (q_out, out, *back, k, v)])
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*got)) and bool((got[0][1][1] != 0).any())
